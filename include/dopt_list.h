@@ -1,0 +1,187 @@
+/*
+ * dopt_list.h -- the mixed-precision AdamW step over a list of separate
+ * tensors, with fp32 or 8-bit Adam moments.
+ *
+ * dopt.h steps one rank's windows of flat, bucketed buffers.  The calls here
+ * run the same step (unscale, inf/NaN check, global L2 norm and clip, AdamW,
+ * copy-back to the 16-bit params, loss scale) over tensors that sit wherever
+ * the caller has them: params kept out of the buckets, a job without
+ * sharding, or, through dopt_list_from_layout, the rank's param shards of a
+ * dopt_layout.  The moments may be held in 8 bits (below), which takes 2
+ * bytes per element in place of 8.
+ *
+ * A dopt_list fixes the tensors' sizes and types.  Grads and params are given
+ * by address at every call; the optimizer state is a few flat arrays in one
+ * index space, the list's arena, in which tensor i's element j sits at
+ * arena_offset(i) + j and every tensor starts on a multiple of
+ * DOPT_LIST_BLOCK.  Arena slots between tensors belong to none; after
+ * dopt_list_init no call writes them.
+ *
+ * 8-bit moments (DOPT_STATE_E4M3).  Each tensor is cut into blocks of
+ * DOPT_LIST_BLOCK elements from its first; a block has one fp32 scale per
+ * moment and every element one OCP e4m3 code per moment (1 sign, 4 exponent,
+ * 3 mantissa bits; largest 448, smallest 2^-9):
+ *     m = code * scale,     v = (code * scale)^2.
+ * The second moment is held by its square root, which the update forms
+ * anyway and whose range is half as many octaves.  After an update, with x =
+ * m or sqrt(v) in fp32, A = max |x| over the block's elements and cap = 2^127
+ * for m, the largest fp32 number below 2^64 for sqrt(v):
+ *     scale = min(A, cap) * fp32(1/448), or 0 with codes 0 if A < 2^-100
+ *     code  = e4m3(clamp(x * (1 / scale), -448, 448)), nearest, ties to even
+ * and a nonzero sqrt(v) takes at least the smallest code, so that a moment
+ * that has been seen never divides m by eps alone.  An element is thereby
+ * within 2^-4 of its value, or within 2^-10 * scale if that is more (up to
+ * 2^-9 * scale for a sqrt(v) raised to the smallest code).  A NaN in a block
+ * makes its scale, and so every element of the block, NaN.
+ *
+ * Conventions as in dopt.h: 0 or a negative DOPT_ERR_* code, stream-ordered,
+ * nothing allocated on the device, no synchronization unless stated.  Calls
+ * that use one workspace must not overlap in time.  dopt_list_stats,
+ * _finalize, _prepare, _apply, _step (out == NULL), _export and _import only
+ * launch kernels and may be captured into a HIP graph; a replay uses the
+ * addresses that the captured call was given.
+ */
+#ifndef DOPT_LIST_H
+#define DOPT_LIST_H
+
+#include "dopt.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- how the Adam moments are held ---- */
+enum { DOPT_STATE_F32 = 0, DOPT_STATE_E4M3 = 1 };
+
+/* Elements per block of an 8-bit moment; every tensor's arena_offset is a multiple. */
+#define DOPT_LIST_BLOCK 128
+
+/* One tensor of a list. */
+typedef struct dopt_tensor_desc {
+    int64_t numel;       /* >= 0 */
+    int32_t param_dtype; /* DOPT_F32 / DOPT_BF16 / DOPT_F16 */
+    int32_t grad_dtype;
+    int32_t hgroup;      /* optimizer param group, 0 <= hgroup < DOPT_MAX_HGROUPS */
+    int32_t reserved;    /* 0 */
+} dopt_tensor_desc;
+
+typedef struct dopt_list dopt_list;
+
+/*
+ * dopt_list_build -- fix a list of n tensors (n >= 0) and how its moments
+ * are held.  *out receives a list owned by the library; free it with
+ * dopt_list_free.  It is immutable and may be shared by threads.
+ * Errors: DOPT_ERR_INVALID (null pointers, n < 0 or n > 2^24, numel < 0, more
+ * than 2^38 elements in all, bad dtype, hgroup or state kind), DOPT_ERR_NOMEM.
+ */
+int dopt_list_build(const dopt_tensor_desc *tensors, int64_t n, int32_t state_kind, dopt_list **out);
+
+/*
+ * dopt_list_from_layout -- the list of a rank's param shards: one tensor per
+ * param with a shard, in model order, of the shard's length, types and
+ * hyper-group.  Tensor i's param and grad are the buffers' arenas at
+ * dopt_param_info.arena_offset of its param (dopt_list_tensor_info.param), and
+ * the list's export order is the layout's model space (dopt_state_export).
+ * Errors as dopt_list_build.
+ */
+int dopt_list_from_layout(const dopt_layout *layout, int32_t state_kind, dopt_list **out);
+
+void dopt_list_free(dopt_list *list);
+
+typedef struct dopt_list_info {
+    int64_t n_tensors;
+    int64_t numel;           /* elements over the tensors: length of the export arrays */
+    int64_t arena_numel;     /* elements of every state array, a multiple of DOPT_LIST_BLOCK */
+    int64_t n_blocks;        /* arena_numel / DOPT_LIST_BLOCK: elements of the scale arrays */
+    int64_t workspace_bytes; /* device workspace the calls need (DOPT_PTR_ALIGN-aligned) */
+    int64_t stats_record_offset; /* as dopt_stats_record_offset */
+    int32_t state_kind;
+    int32_t has_master;      /* 1: some param is 16-bit, so a master array is needed */
+} dopt_list_info;
+
+typedef struct dopt_list_tensor_info {
+    int64_t numel;
+    int64_t arena_offset;    /* where the tensor starts in the state arrays */
+    int64_t export_offset;   /* where it starts in the export arrays */
+    int64_t param;           /* index in the layout's params; -1 for a list of its own */
+    int32_t param_dtype, grad_dtype, hgroup, reserved;
+} dopt_list_tensor_info;
+
+int dopt_list_query(const dopt_list *list, dopt_list_info *out);
+int dopt_list_tensor(const dopt_list *list, int64_t i, dopt_list_tensor_info *out);
+
+/* Device addresses of one tensor: contiguous, aligned to their element.
+ * Both may be NULL for a tensor of no elements, and grad also for the calls
+ * that read no grads.  No two params of a list may overlap, nor a param any
+ * grad or state array. */
+typedef struct dopt_list_ptrs {
+    const void *grad; /* numel x grad dtype, read only */
+    void *param;      /* numel x param dtype, written back */
+} dopt_list_ptrs;
+
+/* The optimizer state, device arrays in arena coordinates (DOPT_PTR_ALIGN-aligned). */
+typedef struct dopt_list_state {
+    float *master;           /* arena_numel fp32; NULL if no param is 16-bit (slots of fp32 params are unused) */
+    void *exp_avg;           /* arena_numel: fp32, or e4m3 codes (1 byte each) */
+    void *exp_avg_sq;        /* arena_numel: fp32 v, or e4m3 codes of sqrt(v) */
+    float *exp_avg_scale;    /* DOPT_STATE_E4M3: n_blocks fp32; else NULL */
+    float *exp_avg_sq_scale; /* DOPT_STATE_E4M3: n_blocks fp32; else NULL */
+} dopt_list_state;
+
+/*
+ * dopt_list_init -- master = upcast of the 16-bit params, moments = 0, step
+ * count 0, loss scale scaler->initial_scale; loads the list's tables into the
+ * workspace.  tensors: host array of n_tensors entries.  Synchronizes
+ * `stream`.  Errors: DOPT_ERR_INVALID (null or misaligned pointers, bad
+ * scaler), DOPT_ERR_HIP.
+ */
+int dopt_list_init(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_list_state *state,
+                   const dopt_scaler_cfg *scaler, void *workspace, hipStream_t stream);
+
+/*
+ * dopt_list_step -- one step: dopt_list_prepare, then dopt_list_apply.  As
+ * dopt_step: an inf/NaN grad skips the step (params, state and the step count
+ * stay), max_grad_norm <= 0 disables clipping, out (host) may be NULL and
+ * otherwise synchronizes `stream`.
+ *
+ * The parts, with the cross-rank seam of dopt_step_stats: dopt_list_stats
+ * forms the grad-stats record {sum of squares, zero count} of this list's
+ * grads; dopt_list_finalize takes the step's decision from the record;
+ * dopt_list_prepare is both in one; dopt_list_apply updates.
+ */
+int dopt_list_step(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_list_state *state,
+                   const dopt_hparams *hp, int32_t n_hgroups, double max_grad_norm, void *workspace,
+                   hipStream_t stream, dopt_stats *out);
+int dopt_list_prepare(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_hparams *hp,
+                      int32_t n_hgroups, double max_grad_norm, void *workspace, hipStream_t stream);
+int dopt_list_stats(const dopt_list *list, const dopt_list_ptrs *tensors, void *workspace, hipStream_t stream);
+int dopt_list_finalize(const dopt_list *list, const dopt_hparams *hp, int32_t n_hgroups, double max_grad_norm,
+                       void *workspace, hipStream_t stream);
+int dopt_list_apply(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_list_state *state,
+                    void *workspace, hipStream_t stream);
+
+/*
+ * Checkpoint of the state as three fp32 arrays of `numel` elements, the
+ * tensors back to back in list order: master (for fp32 params the param), m
+ * and v.  A list's 8-bit moments can thus be read into fp32 ones and the
+ * reverse, and a dopt_list_from_layout list shares its format with
+ * dopt_state_export.  _import also rewrites the params from the master, as the
+ * step's copy-back would, and holds m and v in the list's kind (8 bits: as
+ * after an update; a negative v is NaN).  The arrays need 4-byte alignment
+ * only.  The workspace must have been through dopt_list_init.
+ */
+int dopt_list_export(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_list_state *state,
+                     float *master, float *exp_avg, float *exp_avg_sq, void *workspace, hipStream_t stream);
+int dopt_list_import(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_list_state *state,
+                     const float *master, const float *exp_avg, const float *exp_avg_sq, void *workspace,
+                     hipStream_t stream);
+
+/* As dopt_state_scalars_get / _set and dopt_read_stats, of a list's workspace. */
+int dopt_list_scalars_get(const dopt_list *list, const void *workspace, hipStream_t stream, dopt_state_scalars *out);
+int dopt_list_scalars_set(const dopt_list *list, void *workspace, hipStream_t stream, const dopt_state_scalars *in);
+int dopt_list_read_stats(const dopt_list *list, const void *workspace, hipStream_t stream, dopt_stats *out);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

@@ -1,9 +1,10 @@
 """Python binding of libdopt.so, the shard-local mixed-precision AdamW step
-of a ZeRO-1 distributed optimizer for AMD Instinct MI355X (gfx950).
+of a ZeRO-1 distributed optimizer for AMD Instinct MI355X (gfx950), and the
+same step over a list of separate tensors with fp32 or 8-bit moments.
 
 Argument marshalling only: every computation happens in the library (host
 range mapper in C++, the step in HIP kernels).  Function names match the C
-ABI in include/dopt.h.  Device buffers may be given as PyTorch CUDA tensors
+ABI in include/dopt.h and include/dopt_list.h.  Device buffers may be given as PyTorch CUDA tensors
 or raw integer addresses; PyTorch is used only to own device memory and
 streams.  There is no fallback: if the library is not built, import fails.
 """
@@ -11,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, List, Optional, Sequence
+from typing import Dict, List, NamedTuple, Optional, Sequence, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdopt.so")
@@ -25,6 +26,11 @@ GROUP_KINDS = {"model_float16": 0, "model_fp32": 1, "shard_float16": 2, "shard_f
 DOPT_MAX_HGROUPS = 16
 DOPT_ARENA_ALIGN = 2048
 DOPT_PTR_ALIGN = 256
+
+
+DOPT_STATE_F32, DOPT_STATE_E4M3 = 0, 1
+STATE_KINDS = {"f32": DOPT_STATE_F32, "e4m3": DOPT_STATE_E4M3}
+DOPT_LIST_BLOCK = 128
 
 
 class DoptError(RuntimeError):
@@ -107,6 +113,33 @@ class dopt_stats(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_ if name != "reserved"}
 
 
+class dopt_tensor_desc(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("hgroup", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class dopt_list_info(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int64), ("numel", ctypes.c_int64), ("arena_numel", ctypes.c_int64),
+                ("n_blocks", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
+                ("stats_record_offset", ctypes.c_int64), ("state_kind", ctypes.c_int32),
+                ("has_master", ctypes.c_int32)]
+
+
+class dopt_list_tensor_info(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("arena_offset", ctypes.c_int64), ("export_offset", ctypes.c_int64),
+                ("param", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("hgroup", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class dopt_list_ptrs(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("param", ctypes.c_void_p)]
+
+
+class dopt_list_state(ctypes.Structure):
+    _fields_ = [("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() or "
@@ -142,6 +175,23 @@ def _load():
         "dopt_stats_record_offset": ([VP], I64),
         "dopt_read_stats": ([VP, VP, VP, P(dopt_stats)], ctypes.c_int),
         "dopt_last_error": ([], ctypes.c_char_p),
+        "dopt_list_build": ([P(dopt_tensor_desc), I64, I32, P(VP)], ctypes.c_int),
+        "dopt_list_from_layout": ([VP, I32, P(VP)], ctypes.c_int),
+        "dopt_list_free": ([VP], None),
+        "dopt_list_query": ([VP, P(dopt_list_info)], ctypes.c_int),
+        "dopt_list_tensor": ([VP, I64, P(dopt_list_tensor_info)], ctypes.c_int),
+        "dopt_list_init": ([VP, P(dopt_list_ptrs), P(dopt_list_state), P(dopt_scaler_cfg), VP, VP], ctypes.c_int),
+        "dopt_list_step": ([VP, P(dopt_list_ptrs), P(dopt_list_state), P(dopt_hparams), I32, D, VP, VP,
+                            P(dopt_stats)], ctypes.c_int),
+        "dopt_list_prepare": ([VP, P(dopt_list_ptrs), P(dopt_hparams), I32, D, VP, VP], ctypes.c_int),
+        "dopt_list_stats": ([VP, P(dopt_list_ptrs), VP, VP], ctypes.c_int),
+        "dopt_list_finalize": ([VP, P(dopt_hparams), I32, D, VP, VP], ctypes.c_int),
+        "dopt_list_apply": ([VP, P(dopt_list_ptrs), P(dopt_list_state), VP, VP], ctypes.c_int),
+        "dopt_list_export": ([VP, P(dopt_list_ptrs), P(dopt_list_state), VP, VP, VP, VP, VP], ctypes.c_int),
+        "dopt_list_import": ([VP, P(dopt_list_ptrs), P(dopt_list_state), VP, VP, VP, VP, VP], ctypes.c_int),
+        "dopt_list_scalars_get": ([VP, VP, VP, P(dopt_state_scalars)], ctypes.c_int),
+        "dopt_list_scalars_set": ([VP, VP, VP, P(dopt_state_scalars)], ctypes.c_int),
+        "dopt_list_read_stats": ([VP, VP, VP, P(dopt_stats)], ctypes.c_int),
         "dopt_vmm_granularity": ([I32, P(ctypes.c_size_t)], ctypes.c_int),
         "dopt_vmm_reserve": ([ctypes.c_size_t, ctypes.c_size_t, P(ctypes.c_uint64)], ctypes.c_int),
         "dopt_vmm_free": ([ctypes.c_uint64, ctypes.c_size_t], ctypes.c_int),
@@ -169,6 +219,10 @@ EXPORTED = ("dopt_build_ranges", "dopt_layout_free", "dopt_layout_num_buffers", 
             "dopt_stats_record_offset",
             "dopt_read_stats",
             "dopt_last_error",
+            "dopt_list_build", "dopt_list_from_layout", "dopt_list_free", "dopt_list_query", "dopt_list_tensor",
+            "dopt_list_init", "dopt_list_step", "dopt_list_prepare", "dopt_list_stats", "dopt_list_finalize",
+            "dopt_list_apply", "dopt_list_export", "dopt_list_import", "dopt_list_scalars_get",
+            "dopt_list_scalars_set", "dopt_list_read_stats",
             "dopt_vmm_granularity", "dopt_vmm_reserve", "dopt_vmm_free", "dopt_vmm_create", "dopt_vmm_map",
             "dopt_vmm_set_access", "dopt_vmm_unmap", "dopt_vmm_release")
 
@@ -191,7 +245,8 @@ def _addr(x) -> Optional[int]:
 
 
 DOPT_ERR_INVALID = -1
-_TORCH_DTYPE_NAMES = {"f32": "torch.float32", "bf16": "torch.bfloat16", "f16": "torch.float16"}
+_TORCH_DTYPE_NAMES = {"f32": "torch.float32", "bf16": "torch.bfloat16", "f16": "torch.float16",
+                      "e4m3": "torch.float8_e4m3fn"}
 
 
 def _dev(x, what: str, dtype: Optional[str] = None, min_numel: int = 0, min_bytes: int = 0) -> int:
@@ -527,6 +582,264 @@ def dopt_state_scalars_set(layout: Layout, workspace, scalars: Dict, stream=None
 
 def dopt_last_error() -> str:
     return _lib.dopt_last_error().decode()
+
+
+# ---- the step over a list of tensors (include/dopt_list.h) ----
+
+class TensorSpec(NamedTuple):
+    """One tensor of a list ('f32' | 'bf16' | 'f16' types)."""
+    numel: int
+    param_dtype: str
+    grad_dtype: str
+    hgroup: int = 0
+
+
+class TensorList:
+    """Owns a dopt_list handle (freed with the object)."""
+
+    def __init__(self, handle: ctypes.c_void_p):
+        self._h = handle
+        self._free = _lib.dopt_list_free  # kept so that freeing works during interpreter shutdown
+        o = dopt_list_info()
+        _check(_lib.dopt_list_query(handle, ctypes.byref(o)))
+        self.n_tensors, self.numel, self.arena_numel, self.n_blocks = o.n_tensors, o.numel, o.arena_numel, o.n_blocks
+        self.workspace_bytes, self.stats_record_offset = o.workspace_bytes, o.stats_record_offset
+        self.state_kind = "e4m3" if o.state_kind == DOPT_STATE_E4M3 else "f32"
+        self.has_master = bool(o.has_master)
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None:
+            self._free(h)
+            self._h = None
+
+    @property
+    def handle(self):
+        return self._h
+
+    def tensor(self, i: int) -> Dict:
+        o = dopt_list_tensor_info()
+        _check(_lib.dopt_list_tensor(self._h, i, ctypes.byref(o)))
+        d = {name: getattr(o, name) for name, _ in o._fields_ if name != "reserved"}
+        d["param_dtype"], d["grad_dtype"] = DTYPE_NAMES[d["param_dtype"]], DTYPE_NAMES[d["grad_dtype"]]
+        return d
+
+    def tensors(self) -> List[Dict]:
+        """dopt_list_tensor of every tensor (cached; the list is immutable)."""
+        if getattr(self, "_tensors", None) is None:
+            self._tensors = [self.tensor(i) for i in range(self.n_tensors)]
+        return self._tensors
+
+    def state_arrays(self) -> Dict[str, Tuple[str, int]]:
+        """The state arrays a list needs: name -> (element type, elements)."""
+        e = self.state_kind == "e4m3"
+        out = {"master": ("f32", self.arena_numel)} if self.has_master else {}
+        out.update(exp_avg=("e4m3" if e else "f32", self.arena_numel),
+                   exp_avg_sq=("e4m3" if e else "f32", self.arena_numel))
+        if e:
+            out.update(exp_avg_scale=("f32", self.n_blocks), exp_avg_sq_scale=("f32", self.n_blocks))
+        return out
+
+
+def _state_kind(state: str) -> int:
+    if state not in STATE_KINDS:
+        raise DoptError(DOPT_ERR_INVALID, f"state {state!r}: one of {sorted(STATE_KINDS)}")
+    return STATE_KINDS[state]
+
+
+def dopt_list_build(specs: Sequence, state: str = "f32") -> TensorList:
+    """specs: objects with numel, param_dtype, grad_dtype ('f32'|'bf16'|'f16')
+    and optional hgroup, in the order of the list; state: 'f32' or 'e4m3'
+    (8-bit moments)."""
+    n = len(specs)
+    arr = (dopt_tensor_desc * n)()
+    for i, p in enumerate(specs):
+        arr[i].numel = p.numel
+        arr[i].param_dtype = DTYPES[p.param_dtype] if isinstance(p.param_dtype, str) else p.param_dtype
+        arr[i].grad_dtype = DTYPES[p.grad_dtype] if isinstance(p.grad_dtype, str) else p.grad_dtype
+        arr[i].hgroup = int(getattr(p, "hgroup", 0))
+    h = ctypes.c_void_p()
+    _check(_lib.dopt_list_build(arr, n, _state_kind(state), ctypes.byref(h)))
+    return TensorList(h)
+
+
+def dopt_list_from_layout(layout: Layout, state: str = "f32") -> TensorList:
+    """The list of a layout's param shards, in model order (see shard_views)."""
+    h = ctypes.c_void_p()
+    _check(_lib.dopt_list_from_layout(layout.handle, _state_kind(state), ctypes.byref(h)))
+    return TensorList(h)
+
+
+def shard_views(layout: Layout, lst: TensorList, bufs: Sequence[Dict]):
+    """(params, grads) of a dopt_list_from_layout list: views of the shards in
+    the flat buffers' param and grad arenas."""
+    params, grads = [], []
+    for t in lst.tensors():
+        if t["param"] < 0:
+            raise DoptError(DOPT_ERR_INVALID, "the list was not built from a layout")
+        info = layout.param(t["param"])
+        a, b = info["arena_offset"], bufs[info["buffer"]]
+        params.append(b["param"][a:a + t["numel"]])
+        grads.append(b["grad"][a:a + t["numel"]])
+    return params, grads
+
+
+class ListTensors:
+    """A list's params, grads and state, checked and marshalled (make it once
+    with list_tensors() and pass it to every call; make it anew when a tensor
+    is replaced).  Holds the tensors, so that their memory lives as long."""
+
+    def __init__(self, lst: TensorList, ptrs, state, has_grads: bool, device: Optional[int], held):
+        self.handle, self.ptrs, self.state, self.has_grads, self.device = lst.handle.value, ptrs, state, has_grads, device
+        self._held = held
+
+
+def _spans(names_tensors):
+    """(first byte, past the last, name) of each tensor that holds any."""
+    return [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), name) for name, x in names_tensors
+            if x is not None and not isinstance(x, int) and x.numel() > 0]
+
+
+def list_tensors(lst: TensorList, params: Sequence, grads: Optional[Sequence], state: Dict) -> ListTensors:
+    """params, grads: per tensor of the list a contiguous device tensor of its
+    type and size, at any element-aligned address, or a raw device address;
+    grads None for the calls that read none (init, export, import).  state: the
+    arrays of lst.state_arrays().  Refused: wrong types or sizes, host
+    tensors, tensors of several devices, and params that overlap each other, a
+    grad or a state array."""
+    infos = lst.tensors()
+    if len(params) != len(infos):
+        raise DoptError(DOPT_ERR_INVALID, f"{len(params)} params, the list has {len(infos)} tensors")
+    if grads is not None and len(grads) != len(infos):
+        raise DoptError(DOPT_ERR_INVALID, f"{len(grads)} grads, the list has {len(infos)} tensors")
+    ptrs = (dopt_list_ptrs * len(infos))()
+    for i, t in enumerate(infos):
+        for key, seq in (("param", params), ("grad", grads)):
+            if seq is None or (t["numel"] == 0 and seq[i] is None):
+                continue
+            x, what = seq[i], f"tensor {i} {key}"
+            addr = _dev(x, what, t[key + "_dtype"])
+            if not isinstance(x, int) and x.numel() != t["numel"]:
+                raise DoptError(DOPT_ERR_INVALID, f"{what}: {x.numel()} elements, the list has {t['numel']}")
+            setattr(ptrs[i], key, addr)
+    st = dopt_list_state()
+    need = lst.state_arrays()
+    for name in need:
+        setattr(st, name, _dev(state.get(name), f"state {name}", need[name][0], need[name][1]))
+    mine = [(f"tensor {i} param", x) for i, x in enumerate(params)] + [(f"state {n}", state[n]) for n in need]
+    others = [(f"tensor {i} grad", x) for i, x in enumerate(grads or [])]
+    end, last = 0, ""
+    for lo, hi, name in sorted(_spans(mine)):
+        if lo < end:
+            raise DoptError(DOPT_ERR_INVALID, f"{name} overlaps {last}")
+        end, last = hi, name
+    written = sorted(_spans(mine))
+    at = 0
+    for lo, hi, name in sorted(_spans(others)):  # grads may overlap one another: they are only read
+        while at < len(written) and written[at][1] <= lo:
+            at += 1
+        if at < len(written) and written[at][0] < hi:
+            raise DoptError(DOPT_ERR_INVALID, f"{name} overlaps {written[at][2]}")
+    held = list(params) + list(grads or []) + [state[n] for n in need]
+    devices = {x.device.index for x in held if x is not None and not isinstance(x, int) and x.numel() > 0}
+    if len(devices) > 1:
+        raise DoptError(DOPT_ERR_INVALID, f"tensors on several devices: {sorted(devices)}")
+    return ListTensors(lst, ptrs, st, grads is not None, devices.pop() if devices else None, held)
+
+
+def _list_args(lst: TensorList, t: ListTensors, workspace, stream, need_grads: bool = True):
+    """(tensors, workspace address, stream) of a call, after checking that they belong together."""
+    if t.handle != lst.handle.value:
+        raise DoptError(DOPT_ERR_INVALID, "tensors were marshalled for another list")
+    if need_grads and not t.has_grads:
+        raise DoptError(DOPT_ERR_INVALID, "tensors were marshalled without grads")
+    ws = _list_ws(lst, workspace)
+    if t.device is not None:
+        import torch  # owns the devices and streams the tensors came with
+        if torch.cuda.current_device() != t.device:
+            raise DoptError(DOPT_ERR_INVALID, f"tensors on device {t.device}, the current device is "
+                                              f"{torch.cuda.current_device()}")
+        for x, what in ((stream, "stream"), (workspace, "workspace")):
+            d = getattr(getattr(x, "device", None), "index", None)
+            if d is not None and d != t.device:
+                raise DoptError(DOPT_ERR_INVALID, f"{what} on device {d}, tensors on device {t.device}")
+    return t.ptrs, ws, _stream(stream)
+
+
+def _list_ws(lst: TensorList, workspace) -> int:
+    return _dev(workspace, "workspace", None, 0, lst.workspace_bytes)
+
+
+def dopt_list_init(lst: TensorList, t: ListTensors, scaler: dopt_scaler_cfg, workspace, stream=None):
+    """Masters from the params, zero moments, step 0; synchronizes the stream."""
+    p, ws, s = _list_args(lst, t, workspace, stream, False)
+    _check(_lib.dopt_list_init(lst.handle, p, ctypes.byref(t.state), ctypes.byref(scaler), ws, s))
+
+
+def dopt_list_step(lst: TensorList, t: ListTensors, hparams, max_grad_norm: float, workspace, stream=None,
+                   want_stats: bool = True):
+    p, ws, s = _list_args(lst, t, workspace, stream)
+    hp = hparams if isinstance(hparams, ctypes.Array) else _hparams(hparams)
+    st = dopt_stats() if want_stats else None
+    _check(_lib.dopt_list_step(lst.handle, p, ctypes.byref(t.state), hp, len(hp), max_grad_norm, ws, s,
+                               ctypes.byref(st) if st is not None else None))
+    return st.as_dict() if st is not None else None
+
+
+def dopt_list_prepare(lst: TensorList, t: ListTensors, hparams, max_grad_norm: float, workspace, stream=None):
+    p, ws, s = _list_args(lst, t, workspace, stream)
+    hp = hparams if isinstance(hparams, ctypes.Array) else _hparams(hparams)
+    _check(_lib.dopt_list_prepare(lst.handle, p, hp, len(hp), max_grad_norm, ws, s))
+
+
+def dopt_list_stats(lst: TensorList, t: ListTensors, workspace, stream=None):
+    p, ws, s = _list_args(lst, t, workspace, stream)
+    _check(_lib.dopt_list_stats(lst.handle, p, ws, s))
+
+
+def dopt_list_finalize(lst: TensorList, hparams, max_grad_norm: float, workspace, stream=None):
+    hp = hparams if isinstance(hparams, ctypes.Array) else _hparams(hparams)
+    _check(_lib.dopt_list_finalize(lst.handle, hp, len(hp), max_grad_norm, _list_ws(lst, workspace), _stream(stream)))
+
+
+def dopt_list_apply(lst: TensorList, t: ListTensors, workspace, stream=None):
+    p, ws, s = _list_args(lst, t, workspace, stream)
+    _check(_lib.dopt_list_apply(lst.handle, p, ctypes.byref(t.state), ws, s))
+
+
+def _list_copy(fn, word: str, lst: TensorList, t: ListTensors, master, exp_avg, exp_avg_sq, workspace, stream):
+    p, ws, s = _list_args(lst, t, workspace, stream, False)
+    x = [_dev(a, f"{word} {name}", "f32", lst.numel)
+         for a, name in ((master, "master"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"))]
+    _check(fn(lst.handle, p, ctypes.byref(t.state), *x, ws, s))
+
+
+def dopt_list_export(lst: TensorList, t: ListTensors, master, exp_avg, exp_avg_sq, workspace, stream=None):
+    """Write master, m and v of the list's tensors, back to back in list order,
+    into three fp32 device arrays of lst.numel elements."""
+    _list_copy(_lib.dopt_list_export, "export", lst, t, master, exp_avg, exp_avg_sq, workspace, stream)
+
+
+def dopt_list_import(lst: TensorList, t: ListTensors, master, exp_avg, exp_avg_sq, workspace, stream=None):
+    """Inverse of dopt_list_export; also rewrites the params from the master."""
+    _list_copy(_lib.dopt_list_import, "import", lst, t, master, exp_avg, exp_avg_sq, workspace, stream)
+
+
+def dopt_list_scalars_get(lst: TensorList, workspace, stream=None) -> Dict:
+    st = dopt_state_scalars()
+    _check(_lib.dopt_list_scalars_get(lst.handle, _list_ws(lst, workspace), _stream(stream), ctypes.byref(st)))
+    return {name: getattr(st, name) for name, _ in st._fields_}
+
+
+def dopt_list_scalars_set(lst: TensorList, workspace, scalars: Dict, stream=None):
+    st = dopt_state_scalars(**scalars)
+    _check(_lib.dopt_list_scalars_set(lst.handle, _list_ws(lst, workspace), _stream(stream), ctypes.byref(st)))
+
+
+def dopt_list_read_stats(lst: TensorList, workspace, stream=None) -> Dict:
+    st = dopt_stats()
+    _check(_lib.dopt_list_read_stats(lst.handle, _list_ws(lst, workspace), _stream(stream), ctypes.byref(st)))
+    return st.as_dict()
 
 
 # ---- device-memory placement helpers (include/dopt_vmm.h) ----

@@ -40,7 +40,7 @@ from typing import Dict, List, Optional, Tuple
 
 import torch
 
-from . import DOPT_MAX_HGROUPS, DTYPE_NAMES, Layout
+from . import DOPT_MAX_HGROUPS, DTYPE_NAMES, Layout, TensorList
 
 TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 ES = {"f32": 4, "bf16": 2, "f16": 2}
@@ -429,3 +429,18 @@ class DeviceArenas:
                 if v is not None:
                     tot += v.numel() * v.element_size()
         return tot + self.workspace.numel()
+
+
+class ListArrays:
+    """State arrays and workspace of a tensor list, plain PyTorch allocations:
+    .state (the dict list_tensors() takes) and .workspace.  One list's arrays
+    serve one optimizer; the params and grads are the caller's."""
+
+    def __init__(self, lst: TensorList, device: str = "cuda"):
+        kinds = {**TORCH_DTYPES, "e4m3": torch.float8_e4m3fn}
+        self.state = {name: torch.zeros(n, dtype=torch.uint8 if dt == "e4m3" else kinds[dt], device=device).view(kinds[dt])
+                      for name, (dt, n) in lst.state_arrays().items()}
+        self.workspace = torch.zeros(lst.workspace_bytes, dtype=torch.uint8, device=device)
+
+    def state_bytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in self.state.values()) + self.workspace.numel()
