@@ -16,18 +16,23 @@ static int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 static bool known_dtype(int32_t d) { return d == DOPT_F32 || d == DOPT_BF16 || d == DOPT_F16; }
 
-// Ranges of at most `slots` consecutive tensors of a class.
+// Ranges of at most `slots` consecutive tensors and kListLaunchTiles tiles of
+// a class (a tensor of more tiles lies in several).
 static void cut(const ListClass &C, int slots, std::vector<ListRange> &out) {
     const int32_t n = static_cast<int32_t>(C.tensors.size());
+    const int64_t n_tiles = static_cast<int64_t>(C.tiles.size());
     int64_t t = 0;
     for (int32_t f = 0; f < n; f += slots) {
         ListRange r;
         r.first = f;
         r.count = std::min(slots, n - f);
-        r.t0 = t;
-        while (t < static_cast<int64_t>(C.tiles.size()) && C.tiles[static_cast<size_t>(t)].index < uint32_t(f + r.count)) ++t;
-        r.t1 = t;
-        out.push_back(r);
+        while (t < n_tiles && C.tiles[static_cast<size_t>(t)].index < uint32_t(f + r.count)) {
+            r.t0 = t;
+            while (t < n_tiles && t - r.t0 < kListLaunchTiles && C.tiles[static_cast<size_t>(t)].index < uint32_t(f + r.count))
+                ++t;
+            r.t1 = t;
+            out.push_back(r);
+        }
     }
 }
 
@@ -70,7 +75,7 @@ static int plan(dopt_list &P) {
     for (ListClass &C : P.classes) {
         cut(C, kListSlots, C.apply);
         cut(C, kListGradSlots, C.stats);
-        for (ListRange &r : C.apply) r.grid = list_apply_grid(r.t1 - r.t0);
+        for (ListRange &r : C.apply) r.grid = static_cast<int32_t>(r.t1 - r.t0);
         for (ListRange &r : C.stats) {
             r.grid = list_stats_grid(r.t1 - r.t0);
             r.partial_base = partials;

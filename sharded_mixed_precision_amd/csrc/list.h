@@ -30,24 +30,24 @@ struct ListTile {
 constexpr int kListSlots = 240;
 constexpr int kListGradSlots = 2 * kListSlots;
 
-// Workgroups of a launch over n tiles: one per tile (pass 2, the copies) or
-// per kListStatsTiles tiles (pass 1) up to a fixed number, which then
-// grid-stride.  A function of the list only, so the reduction order is too.
+// Tiles of one launch: 2^28 threads, below the 2^32 a launch may have.
+constexpr int64_t kListLaunchTiles = int64_t(1) << 20;
+
+// Pass 2 and the copies take one workgroup per tile; pass 1 one per
+// kListStatsTiles tiles up to a fixed number, which then grid-stride (the
+// finish adds a partial of each).  A function of the list only, so the
+// reduction order is too.
 constexpr int kListStatsTiles = 4;
-constexpr int64_t kListApplyBlocks = 16384;
 constexpr int64_t kListStatsBlocks = 4096;
-inline int32_t list_apply_grid(int64_t tiles) {
-    return static_cast<int32_t>(tiles < kListApplyBlocks ? tiles : kListApplyBlocks);
-}
 inline int32_t list_stats_grid(int64_t tiles) {
     const int64_t n = (tiles + kListStatsTiles - 1) / kListStatsTiles;
     return static_cast<int32_t>(n < kListStatsBlocks ? n : kListStatsBlocks);
 }
 
-struct ListRange {  // the tiles of `count` consecutive tensors of a class, from tensor `first`
-    int32_t first, count;
-    int64_t t0, t1;
-    int32_t grid = 0;
+struct ListRange {  // tiles [t0, t1) of `count` consecutive tensors of a class, from tensor `first`
+    int32_t first = 0, count = 0;
+    int64_t t0 = 0, t1 = 0;
+    int32_t grid = 0;  // workgroups: one per tile in pass 2 and the copies, as above in pass 1
     int32_t partial_base = 0;
 };
 

@@ -9,13 +9,25 @@
 // the scale S of a block of 128 elements; the new m and sqrt(v) are encoded
 // with their block's new scale.  p uses them before they are rounded.
 //
-// A list is cut into tiles of 2048 elements, one workgroup each, 8
-// consecutive elements per lane: a block of 128 elements is then one row of
-// 16 lanes, the group that the DPP lane permutes reduce over without LDS.
+// Every pass streams its arrays once and is bound by HBM: pass 2 without its
+// arithmetic takes the same time.  A list is cut into tiles of 2048 elements,
+// one 256-thread workgroup each, and what the layout decides is how well the
+// streams run.  Measured on MI355X, pass 2 of 1.1e9 bf16 params with fp32
+// moments / of 1.0e9 with fp32 grads and e4m3 moments:
+//   grid-stride over 16384 workgroups, 8 consecutive elements per lane   5.65 / 3.85 ms
+//   one workgroup per tile                                               5.46 / 3.52 ms
+//   a lane owns 4 elements in each half of its wave's 512, so that each
+//   16-byte access of a wave covers a whole KB, all accesses nontemporal 5.02 / 3.16 ms
+//   runs of 16 consecutive tiles on one XCD (tile_of)                    4.95 / 3.04 ms
+// Nontemporal accesses lose in the first layout, whose instructions leave
+// half of every line they touch to the next one.
+//
+// A block of 128 elements is then a half-wave: the DPP lane permutes reduce
+// over 16 lanes, one swizzle joins the two halves, and LDS is not used.
 // Tensors start anywhere their element type allows, so params and grads go
-// through 16-byte accesses of element alignment (gfx950 takes unaligned
-// global accesses); the arena arrays are aligned.  The last lanes of a
-// tensor's last tile take single elements: nothing outside a tensor is read.
+// through accesses of element alignment (gfx950 takes unaligned global
+// accesses); the arena arrays are aligned.  The last lane of a tensor takes
+// single elements: nothing outside a tensor is read.
 #include "device.h"
 
 #include "list.h"
@@ -34,55 +46,54 @@ static_assert(sizeof(ListPtrs) <= 3840 && sizeof(GradPtrs) <= 3840, "addresses m
 
 // ---- element I/O at element alignment -------------------------------------------
 
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ u32x4 ldu(const uint16_t *p) { return *reinterpret_cast<const u32x4_a2 *>(p); }
-__device__ __forceinline__ u32x4 ldu(const float *p) { return *reinterpret_cast<const u32x4_a4 *>(p); }
-__device__ __forceinline__ void stu(uint16_t *p, u32x4 x) { *reinterpret_cast<u32x4_a2 *>(p) = x; }
-__device__ __forceinline__ void stu(float *p, u32x4 x) { *reinterpret_cast<u32x4_a4 *>(p) = x; }
+constexpr int kQuad = 4;               // consecutive elements of a lane
+constexpr int kGroup = 64 * kQuad;     // what a wave's access covers
+constexpr int kGroups = kVec / kQuad;  // groups of a wave, back to back
 
+// The raw bytes of 4 consecutive elements, and their type at the element's alignment.
 template <int DT>
-struct Store {
+struct Quad {
     typedef uint16_t T;
+    typedef u32x2 Raw;
+    typedef u32x2 At __attribute__((aligned(2)));
 };
 template <>
-struct Store<DOPT_F32> {
+struct Quad<DOPT_F32> {
     typedef float T;
+    typedef u32x4 Raw;
+    typedef u32x4 At __attribute__((aligned(4)));
 };
 
 template <int DT>
-__device__ __forceinline__ float up1(typename Store<DT>::T x) {
+__device__ __forceinline__ float up1(typename Quad<DT>::T x) {
     if constexpr (DT == DOPT_F32) return x;
     else if constexpr (DT == DOPT_BF16) return __uint_as_float(uint32_t(x) << 16);
     else return Elem<DOPT_F16>::up(x);
 }
 
 template <int DT>
-__device__ __forceinline__ typename Store<DT>::T down1(float x) {
+__device__ __forceinline__ typename Quad<DT>::T down1(float x) {
     if constexpr (DT == DOPT_F32) return x;
     else return static_cast<uint16_t>(Elem<DT>::bits(x));
 }
 
-// Elements i .. i+7 of a tensor, of which the first n exist (n <= 0: none);
+// Elements i .. i+3 of a tensor, of which the first n exist (n <= 0: none);
 // the others read as 0.
 template <int DT>
-__device__ __forceinline__ Raw8 load_raw_n(const void *base, int64_t i, int n) {
-    typedef typename Store<DT>::T T;
-    const T *p = static_cast<const T *>(base) + i;
-    Raw8 r{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
-    if (n >= kVec) {
-        r.lo = ldu(p);
-        if (DT == DOPT_F32) r.hi = ldu(p + 4);
+__device__ __forceinline__ typename Quad<DT>::Raw load4(const void *base, int64_t i, int n) {
+    typedef Quad<DT> Q;
+    const typename Q::T *p = static_cast<const typename Q::T *>(base) + i;
+    typename Q::Raw r{};
+    if (n >= kQuad) {
+        r = __builtin_nontemporal_load(reinterpret_cast<const typename Q::At *>(p));
     } else {
-        for (int j = 0; j < kVec; ++j) {
-            if (j >= n) break;
-            if constexpr (DT == DOPT_F32) {
-                if (j < 4) r.lo[j] = __float_as_uint(p[j]);
-                else r.hi[j - 4] = __float_as_uint(p[j]);
-            } else {
-                r.lo[j >> 1] |= uint32_t(p[j]) << (16 * (j & 1));
+#pragma unroll
+        for (int j = 0; j < kQuad - 1; ++j) {
+            if (j < n) {
+                if constexpr (DT == DOPT_F32) r[j] = __float_as_uint(p[j]);
+                else r[j >> 1] |= uint32_t(p[j]) << (16 * (j & 1));
             }
         }
     }
@@ -90,22 +101,31 @@ __device__ __forceinline__ Raw8 load_raw_n(const void *base, int64_t i, int n) {
 }
 
 template <int DT>
-__device__ __forceinline__ void store_n(void *base, int64_t i, int n, const float (&x)[kVec]) {
-    typedef typename Store<DT>::T T;
-    T *p = static_cast<T *>(base) + i;
-    if (n >= kVec) {
-        if constexpr (DT == DOPT_F32) {
-            stu(p, u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])});
-            stu(p + 4, u32x4{__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])});
-        } else {
-            u32x4 u;
+__device__ __forceinline__ void unpack4(typename Quad<DT>::Raw r, float (&x)[kQuad]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = Elem<DT>::bits(x[2 * j]) | (Elem<DT>::bits(x[2 * j + 1]) << 16);
-            stu(p, u);
+    for (int j = 0; j < kQuad; ++j) {
+        if constexpr (DT == DOPT_F32) x[j] = __uint_as_float(r[j]);
+        else x[j] = up1<DT>(static_cast<uint16_t>(r[j >> 1] >> (16 * (j & 1))));
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(void *base, int64_t i, int n, const float (&x)[kQuad]) {
+    typedef Quad<DT> Q;
+    typename Q::T *p = static_cast<typename Q::T *>(base) + i;
+    if (n >= kQuad) {
+        typename Q::Raw r;
+        if constexpr (DT == DOPT_F32) {
+#pragma unroll
+            for (int j = 0; j < kQuad; ++j) r[j] = __float_as_uint(x[j]);
+        } else {
+            r[0] = Elem<DT>::bits(x[0]) | (Elem<DT>::bits(x[1]) << 16);
+            r[1] = Elem<DT>::bits(x[2]) | (Elem<DT>::bits(x[3]) << 16);
         }
+        __builtin_nontemporal_store(r, reinterpret_cast<typename Q::At *>(p));
     } else {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
+        for (int j = 0; j < kQuad - 1; ++j)
             if (j < n) p[j] = down1<DT>(x[j]);
     }
 }
@@ -117,16 +137,13 @@ constexpr float kCapM = 0x1p127f;
 constexpr float kCapRoot = 0x1.fffffep63f;  // the largest fp32 number whose square is finite
 constexpr float kTop = 448.0f, kLeast = 0x1p-9f;  // e4m3's largest and smallest magnitudes
 
-__device__ __forceinline__ void decode8(u32x2 c, float scale, float (&x)[kVec]) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c[j]), false);
-        const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c[j]), true);
-        x[4 * j] = a[0] * scale;
-        x[4 * j + 1] = a[1] * scale;
-        x[4 * j + 2] = b[0] * scale;
-        x[4 * j + 3] = b[1] * scale;
-    }
+__device__ __forceinline__ void decode4(uint32_t c, float scale, float (&x)[kQuad]) {
+    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c), false);
+    const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c), true);
+    x[0] = a[0] * scale;
+    x[1] = a[1] * scale;
+    x[2] = b[0] * scale;
+    x[3] = b[1] * scale;
 }
 
 template <int CTRL>
@@ -135,13 +152,13 @@ __device__ __forceinline__ uint32_t row_max(uint32_t u) {
     return u > o ? u : o;
 }
 
-// The largest magnitude over a row of 16 lanes, as fp32 bits: an unsigned
-// maximum of the bits without their sign, in which NaN is above infinity and
-// both above every number, so a NaN is never dropped.
-__device__ __forceinline__ float block_max(const float (&x)[kVec]) {
+// The largest magnitude over a half-wave, as fp32 bits: an unsigned maximum of
+// the bits without their sign, in which NaN is above infinity and both above
+// every number, so a NaN is never dropped.
+__device__ __forceinline__ float block_max(const float (&x)[kQuad]) {
     uint32_t u = 0;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
+    for (int j = 0; j < kQuad; ++j) {
         const uint32_t b = __float_as_uint(x[j]) & 0x7fffffffu;
         u = u > b ? u : b;
     }
@@ -149,68 +166,144 @@ __device__ __forceinline__ float block_max(const float (&x)[kVec]) {
     u = row_max<0x4e>(u);   // quad_perm 2,3,0,1
     u = row_max<0x141>(u);  // row_half_mirror
     u = row_max<0x140>(u);  // row_mirror
-    return __uint_as_float(u);
+    const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(static_cast<int>(u), 0x401f));  // lane ^ 16
+    return __uint_as_float(u > o ? u : o);
 }
 
-// Codes and scale of a block, all 16 lanes of its row together.  ROOT: a
-// square root of v, whose nonzero values keep a nonzero code.
+// Codes and scale of a block, all 32 lanes of its half-wave together.  ROOT:
+// a square root of v, whose nonzero values keep a nonzero code.
 template <bool ROOT>
-__device__ __forceinline__ u32x2 encode8(const float (&x)[kVec], float &scale) {
+__device__ __forceinline__ uint32_t encode4(const float (&x)[kQuad], float &scale) {
     const float a = block_max(x);
     const float cap = ROOT ? kCapRoot : kCapM;
     const bool live = !(a < kLeastScaled);
     scale = live ? (a > cap ? cap : a) * (1.0f / kTop) : 0.0f;  // a NaN passes both comparisons
     const float inv = live ? 1.0f / scale : 0.0f;
-    u32x2 c;
+    float q[kQuad];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        float q[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float v = x[4 * j + k];
-            q[k] = __builtin_amdgcn_fmed3f(v * inv, -kTop, kTop);
-            if (ROOT) q[k] = v > 0.0f ? fmaxf(q[k], kLeast) : q[k];
-        }
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
-        c[j] = live ? static_cast<uint32_t>(w) : 0u;
+    for (int j = 0; j < kQuad; ++j) {
+        q[j] = __builtin_amdgcn_fmed3f(x[j] * inv, -kTop, kTop);
+        if (ROOT) q[j] = x[j] > 0.0f ? fmaxf(q[j], kLeast) : q[j];
     }
-    return c;
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+    return live ? static_cast<uint32_t>(w) : 0u;
 }
 
-// 8 codes at arena element e, of which the first n exist (the others keep
+// 4 codes at arena element e, of which the first n exist (the others keep
 // their bytes).
-__device__ __forceinline__ void store_codes(void *base, int64_t e, int n, u32x2 c) {
+__device__ __forceinline__ void store_codes(void *base, int64_t e, int n, uint32_t c) {
     uint8_t *p = static_cast<uint8_t *>(base) + e;
-    if (n >= kVec) {
-        *reinterpret_cast<u32x2 *>(p) = c;
+    if (n >= kQuad) {
+        __builtin_nontemporal_store(c, reinterpret_cast<uint32_t *>(p));
     } else {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (j < n) p[j] = static_cast<uint8_t>(c[j >> 2] >> (8 * (j & 3)));
+        for (int j = 0; j < kQuad - 1; ++j)
+            if (j < n) p[j] = static_cast<uint8_t>(c >> (8 * j));
     }
 }
 
-// A lane's place in its tile.
-struct Lane {
-    int64_t e;      // the first of its 8 elements within the tensor
+// ---- tiles and lanes --------------------------------------------------------------
+
+// The tile of workgroup b of n.  Workgroups go to the 8 XCDs in turn; runs of
+// kXcdRun consecutive tiles are dealt to one XCD, so that the lines two tiles
+// share (a tile's scales are half a line) meet in one L2, and each XCD's
+// requests run along the arrays.  On MI355X 16 was the best of 1 to 64 for
+// pass 2 with e4m3 moments (1.0e9 elements: 3.16 ms at 1, 3.34 at 4, 3.22 at 8, 3.04 at
+// 16, 3.03 at 32, 3.09 at 64) and with fp32 moments (5.02, 4.99, 4.98, 4.95, 4.98, 5.16).
+constexpr int64_t kXcds = 8, kXcdRun = 16;
+__device__ __forceinline__ int64_t tile_of(int64_t b, int64_t n) {
+    const int64_t whole = n / (kXcds * kXcdRun) * (kXcds * kXcdRun);
+    if (b >= whole) return b;
+    return b / (kXcds * kXcdRun) * (kXcds * kXcdRun) + b % kXcds * kXcdRun + b / kXcds % kXcdRun;
+}
+
+// A lane's 4 elements of one group of its tile.
+struct Place {
+    int64_t e;      // the first within the tensor
     int64_t arena;  // and in the arena
     int n;          // how many of them exist (<= 0: none)
-    bool heads;     // first lane of a block that holds an element
 };
 
-__device__ __forceinline__ Lane lane_of(const ListTile &d) {
-    const int l = static_cast<int>(threadIdx.x) * kVec;
-    const int n = static_cast<int>(d.packed & 0xffffu) - l;
-    return Lane{int64_t(d.tile) * kTile + l, int64_t(d.block) * kListBlock + l, n,
-                (threadIdx.x & (kListBlock / kVec - 1)) == 0 && n > 0};
+__device__ __forceinline__ Place place_of(const ListTile &d, int group) {
+    const int l = static_cast<int>(threadIdx.x >> 6) * (kGroup * kGroups) + group * kGroup +
+                  static_cast<int>(threadIdx.x & 63) * kQuad;
+    return Place{int64_t(d.tile) * kTile + l, int64_t(d.block) * kListBlock + l, static_cast<int>(d.packed & 0xffffu) - l};
 }
+
+struct StateArrays {
+    float *master;
+    void *m, *v;
+    float *ms, *vs;
+};
+
+// m and v of a lane's 4 elements as they are held: loaded together, decoded later.
+template <int ST>
+struct Moments;
+
+template <>
+struct Moments<DOPT_STATE_F32> {
+    u32x4 m, v;
+    __device__ __forceinline__ void load(const StateArrays &s, const Place &L) {
+        m = load4<DOPT_F32>(s.m, L.arena, L.n);
+        v = load4<DOPT_F32>(s.v, L.arena, L.n);
+    }
+    __device__ __forceinline__ void decode(float (&a)[kQuad], float (&b)[kQuad]) const {
+        unpack4<DOPT_F32>(m, a);
+        unpack4<DOPT_F32>(v, b);
+    }
+    // r = sqrt(v)
+    static __device__ __forceinline__ void store(const StateArrays &s, const Place &L, float (&a)[kQuad],
+                                                 const float (&b)[kQuad], float (&)[kQuad]) {
+        store4<DOPT_F32>(s.m, L.arena, L.n, a);
+        store4<DOPT_F32>(s.v, L.arena, L.n, b);
+    }
+};
+
+template <>
+struct Moments<DOPT_STATE_E4M3> {
+    uint32_t m, v;
+    float ms, vs;
+    __device__ __forceinline__ void load(const StateArrays &s, const Place &L) {
+        m = v = 0;
+        ms = vs = 0.0f;
+        if (L.n > 0) {  // a block's slots past the tensor's end are arena memory: whole 4-byte loads
+            m = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(s.m) + L.arena));
+            v = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(s.v) + L.arena));
+            ms = s.ms[L.arena / kListBlock];
+            vs = s.vs[L.arena / kListBlock];
+        }
+    }
+    __device__ __forceinline__ void decode(float (&a)[kQuad], float (&b)[kQuad]) const {
+        decode4(m, ms, a);
+        decode4(v, vs, b);
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j) b[j] = b[j] * b[j];
+    }
+    static __device__ __forceinline__ void store(const StateArrays &s, const Place &L, float (&a)[kQuad],
+                                                 const float (&)[kQuad], float (&r)[kQuad]) {
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j) {  // what is not of the tensor does not enter its block's maximum
+            a[j] = j < L.n ? a[j] : 0.0f;
+            r[j] = j < L.n ? r[j] : 0.0f;
+        }
+        float sm, sr;
+        const uint32_t cm = encode4<false>(a, sm), cr = encode4<true>(r, sr);
+        store_codes(s.m, L.arena, L.n, cm);
+        store_codes(s.v, L.arena, L.n, cr);
+        if ((threadIdx.x & 31) == 0 && L.n > 0) {
+            s.ms[L.arena / kListBlock] = sm;
+            s.vs[L.arena / kListBlock] = sr;
+        }
+    }
+};
 
 // ---- pass 1: sum of squares and zero count ----------------------------------------
 //
 // As the flat step's pass 1: g = fp32(raw) * inv_scale, g*g exact in double,
-// one partial per workgroup, added in index order by k_finish.  It reads
-// kListStatsTiles consecutive tiles per iteration.
+// one partial per workgroup, added in index order by k_finish.  A workgroup
+// reads kListStatsTiles consecutive tiles per iteration, all loads before the
+// first use.
 template <int GD>
 __global__ void __launch_bounds__(kBlock) k_list_stats(const ListTile *__restrict__ tiles, int64_t t_begin,
                                                       int64_t t_end, int32_t first, const DevState *__restrict__ st,
@@ -220,102 +313,71 @@ __global__ void __launch_bounds__(kBlock) k_list_stats(const ListTile *__restric
     uint32_t zeros = 0;
     for (int64_t t0 = t_begin + int64_t(blockIdx.x) * kListStatsTiles; t0 < t_end;
          t0 += int64_t(gridDim.x) * kListStatsTiles) {
-        Raw8 raw[kListStatsTiles];
-        int n[kListStatsTiles];
+        typename Quad<GD>::Raw raw[kListStatsTiles][kGroups];
+        int n[kListStatsTiles][kGroups];
 #pragma unroll
         for (int u = 0; u < kListStatsTiles; ++u) {
-            n[u] = 0;
-            if (t0 + u < t_end) {
-                const ListTile d = tiles[t0 + u];
-                const Lane L = lane_of(d);
-                n[u] = L.n;
-                raw[u] = load_raw_n<GD>(ptrs.p[d.index - first], L.e, L.n);
+            const ListTile d = tiles[t0 + u < t_end ? t0 + u : t_end - 1];
+            const void *g = ptrs.p[d.index - first];
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                const Place L = place_of(d, k);
+                n[u][k] = t0 + u < t_end ? L.n : 0;
+                raw[u][k] = load4<GD>(g, L.e, n[u][k]);
             }
         }
 #pragma unroll
-        for (int u = 0; u < kListStatsTiles; ++u) {
-            float g[kVec];
-            Elem<GD>::unpack(raw[u], g);
+        for (int u = 0; u < kListStatsTiles; ++u)
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                if (j >= n[u]) continue;
-                const float x = g[j] * inv;
-                const double xd = static_cast<double>(x);
-                acc = fma(xd, xd, acc);
-                zeros += x == 0.0f ? 1u : 0u;
+            for (int k = 0; k < kGroups; ++k) {
+                float g[kQuad];
+                unpack4<GD>(raw[u][k], g);
+#pragma unroll
+                for (int j = 0; j < kQuad; ++j) {  // a slot of no element adds +0
+                    const float x = g[j] * inv;
+                    const double xd = static_cast<double>(x);
+                    acc = fma(xd, xd, acc);
+                    zeros += (j < n[u][k] && x == 0.0f) ? 1u : 0u;
+                }
             }
-        }
     }
     block_sum_store(acc, zeros, out + blockIdx.x);
 }
 
 // ---- pass 2 -------------------------------------------------------------------------
 
-struct StateArrays {
-    float *master;
-    void *m, *v;
-    float *ms, *vs;
-};
-
 template <int PD, int GD, int ST>
 __global__ void __launch_bounds__(kBlock) k_list_apply(const ListTile *__restrict__ tiles, int64_t t_begin,
                                                       int64_t t_end, int32_t first, StateArrays s,
                                                       const StepRec *__restrict__ rec, ListPtrs ptrs) {
     if (rec->skip) return;
-    const float inv = rec->inv_scale;
+    const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
+    const dopt_list_ptrs q = ptrs.p[d.index - first];
+    const Hp h = load_hp(rec, d.packed >> 16);
+    const float inv = rec->inv_scale, clip = rec->clip;
     const int clip_on = rec->clip_on;
-    const float clip = rec->clip;
-    for (int64_t t = t_begin + blockIdx.x; t < t_end; t += gridDim.x) {
-        const ListTile d = tiles[t];
-        const Lane L = lane_of(d);
-        const dopt_list_ptrs q = ptrs.p[d.index - first];
-        const Hp h = load_hp(rec, d.packed >> 16);
-        const Raw8 graw = load_raw_n<GD>(q.grad, L.e, L.n);
-        float g[kVec], p[kVec], a[kVec], b[kVec];
-        const Raw8 praw = PD == DOPT_F32 ? load_raw_n<DOPT_F32>(q.param, L.e, L.n)
-                                         : load_raw_n<DOPT_F32>(s.master, L.arena, L.n);
-        if constexpr (ST == DOPT_STATE_E4M3) {
-            u32x2 cm{0, 0}, cv{0, 0};
-            float sm = 0.0f, sv = 0.0f;
-            if (L.n > 0) {  // a block's slots past the tensor's end are arena memory: whole 8-byte loads
-                cm = *reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(s.m) + L.arena);
-                cv = *reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(s.v) + L.arena);
-                sm = s.ms[L.arena / kListBlock];
-                sv = s.vs[L.arena / kListBlock];
-            }
-            decode8(cm, sm, a);
-            decode8(cv, sv, b);
+    Place L[kGroups];
+    typename Quad<GD>::Raw graw[kGroups];
+    u32x4 praw[kGroups];
+    Moments<ST> mom[kGroups];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) b[j] = b[j] * b[j];
-        } else {
-            Elem<DOPT_F32>::unpack(load_raw_n<DOPT_F32>(s.m, L.arena, L.n), a);
-            Elem<DOPT_F32>::unpack(load_raw_n<DOPT_F32>(s.v, L.arena, L.n), b);
-        }
-        Elem<GD>::unpack(graw, g);
-        Elem<DOPT_F32>::unpack(praw, p);
-        float r[kVec];
+    for (int k = 0; k < kGroups; ++k) {
+        L[k] = place_of(d, k);
+        graw[k] = load4<GD>(q.grad, L[k].e, L[k].n);
+        praw[k] = PD == DOPT_F32 ? load4<DOPT_F32>(q.param, L[k].e, L[k].n) : load4<DOPT_F32>(s.master, L[k].arena, L[k].n);
+        mom[k].load(s, L[k]);
+    }
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) r[j] = adamw_root(g[j], p[j], a[j], b[j], inv, clip_on, clip, h);
-        if constexpr (ST == DOPT_STATE_E4M3) {
+    for (int k = 0; k < kGroups; ++k) {
+        float g[kQuad], p[kQuad], a[kQuad], b[kQuad], r[kQuad];
+        unpack4<GD>(graw[k], g);
+        unpack4<DOPT_F32>(praw[k], p);
+        mom[k].decode(a, b);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {  // what is not of the tensor does not enter its block's maximum
-                a[j] = j < L.n ? a[j] : 0.0f;
-                r[j] = j < L.n ? r[j] : 0.0f;
-            }
-            float sm, sv;
-            const u32x2 cm = encode8<false>(a, sm), cv = encode8<true>(r, sv);
-            store_codes(s.m, L.arena, L.n, cm);
-            store_codes(s.v, L.arena, L.n, cv);
-            if (L.heads) {
-                s.ms[L.arena / kListBlock] = sm;
-                s.vs[L.arena / kListBlock] = sv;
-            }
-        } else {
-            store_n<DOPT_F32>(s.m, L.arena, L.n, a);
-            store_n<DOPT_F32>(s.v, L.arena, L.n, b);
-        }
-        if (PD != DOPT_F32) store_n<DOPT_F32>(s.master, L.arena, L.n, p);
-        store_n<PD>(q.param, L.e, L.n, p);
+        for (int j = 0; j < kQuad; ++j) r[j] = adamw_root(g[j], p[j], a[j], b[j], inv, clip_on, clip, h);
+        Moments<ST>::store(s, L[k], a, b, r);
+        if (PD != DOPT_F32) store4<DOPT_F32>(s.master, L[k].arena, L[k].n, p);
+        store4<PD>(q.param, L[k].e, L[k].n, p);
     }
 }
 
@@ -330,33 +392,26 @@ __global__ void __launch_bounds__(kBlock) k_list_export(const ListTile *__restri
                                                        int64_t t_end, int32_t first,
                                                        const int64_t *__restrict__ xoff, StateArrays s,
                                                        ExportArrays x, ListPtrs ptrs) {
-    for (int64_t t = t_begin + blockIdx.x; t < t_end; t += gridDim.x) {
-        const ListTile d = tiles[t];
-        const Lane L = lane_of(d);
-        const int64_t o = xoff[d.index] + L.e;
-        float p[kVec], a[kVec], b[kVec];
-        Elem<DOPT_F32>::unpack(PD == DOPT_F32 ? load_raw_n<DOPT_F32>(ptrs.p[d.index - first].param, L.e, L.n)
-                                              : load_raw_n<DOPT_F32>(s.master, L.arena, L.n), p);
-        if constexpr (ST == DOPT_STATE_E4M3) {
-            u32x2 cm{0, 0}, cv{0, 0};
-            float sm = 0.0f, sv = 0.0f;
-            if (L.n > 0) {
-                cm = *reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(s.m) + L.arena);
-                cv = *reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(s.v) + L.arena);
-                sm = s.ms[L.arena / kListBlock];
-                sv = s.vs[L.arena / kListBlock];
-            }
-            decode8(cm, sm, a);
-            decode8(cv, sv, b);
+    const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
+    const void *param = ptrs.p[d.index - first].param;
+    const int64_t o = xoff[d.index];
+    Place L[kGroups];
+    u32x4 praw[kGroups];
+    Moments<ST> mom[kGroups];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) b[j] = b[j] * b[j];
-        } else {
-            Elem<DOPT_F32>::unpack(load_raw_n<DOPT_F32>(s.m, L.arena, L.n), a);
-            Elem<DOPT_F32>::unpack(load_raw_n<DOPT_F32>(s.v, L.arena, L.n), b);
-        }
-        store_n<DOPT_F32>(x.p, o, L.n, p);
-        store_n<DOPT_F32>(x.m, o, L.n, a);
-        store_n<DOPT_F32>(x.v, o, L.n, b);
+    for (int k = 0; k < kGroups; ++k) {
+        L[k] = place_of(d, k);
+        praw[k] = PD == DOPT_F32 ? load4<DOPT_F32>(param, L[k].e, L[k].n) : load4<DOPT_F32>(s.master, L[k].arena, L[k].n);
+        mom[k].load(s, L[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        float p[kQuad], a[kQuad], b[kQuad];
+        unpack4<DOPT_F32>(praw[k], p);
+        mom[k].decode(a, b);
+        store4<DOPT_F32>(x.p, o + L[k].e, L[k].n, p);
+        store4<DOPT_F32>(x.m, o + L[k].e, L[k].n, a);
+        store4<DOPT_F32>(x.v, o + L[k].e, L[k].n, b);
     }
 }
 
@@ -365,61 +420,59 @@ __global__ void __launch_bounds__(kBlock) k_list_import(const ListTile *__restri
                                                        int64_t t_end, int32_t first,
                                                        const int64_t *__restrict__ xoff, StateArrays s,
                                                        ExportArrays x, ListPtrs ptrs) {
-    for (int64_t t = t_begin + blockIdx.x; t < t_end; t += gridDim.x) {
-        const ListTile d = tiles[t];
-        const Lane L = lane_of(d);
-        const int64_t o = xoff[d.index] + L.e;
-        float p[kVec], a[kVec], b[kVec];
-        Elem<DOPT_F32>::unpack(load_raw_n<DOPT_F32>(x.p, o, L.n), p);
-        Elem<DOPT_F32>::unpack(load_raw_n<DOPT_F32>(x.m, o, L.n), a);
-        Elem<DOPT_F32>::unpack(load_raw_n<DOPT_F32>(x.v, o, L.n), b);
-        if (PD != DOPT_F32) store_n<DOPT_F32>(s.master, L.arena, L.n, p);
-        store_n<PD>(ptrs.p[d.index - first].param, L.e, L.n, p);
-        if constexpr (ST == DOPT_STATE_E4M3) {
+    const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
+    void *param = ptrs.p[d.index - first].param;
+    const int64_t o = xoff[d.index];
+    Place L[kGroups];
+    u32x4 praw[kGroups], araw[kGroups], braw[kGroups];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) b[j] = sqrtf(b[j]);
-            float sm, sv;
-            const u32x2 cm = encode8<false>(a, sm), cv = encode8<true>(b, sv);
-            store_codes(s.m, L.arena, L.n, cm);
-            store_codes(s.v, L.arena, L.n, cv);
-            if (L.heads) {
-                s.ms[L.arena / kListBlock] = sm;
-                s.vs[L.arena / kListBlock] = sv;
-            }
-        } else {
-            store_n<DOPT_F32>(s.m, L.arena, L.n, a);
-            store_n<DOPT_F32>(s.v, L.arena, L.n, b);
-        }
+    for (int k = 0; k < kGroups; ++k) {
+        L[k] = place_of(d, k);
+        praw[k] = load4<DOPT_F32>(x.p, o + L[k].e, L[k].n);
+        araw[k] = load4<DOPT_F32>(x.m, o + L[k].e, L[k].n);
+        braw[k] = load4<DOPT_F32>(x.v, o + L[k].e, L[k].n);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        float p[kQuad], a[kQuad], b[kQuad], r[kQuad];
+        unpack4<DOPT_F32>(praw[k], p);
+        unpack4<DOPT_F32>(araw[k], a);
+        unpack4<DOPT_F32>(braw[k], b);
+        if (PD != DOPT_F32) store4<DOPT_F32>(s.master, L[k].arena, L[k].n, p);
+        store4<PD>(param, L[k].e, L[k].n, p);
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j) r[j] = ST == DOPT_STATE_E4M3 ? sqrtf(b[j]) : 0.0f;
+        Moments<ST>::store(s, L[k], a, b, r);
     }
 }
 
 // Masters from the params, everything else zero, whole blocks of the arena.
 template <int PD, int ST>
 __global__ void __launch_bounds__(kBlock) k_list_init(const ListTile *__restrict__ tiles, int64_t t_begin,
-                                                     int64_t t_end, int32_t first, bool masters, StateArrays s,
-                                                     ListPtrs ptrs) {
-    const float z[kVec] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int64_t t = t_begin + blockIdx.x; t < t_end; t += gridDim.x) {
-        const ListTile d = tiles[t];
-        const Lane L = lane_of(d);
-        // the lane's slots lie in a block of the tensor
-        const int whole = (static_cast<int>(d.packed & 0xffffu) + kListBlock - 1) / kListBlock * kListBlock;
-        if (static_cast<int>(threadIdx.x) * kVec >= whole) continue;
+                                                     int32_t first, bool masters, StateArrays s, ListPtrs ptrs) {
+    const float z[kQuad] = {0, 0, 0, 0};
+    const ListTile d = tiles[t_begin + blockIdx.x];
+    const int whole = (static_cast<int>(d.packed & 0xffffu) + kListBlock - 1) / kListBlock * kListBlock;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const Place L = place_of(d, k);
+        const int n = L.n + whole - static_cast<int>(d.packed & 0xffffu);  // slots of the tensor's blocks
+        if (n <= 0) continue;
         if (masters) {
-            float p[kVec] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (PD != DOPT_F32) Elem<PD>::unpack(load_raw_n<PD>(ptrs.p[d.index - first].param, L.e, L.n), p);
-            store8f(s.master, L.arena, p);
+            float p[kQuad] = {0, 0, 0, 0};
+            if (PD != DOPT_F32) unpack4<PD>(load4<PD>(ptrs.p[d.index - first].param, L.e, L.n), p);
+            store4<DOPT_F32>(s.master, L.arena, n, p);
         }
         if constexpr (ST == DOPT_STATE_E4M3) {
-            store_codes(s.m, L.arena, kVec, u32x2{0, 0});
-            store_codes(s.v, L.arena, kVec, u32x2{0, 0});
-            if (L.heads) {
+            store_codes(s.m, L.arena, n, 0);
+            store_codes(s.v, L.arena, n, 0);
+            if ((threadIdx.x & 31) == 0) {
                 s.ms[L.arena / kListBlock] = 0.0f;
                 s.vs[L.arena / kListBlock] = 0.0f;
             }
         } else {
-            store8f(static_cast<float *>(s.m), L.arena, z);
-            store8f(static_cast<float *>(s.v), L.arena, z);
+            store4<DOPT_F32>(s.m, L.arena, n, z);
+            store4<DOPT_F32>(s.v, L.arena, n, z);
         }
     }
 }
@@ -565,7 +618,7 @@ int dopt_list_init(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
             with_dtype(C.pd, [&](auto pd) {
                 with_state(P->state_kind, [&](auto st) {
                     k_list_init<decltype(pd)::value, decltype(st)::value><<<r.grid, kBlock, 0, stream>>>(
-                        tiles_of(C, ws), r.t0, r.t1, r.first, P->has_master, s, a);
+                        tiles_of(C, ws), r.t0, r.first, P->has_master, s, a);
                 });
             });
             if ((rc = check_launch("launch k_list_init"))) return rc;
