@@ -318,6 +318,11 @@ struct Elem<DOPT_F32> {
     static __device__ __forceinline__ void store1(void *base, int64_t i, float x) { static_cast<float *>(base)[i] = x; }
 };
 
+// An optimizer param group's scalars of one step.
+struct Hp {
+    float decay, b1, omb1, b2, omb2, eps, step, sbc2;
+};
+
 // ---- finalize: skip, norm, clip, loss scale, step count, AdamW scalars ------
 //
 // [DO] "三层继承体系": an overflow skips the inner step; clipping uses the
@@ -325,74 +330,91 @@ struct Elem<DOPT_F32> {
 // coefficient max_norm / (norm + 1e-6), applied when below 1; the dynamic
 // scale backs off (after `hysteresis` overflows) and grows every
 // growth_interval clean steps; AdamW scalars are computed in double and
-// rounded once to fp32.  Called by every thread of one workgroup: thread 0
-// takes the step decision, then thread h fills the scalars of hyper-group h.
-// `cur` is the caller's copy of *st, read at kernel start so that its load
-// overlaps the reduction; the new state is written to *st.
+// rounded once to fp32.  `cur` is the caller's copy of *st, read at kernel
+// start so that its load overlaps the reduction; the new state is written to
+// *st.
+
+// The decision, by one thread; returns the step count after it.
+static __device__ __forceinline__ int64_t decide_step(double sumsq, double zeros, const DevState &cur, DevState *st,
+                                                      StepRec *sr, dopt_stats *out, double max_norm) {
+    DevState n = cur;
+    const int found_inf = isfinite(sumsq) ? 0 : 1;
+    const double norm = sqrt(sumsq);
+    out->found_inf = found_inf;
+    out->skipped = found_inf;
+    out->reserved = 0;
+    out->sumsq = sumsq;
+    out->grad_norm = norm;
+    out->num_zeros = static_cast<uint64_t>(zeros);
+    out->loss_scale_used = n.scale;
+    sr->skip = found_inf;
+    sr->inv_scale = n.inv_scale;
+    if (n.kind == DOPT_SCALER_DYNAMIC) {
+        if (found_inf) {
+            n.growth_tracker = 0;
+            n.hysteresis_tracker -= 1;
+            if (n.hysteresis_tracker <= 0) n.scale = fmax(n.scale * n.backoff_factor, n.min_scale);
+        } else {
+            n.growth_tracker += 1;
+            if (n.growth_tracker == n.growth_interval) {
+                n.growth_tracker = 0;
+                n.hysteresis_tracker = n.hysteresis;
+                n.scale = n.scale * n.growth_factor;
+            }
+        }
+        n.inv_scale = static_cast<float>(1.0 / n.scale);
+    }
+    out->loss_scale_next = n.scale;
+    double clip = 1.0;
+    int clip_on = 0;
+    if (!found_inf) {
+        n.t += 1;
+        if (max_norm > 0.0) {
+            clip = max_norm / (norm + 1e-6);
+            clip_on = clip < 1.0 ? 1 : 0;
+        }
+    }
+    out->clip_coef = clip;
+    out->clip_applied = clip_on;
+    sr->clip_on = clip_on;
+    sr->clip = clip_on ? static_cast<float>(clip) : 0.0f;
+    out->step_count = n.t;
+    *st = n;
+    return n.t;
+}
+
+// One hyper-group's scalars for step t.
+static __device__ __forceinline__ Hp step_scalars(const dopt_hparams &hp, double t) {
+    return Hp{static_cast<float>(1.0 - hp.lr * hp.weight_decay), static_cast<float>(hp.beta1),
+              static_cast<float>(1.0 - hp.beta1), static_cast<float>(hp.beta2), static_cast<float>(1.0 - hp.beta2),
+              static_cast<float>(hp.eps), static_cast<float>(hp.lr / (1.0 - pow(hp.beta1, t))),
+              static_cast<float>(sqrt(1.0 - pow(hp.beta2, t)))};
+}
+
+static __device__ __forceinline__ void store_scalars(StepRec *sr, int h, const Hp &x) {
+    sr->decay[h] = x.decay;
+    sr->beta1[h] = x.b1;
+    sr->omb1[h] = x.omb1;
+    sr->beta2[h] = x.b2;
+    sr->omb2[h] = x.omb2;
+    sr->eps[h] = x.eps;
+    sr->step_size[h] = x.step;
+    sr->sqrt_bc2[h] = x.sbc2;
+}
+
+// Called by every thread of one workgroup: thread 0 takes the step decision,
+// then thread h fills the scalars of hyper-group h.
 static __device__ void finalize_block(double sumsq, double zeros, const DevState &cur, DevState *st, StepRec *sr,
-                               dopt_stats *out, const FinalizeArgs &a) {
+                                      dopt_stats *out, const FinalizeArgs &a) {
     __shared__ double s_t;
     __shared__ int s_skip;
     if (threadIdx.x == 0) {
-        DevState n = cur;
-        const int found_inf = isfinite(sumsq) ? 0 : 1;
-        const double norm = sqrt(sumsq);
-        out->found_inf = found_inf;
-        out->skipped = found_inf;
-        out->reserved = 0;
-        out->sumsq = sumsq;
-        out->grad_norm = norm;
-        out->num_zeros = static_cast<uint64_t>(zeros);
-        out->loss_scale_used = n.scale;
-        sr->skip = found_inf;
-        sr->inv_scale = n.inv_scale;
-        if (n.kind == DOPT_SCALER_DYNAMIC) {
-            if (found_inf) {
-                n.growth_tracker = 0;
-                n.hysteresis_tracker -= 1;
-                if (n.hysteresis_tracker <= 0) n.scale = fmax(n.scale * n.backoff_factor, n.min_scale);
-            } else {
-                n.growth_tracker += 1;
-                if (n.growth_tracker == n.growth_interval) {
-                    n.growth_tracker = 0;
-                    n.hysteresis_tracker = n.hysteresis;
-                    n.scale = n.scale * n.growth_factor;
-                }
-            }
-            n.inv_scale = static_cast<float>(1.0 / n.scale);
-        }
-        out->loss_scale_next = n.scale;
-        double clip = 1.0;
-        int clip_on = 0;
-        if (!found_inf) {
-            n.t += 1;
-            if (a.max_norm > 0.0) {
-                clip = a.max_norm / (norm + 1e-6);
-                clip_on = clip < 1.0 ? 1 : 0;
-            }
-        }
-        out->clip_coef = clip;
-        out->clip_applied = clip_on;
-        sr->clip_on = clip_on;
-        sr->clip = clip_on ? static_cast<float>(clip) : 0.0f;
-        out->step_count = n.t;
-        *st = n;
-        s_t = static_cast<double>(n.t);
-        s_skip = found_inf;
+        s_t = static_cast<double>(decide_step(sumsq, zeros, cur, st, sr, out, a.max_norm));
+        s_skip = isfinite(sumsq) ? 0 : 1;
     }
     __syncthreads();
     const int h = threadIdx.x;
-    if (!s_skip && h < a.nh) {
-        const dopt_hparams &hp = a.hp[h];
-        sr->decay[h] = static_cast<float>(1.0 - hp.lr * hp.weight_decay);
-        sr->beta1[h] = static_cast<float>(hp.beta1);
-        sr->omb1[h] = static_cast<float>(1.0 - hp.beta1);
-        sr->beta2[h] = static_cast<float>(hp.beta2);
-        sr->omb2[h] = static_cast<float>(1.0 - hp.beta2);
-        sr->eps[h] = static_cast<float>(hp.eps);
-        sr->step_size[h] = static_cast<float>(hp.lr / (1.0 - pow(hp.beta1, s_t)));
-        sr->sqrt_bc2[h] = static_cast<float>(sqrt(1.0 - pow(hp.beta2, s_t)));
-    }
+    if (!s_skip && h < a.nh) store_scalars(sr, h, step_scalars(a.hp[h], s_t));
 }
 
 static __global__ void __launch_bounds__(64) k_finalize(const Record *rec, DevState *st, StepRec *sr, dopt_stats *out,
@@ -496,10 +518,6 @@ static __global__ void __launch_bounds__(THREADS) k_finish(const Partial *__rest
 }
 
 // ---- the update formula (fp32, in the order stated at pass 2) -------------------
-
-struct Hp {
-    float decay, b1, omb1, b2, omb2, eps, step, sbc2;
-};
 
 __device__ __forceinline__ Hp load_hp(const StepRec *__restrict__ r, int h) {
     return Hp{r->decay[h], r->beta1[h], r->omb1[h], r->beta2[h], r->omb2[h], r->eps[h], r->step_size[h], r->sqrt_bc2[h]};

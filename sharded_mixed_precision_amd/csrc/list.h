@@ -24,25 +24,36 @@ struct ListTile {
 };
 
 // Tensor addresses reach a kernel by value, in its arguments (4 KB hold
-// kListSlots param and grad pairs, or kListGradSlots grads); a list of more
-// tensors of one class takes a launch for each so many.  Nothing is copied
+// kListSlots param and grad pairs, or kListGradSlots grads beside pass 1's own);
+// a list of more tensors of one class takes a launch for each so many.  Nothing is copied
 // from the host and the addresses may change from call to call.
 constexpr int kListSlots = 240;
-constexpr int kListGradSlots = 2 * kListSlots;
+constexpr int kListGradSlots = 400;
 
 // Tiles of one launch: 2^28 threads, below the 2^32 a launch may have.
 constexpr int64_t kListLaunchTiles = int64_t(1) << 20;
 
-// Pass 2 and the copies take one workgroup per tile; pass 1 one per
-// kListStatsTiles tiles up to a fixed number, which then grid-stride (the
-// finish adds a partial of each).  A function of the list only, so the
-// reduction order is too.
+// Pass 2 and the copies take one workgroup per tile.  A workgroup of pass 1
+// reads kListStatsTiles tiles at a time and grid-strides, about 8 times on
+// the largest lists: on MI355X 1.1e9 bf16 grads took 329 us with 16384
+// workgroups and 342 with 4096, 1.2e8 took 51 and 47.5 (the finish adds a
+// partial of each).  A function of the list only, so the reduction order is
+// too.
 constexpr int kListStatsTiles = 4;
-constexpr int64_t kListStatsBlocks = 4096;
 inline int32_t list_stats_grid(int64_t tiles) {
     const int64_t n = (tiles + kListStatsTiles - 1) / kListStatsTiles;
-    return static_cast<int32_t>(n < kListStatsBlocks ? n : kListStatsBlocks);
+    const int64_t most = n / 8 < 4096 ? 4096 : n / 8 > 16384 ? 16384 : n / 8;
+    return static_cast<int32_t>(n < most ? n : most);
 }
+
+// Up to this many partials, pass 1's last workgroup adds them: a launch less.
+// Each workgroup pays for it with a release and a count that all XCDs share,
+// so a larger list keeps a finish of its own.  dopt_list_prepare on MI355X,
+// with and without: 6.7 / 8.6 us at 8 partials, 7.7 / 8.2 at 64, 8.5 / 8.2 at
+// 100, 10.8 / 8.2 at 200.
+constexpr int32_t kListFused = 64;
+// Where the workspace counts pass 1's finished workgroups.
+constexpr int64_t kWsListDone = kWsRecord + 64;
 
 struct ListRange {  // tiles [t0, t1) of `count` consecutive tensors of a class, from tensor `first`
     int32_t first = 0, count = 0;

@@ -42,7 +42,6 @@ struct ListPtrs {
 struct GradPtrs {
     const void *p[kListGradSlots];
 };
-static_assert(sizeof(ListPtrs) <= 3840 && sizeof(GradPtrs) <= 3840, "addresses must fit the kernel argument space");
 
 // ---- element I/O at element alignment -------------------------------------------
 
@@ -225,9 +224,9 @@ struct Place {
     int n;          // how many of them exist (<= 0: none)
 };
 
-__device__ __forceinline__ Place place_of(const ListTile &d, int group) {
-    const int l = static_cast<int>(threadIdx.x >> 6) * (kGroup * kGroups) + group * kGroup +
-                  static_cast<int>(threadIdx.x & 63) * kQuad;
+// `thread`: among the kBlock that share the tile.
+__device__ __forceinline__ Place place_of(const ListTile &d, int group, int thread) {
+    const int l = (thread >> 6) * (kGroup * kGroups) + group * kGroup + (thread & 63) * kQuad;
     return Place{int64_t(d.tile) * kTile + l, int64_t(d.block) * kListBlock + l, static_cast<int>(d.packed & 0xffffu) - l};
 }
 
@@ -301,28 +300,129 @@ struct Moments<DOPT_STATE_E4M3> {
 // ---- pass 1: sum of squares and zero count ----------------------------------------
 //
 // As the flat step's pass 1: g = fp32(raw) * inv_scale, g*g exact in double,
-// one partial per workgroup, added in index order by k_finish.  A workgroup
-// reads kListStatsTiles consecutive tiles per iteration, all loads before the
-// first use.
-template <int GD>
-__global__ void __launch_bounds__(kBlock) k_list_stats(const ListTile *__restrict__ tiles, int64_t t_begin,
-                                                      int64_t t_end, int32_t first, const DevState *__restrict__ st,
-                                                      Partial *__restrict__ out, GradPtrs ptrs) {
-    const float inv = st->inv_scale;
+// one partial per workgroup, added in index order.  A workgroup reads
+// kListStatsTiles consecutive tiles per iteration, all loads before the first
+// use.  The partials of a small list are added by the workgroup that finishes
+// last, those of a larger one by a kernel of their own (kListFused).
+
+struct StatsArgs {
+    const ListTile *tiles;
+    int64_t t_begin, t_end;
+    int32_t first, part0;   // first tensor and first partial of the launch
+    int32_t total;          // partials of all launches of the pass
+    int32_t finalize;       // 0: the record only
+    DevState *st;
+    Partial *part;
+    uint32_t *done;         // FUSED: workgroups that have finished; zero between passes
+    Record *rec;
+    StepRec *sr;
+    dopt_stats *out;
+    FinalizeArgs fa;
+};
+static_assert(sizeof(ListPtrs) <= 3840 && sizeof(GradPtrs) + sizeof(StatsArgs) <= 4096,
+              "addresses must fit the kernel argument space");
+
+// A wave's sums by a fixed butterfly.
+__device__ __forceinline__ void wave_sum(double &acc, unsigned long long &z) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        acc += __shfl_xor(acc, off, 64);
+        z += __shfl_xor(z, off, 64);
+    }
+}
+
+// The sum of the partials in a fixed order (thread i adds partials i, i +
+// THREADS, ...; each wave folds its lanes; thread 0 adds the waves), the
+// record and the finalize, by one whole workgroup.  The hyper-groups' scalars
+// are formed for the step that follows a clean pass while the loads are in
+// flight, and stored if the pass was clean.
+// AGENT: the partials were written by workgroups of this launch, on any XCD.
+template <int THREADS, int BATCH, bool AGENT>
+__device__ __forceinline__ void finish_stats(const StatsArgs &a) {
+    __shared__ double f_acc[THREADS / 64];
+    __shared__ unsigned long long f_z[THREADS / 64];
+    __shared__ int f_skip;
+    const DevState cur = *a.st;
     double acc = 0.0;
-    uint32_t zeros = 0;
-    for (int64_t t0 = t_begin + int64_t(blockIdx.x) * kListStatsTiles; t0 < t_end;
+    unsigned long long z = 0;
+    Hp mine{};
+    for (int32_t i0 = threadIdx.x; i0 < a.total; i0 += BATCH * THREADS) {
+        double s[BATCH];
+        unsigned long long q[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int32_t i = i0 + j * THREADS < a.total ? i0 + j * THREADS : a.total - 1;
+            if (AGENT) {
+                s[j] = __hip_atomic_load(&a.part[i].sumsq, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                q[j] = __hip_atomic_load(&a.part[i].zeros, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            } else {
+                const Partial x = a.part[i];
+                s[j] = x.sumsq;
+                q[j] = x.zeros;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const bool in = i0 + j * THREADS < a.total;  // a clamped duplicate adds +0
+            acc += in ? s[j] : 0.0;
+            z += in ? q[j] : 0ull;
+        }
+    }
+    // the last wave, whose partials are the fewest
+    const int h = static_cast<int>(threadIdx.x) - (THREADS - 64);
+    if (a.finalize && h >= 0 && h < a.fa.nh) mine = step_scalars(a.fa.hp[h], static_cast<double>(cur.t + 1));
+    wave_sum(acc, z);
+    if ((threadIdx.x & 63) == 0) {
+        f_acc[threadIdx.x >> 6] = acc;
+        f_z[threadIdx.x >> 6] = z;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        unsigned long long tz = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w) {
+            t += f_acc[w];
+            tz += f_z[w];
+        }
+        a.rec->sumsq = t;
+        a.rec->zeros = static_cast<double>(tz);
+        f_skip = isfinite(t) ? 0 : 1;
+        if (a.finalize) decide_step(t, static_cast<double>(tz), cur, a.st, a.sr, a.out, a.fa.max_norm);
+    }
+    __syncthreads();
+    if (a.finalize && !f_skip && h >= 0 && h < a.fa.nh) store_scalars(a.sr, h, mine);
+}
+
+// One unscaled grad; a slot of no element (in false) holds 0 and adds +0.
+__device__ __forceinline__ void add_grad(float x, bool in, double &acc, uint32_t &zeros) {
+    const double xd = static_cast<double>(x);
+    acc = fma(xd, xd, acc);
+    zeros += (in && x == 0.0f) ? 1u : 0u;
+}
+
+template <int THREADS, int BATCH>
+__global__ void __launch_bounds__(THREADS) k_list_finish(StatsArgs a) {
+    finish_stats<THREADS, BATCH, false>(a);
+}
+
+template <int GD, bool FUSED>
+__global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradPtrs ptrs) {
+    const float inv = a.st->inv_scale;
+    double acc = 0.0;
+    uint32_t zeros = 0;  // of one lane: at most its share of 2^38 elements over its workgroup's 256
+    for (int64_t t0 = a.t_begin + int64_t(blockIdx.x) * kListStatsTiles; t0 < a.t_end;
          t0 += int64_t(gridDim.x) * kListStatsTiles) {
         typename Quad<GD>::Raw raw[kListStatsTiles][kGroups];
         int n[kListStatsTiles][kGroups];
 #pragma unroll
         for (int u = 0; u < kListStatsTiles; ++u) {
-            const ListTile d = tiles[t0 + u < t_end ? t0 + u : t_end - 1];
-            const void *g = ptrs.p[d.index - first];
+            const ListTile d = a.tiles[t0 + u < a.t_end ? t0 + u : a.t_end - 1];
+            const void *g = ptrs.p[d.index - a.first];
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
-                const Place L = place_of(d, k);
-                n[u][k] = t0 + u < t_end ? L.n : 0;
+                const Place L = place_of(d, k, threadIdx.x);
+                n[u][k] = t0 + u < a.t_end ? L.n : 0;
                 raw[u][k] = load4<GD>(g, L.e, n[u][k]);
             }
         }
@@ -333,15 +433,49 @@ __global__ void __launch_bounds__(kBlock) k_list_stats(const ListTile *__restric
                 float g[kQuad];
                 unpack4<GD>(raw[u][k], g);
 #pragma unroll
-                for (int j = 0; j < kQuad; ++j) {  // a slot of no element adds +0
-                    const float x = g[j] * inv;
-                    const double xd = static_cast<double>(x);
-                    acc = fma(xd, xd, acc);
-                    zeros += (j < n[u][k] && x == 0.0f) ? 1u : 0u;
-                }
+                for (int j = 0; j < kQuad; ++j) add_grad(g[j] * inv, j < n[u][k], acc, zeros);
             }
     }
-    block_sum_store(acc, zeros, out + blockIdx.x);
+    __shared__ double s_acc[kBlock / 64];
+    __shared__ unsigned long long s_z[kBlock / 64];
+    __shared__ bool s_last;
+    unsigned long long z = zeros;
+    wave_sum(acc, z);
+    if ((threadIdx.x & 63) == 0) {
+        s_acc[threadIdx.x >> 6] = acc;
+        s_z[threadIdx.x >> 6] = z;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        unsigned long long tz = 0;
+#pragma unroll
+        for (int w = 0; w < kBlock / 64; ++w) {
+            t += s_acc[w];
+            tz += s_z[w];
+        }
+        Partial *dst = a.part + a.part0 + blockIdx.x;
+        if (!FUSED) {
+            dst->sumsq = t;
+            dst->zeros = tz;
+        } else {
+            // the partial goes past this XCD's L2, and the count is released after it
+            __hip_atomic_store(&dst->sumsq, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&dst->zeros, tz, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_last = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == uint32_t(a.total) - 1;
+        }
+    }
+    if constexpr (FUSED) {
+        __syncthreads();
+        if (!s_last) return;
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        if (threadIdx.x == 0) __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        finish_stats<kBlock, 1, true>(a);
+    }
+}
+
+__global__ void k_list_done(uint32_t *done) {
+    if (threadIdx.x == 0) *done = 0;
 }
 
 // ---- pass 2 -------------------------------------------------------------------------
@@ -362,7 +496,7 @@ __global__ void __launch_bounds__(kBlock) k_list_apply(const ListTile *__restric
     Moments<ST> mom[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        L[k] = place_of(d, k);
+        L[k] = place_of(d, k, threadIdx.x);
         graw[k] = load4<GD>(q.grad, L[k].e, L[k].n);
         praw[k] = PD == DOPT_F32 ? load4<DOPT_F32>(q.param, L[k].e, L[k].n) : load4<DOPT_F32>(s.master, L[k].arena, L[k].n);
         mom[k].load(s, L[k]);
@@ -400,7 +534,7 @@ __global__ void __launch_bounds__(kBlock) k_list_export(const ListTile *__restri
     Moments<ST> mom[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        L[k] = place_of(d, k);
+        L[k] = place_of(d, k, threadIdx.x);
         praw[k] = PD == DOPT_F32 ? load4<DOPT_F32>(param, L[k].e, L[k].n) : load4<DOPT_F32>(s.master, L[k].arena, L[k].n);
         mom[k].load(s, L[k]);
     }
@@ -427,7 +561,7 @@ __global__ void __launch_bounds__(kBlock) k_list_import(const ListTile *__restri
     u32x4 praw[kGroups], araw[kGroups], braw[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        L[k] = place_of(d, k);
+        L[k] = place_of(d, k, threadIdx.x);
         praw[k] = load4<DOPT_F32>(x.p, o + L[k].e, L[k].n);
         araw[k] = load4<DOPT_F32>(x.m, o + L[k].e, L[k].n);
         braw[k] = load4<DOPT_F32>(x.v, o + L[k].e, L[k].n);
@@ -455,7 +589,7 @@ __global__ void __launch_bounds__(kBlock) k_list_init(const ListTile *__restrict
     const int whole = (static_cast<int>(d.packed & 0xffffu) + kListBlock - 1) / kListBlock * kListBlock;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        const Place L = place_of(d, k);
+        const Place L = place_of(d, k, threadIdx.x);
         const int n = L.n + whole - static_cast<int>(d.packed & 0xffffu);  // slots of the tensor's blocks
         if (n <= 0) continue;
         if (masters) {
@@ -543,24 +677,45 @@ static void with_state(int kind, F f) {
     else f(Const<DOPT_STATE_F32>());
 }
 
-template <bool FINALIZE>
+// Pass 1 over every class; fa null: the record only.
 static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void *ws, hipStream_t stream,
-                             const FinalizeArgs &fa) {
-    const DevState *st = reinterpret_cast<const DevState *>(ws_ptr(ws, kWsState));
-    Partial *part = reinterpret_cast<Partial *>(ws_ptr(ws, kWsPartials));
-    for (const ListClass &C : P->classes)
+                             const FinalizeArgs *fa) {
+    StatsArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.total = P->total_partials;
+    const bool fused = a.total > 0 && a.total <= kListFused;
+    a.finalize = fa != nullptr;
+    if (fa) a.fa = *fa;
+    a.st = reinterpret_cast<DevState *>(ws_ptr(ws, kWsState));
+    a.part = reinterpret_cast<Partial *>(ws_ptr(ws, kWsPartials));
+    a.done = reinterpret_cast<uint32_t *>(ws_ptr(ws, kWsListDone));
+    a.rec = reinterpret_cast<Record *>(ws_ptr(ws, kWsRecord));
+    a.sr = reinterpret_cast<StepRec *>(ws_ptr(ws, kWsStepRec));
+    a.out = reinterpret_cast<dopt_stats *>(ws_ptr(ws, kWsStats));
+    for (const ListClass &C : P->classes) {
+        a.tiles = tiles_of(C, ws);
         for (const ListRange &r : C.stats) {
-            GradPtrs a;
-            std::memset(&a, 0, sizeof a);
-            for (int32_t i = 0; i < r.count; ++i) a.p[i] = ts[C.tensors[static_cast<size_t>(r.first + i)]].grad;
+            GradPtrs g;
+            for (int32_t i = 0; i < r.count; ++i) g.p[i] = ts[C.tensors[static_cast<size_t>(r.first + i)]].grad;
+            a.t_begin = r.t0;
+            a.t_end = r.t1;
+            a.first = r.first;
+            a.part0 = r.partial_base;
             with_dtype(C.gd, [&](auto gd) {
-                k_list_stats<decltype(gd)::value><<<r.grid, kBlock, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, st,
-                                                                                 part + r.partial_base, a);
+                if (fused) k_list_stats<decltype(gd)::value, true><<<r.grid, kBlock, 0, stream>>>(a, g);
+                else k_list_stats<decltype(gd)::value, false><<<r.grid, kBlock, 0, stream>>>(a, g);
             });
             const int rc = check_launch("launch k_list_stats");
-            if (rc) return rc;
+            if (rc) {
+                k_list_done<<<1, 64, 0, stream>>>(a.done);  // the pass is not complete: forget its count
+                return rc;
+            }
         }
-    return launch_finish<FINALIZE>(P->total_partials, ws, stream, fa);
+    }
+    if (fused) return DOPT_OK;
+    if (a.total <= kFinishSmall) k_list_finish<256, 8><<<1, 256, 0, stream>>>(a);
+    else k_list_finish<1024, 16><<<1, 1024, 0, stream>>>(a);
+    return check_launch("launch k_list_finish");
 }
 
 template <bool IMPORT>
@@ -625,15 +780,15 @@ int dopt_list_init(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
         }
     }
     if ((rc = launch_init_records(*sc, ws, stream))) return rc;
+    k_list_done<<<1, 64, 0, stream>>>(reinterpret_cast<uint32_t *>(ws_ptr(ws, kWsListDone)));
+    if ((rc = check_launch("launch k_list_done"))) return rc;
     return hip_check(hipStreamSynchronize(stream), "synchronize after list init");
 }
 
 int dopt_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void *ws, hipStream_t stream) {
     int rc = check_list(P, ws);
     if (rc || (rc = check_tensors(P, ts, true, false))) return rc;
-    FinalizeArgs none;
-    std::memset(&none, 0, sizeof none);
-    return launch_list_stats<false>(P, ts, ws, stream, none);
+    return launch_list_stats(P, ts, ws, stream, nullptr);
 }
 
 int dopt_list_finalize(const dopt_list *P, const dopt_hparams *hp, int32_t n_hgroups, double max_grad_norm, void *ws,
@@ -651,7 +806,7 @@ int dopt_list_prepare(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_h
     if (rc || (rc = check_tensors(P, ts, true, false)) ||
         (rc = build_finalize_args(P->max_hgroup, hp, n_hgroups, max_grad_norm, a)))
         return rc;
-    return launch_list_stats<true>(P, ts, ws, stream, a);
+    return launch_list_stats(P, ts, ws, stream, &a);
 }
 
 int dopt_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list_state *state, void *ws,
