@@ -83,6 +83,7 @@ static int plan(dopt_list &P) {
         }
     }
     P.total_partials = partials;
+    for (const ListClass &C : P.classes) P.total_tiles += static_cast<int64_t>(C.tiles.size());
     int64_t ws = kWsPartials + up(int64_t(partials) * 16, 256);
     for (ListClass &C : P.classes) {
         C.ws_tiles = ws;

@@ -72,6 +72,10 @@ struct ListClass {
     int64_t ws_tiles = 0, ws_xoff = 0;  // byte offsets in the workspace
 };
 
+// A list of at most this many tiles is stepped by one launch of one workgroup
+// (k_list_small).
+constexpr int kSmallTiles = 4;
+
 struct ListTensor {
     int64_t numel = 0, arena = 0, xoff = 0, param = -1;
     int32_t pd = 0, gd = 0, hgroup = 0;
@@ -86,4 +90,5 @@ struct dopt_list {
     std::vector<dopt::ListClass> classes;
     int64_t numel = 0, arena_numel = 0, ws_bytes = 0;
     int32_t total_partials = 0;
+    int64_t total_tiles = 0;
 };

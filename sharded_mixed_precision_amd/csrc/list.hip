@@ -217,6 +217,12 @@ __device__ __forceinline__ int64_t tile_of(int64_t b, int64_t n) {
     return b / (kXcds * kXcdRun) * (kXcds * kXcdRun) + b % kXcds * kXcdRun + b / kXcds % kXcdRun;
 }
 
+// Whether a wave's group of a tile holds an element (wave-uniform).
+__device__ __forceinline__ bool group_lives(const ListTile &d, int group, int thread) {
+    return __builtin_amdgcn_readfirstlane(thread >> 6) * (kGroup * kGroups) + group * kGroup <
+           static_cast<int>(d.packed & 0xffffu);
+}
+
 // A lane's 4 elements of one group of its tile.
 struct Place {
     int64_t e;      // the first within the tensor
@@ -225,8 +231,11 @@ struct Place {
 };
 
 // `thread`: among the kBlock that share the tile.
+__device__ __forceinline__ int lane_offset(int group, int thread) {
+    return (thread >> 6) * (kGroup * kGroups) + group * kGroup + (thread & 63) * kQuad;
+}
 __device__ __forceinline__ Place place_of(const ListTile &d, int group, int thread) {
-    const int l = (thread >> 6) * (kGroup * kGroups) + group * kGroup + (thread & 63) * kQuad;
+    const int l = lane_offset(group, thread);
     return Place{int64_t(d.tile) * kTile + l, int64_t(d.block) * kListBlock + l, static_cast<int>(d.packed & 0xffffu) - l};
 }
 
@@ -515,6 +524,159 @@ __global__ void __launch_bounds__(kBlock) k_list_apply(const ListTile *__restric
     }
 }
 
+// ---- the whole step of a small list ---------------------------------------------------
+//
+// At most kSmallTiles tiles: one workgroup of that many times kBlock threads
+// takes both passes, a quarter a tile, and sums, stats and results are those
+// of the two launches bit for bit.  Everything is read once, before anything
+// is waited for; pass 1 takes the grads over LDS in the order of its own
+// kernel, and the hyper-groups' scalars are formed meanwhile.  Latency is all
+// there is here, and what four waves of a SIMD compute one after the other:
+// groups without elements are left out (pass 2 of a large list, where they
+// are rare, ran 1.5% slower with that test).  On MI355X, back to back, a step
+// of 2,608 bf16 elements in 4 tensors takes 8.8 us, 12 in two launches; four
+// whole tiles take 11.2 with e4m3 moments and 9.3 with fp32 ones, 11.6 and
+// 10.5 in two.
+// Arrays of the arguments are indexed with scalars: their elements are whole
+// words, for scalar loads ignore the low two bits of each part of an address.
+struct SmallTile {
+    ListTile t;
+    dopt_list_ptrs p;
+    int32_t pd, gd;
+};
+struct SmallRun {
+    int32_t first, n;
+};
+struct SmallArgs {
+    StateArrays s;
+    DevState *st;
+    Record *rec;
+    StepRec *sr;
+    dopt_stats *out;
+    int32_t n_tiles, n_runs;
+    SmallTile tiles[kSmallTiles];
+    SmallRun runs[kSmallTiles];  // the tiles of pass 1's partials
+    FinalizeArgs fa;
+};
+static_assert(sizeof(SmallTile) % 4 == 0 && sizeof(SmallRun) % 4 == 0, "scalar loads take whole words");
+static_assert(sizeof(SmallArgs) <= 4096, "the list must fit the kernel argument space");
+
+// load4, unpack4 and store4 of a type that is an argument.
+__device__ __forceinline__ u32x4 load4_any(int dt, const void *base, int64_t i, int n) {
+    if (dt == DOPT_F32) return load4<DOPT_F32>(base, i, n);
+    const u32x2 r = load4<DOPT_BF16>(base, i, n);  // the bits of either 16-bit type
+    return u32x4{r[0], r[1], 0, 0};
+}
+__device__ __forceinline__ void unpack4_any(int dt, u32x4 r, float (&x)[kQuad]) {
+    if (dt == DOPT_F32) unpack4<DOPT_F32>(r, x);
+    else if (dt == DOPT_BF16) unpack4<DOPT_BF16>(u32x2{r[0], r[1]}, x);
+    else unpack4<DOPT_F16>(u32x2{r[0], r[1]}, x);
+}
+__device__ __forceinline__ void store4_any(int dt, void *base, int64_t i, int n, const float (&x)[kQuad]) {
+    if (dt == DOPT_F32) store4<DOPT_F32>(base, i, n, x);
+    else if (dt == DOPT_BF16) store4<DOPT_BF16>(base, i, n, x);
+    else store4<DOPT_F16>(base, i, n, x);
+}
+
+template <int ST>
+__global__ void __launch_bounds__(kSmallTiles * kBlock) k_list_small(SmallArgs a) {
+    __shared__ float s_g[kSmallTiles][kGroups][kQuad][kBlock];
+    __shared__ double s_acc[kSmallTiles][kBlock / 64];
+    __shared__ unsigned long long s_z[kSmallTiles][kBlock / 64];
+    __shared__ StepRec s_rec;
+    const int mine = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kBlock);  // this quarter's tile
+    const int thread = threadIdx.x % kBlock;
+    const SmallTile t = a.tiles[mine];  // of no element beyond n_tiles
+    float *const master = a.s.master;
+    const DevState cur = *a.st;
+    Place L[kGroups];
+    u32x4 graw[kGroups], praw[kGroups];
+    Moments<ST> mom[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        if (!group_lives(t.t, k, thread)) continue;
+        L[k] = place_of(t.t, k, thread);
+        graw[k] = load4_any(t.gd, t.p.grad, L[k].e, L[k].n);
+        praw[k] = t.pd == DOPT_F32 ? load4<DOPT_F32>(t.p.param, L[k].e, L[k].n)
+                                   : load4<DOPT_F32>(master, L[k].arena, L[k].n);
+        mom[k].load(a.s, L[k]);
+    }
+    Hp scal{};
+    const int h = static_cast<int>(threadIdx.x) - (kSmallTiles * kBlock - 64);  // the last wave's lanes
+    if (h >= 0 && h < a.fa.nh) scal = step_scalars(a.fa.hp[h], static_cast<double>(cur.t + 1));
+    float g[kGroups][kQuad];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        if (!group_lives(t.t, k, thread)) continue;
+        unpack4_any(t.gd, graw[k], g[k]);
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j) s_g[mine][k][j][thread] = g[k][j];
+    }
+    __syncthreads();
+    // pass 1: quarter r adds partial r
+    if (mine < a.n_runs) {
+        double acc = 0.0;
+        uint32_t zeros = 0;
+        for (int u = a.runs[mine].first; u < a.runs[mine].first + a.runs[mine].n; ++u) {
+            const ListTile d = a.tiles[u].t;
+            const int count = static_cast<int>(d.packed & 0xffffu);
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                if (!group_lives(d, k, thread)) continue;  // it would add +0
+#pragma unroll
+                for (int j = 0; j < kQuad; ++j)
+                    add_grad(s_g[u][k][j][thread] * cur.inv_scale, lane_offset(k, thread) + j < count, acc, zeros);
+            }
+        }
+        unsigned long long z = zeros;
+        wave_sum(acc, z);
+        if ((thread & 63) == 0) {
+            s_acc[mine][thread >> 6] = acc;
+            s_z[mine][thread >> 6] = z;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        double acc = 0.0;
+        unsigned long long z = 0;
+        if (static_cast<int>(threadIdx.x) < a.n_runs)
+#pragma unroll
+            for (int w = 0; w < kBlock / 64; ++w) {
+                acc += s_acc[threadIdx.x][w];
+                z += s_z[threadIdx.x][w];
+            }
+        wave_sum(acc, z);
+        if (threadIdx.x == 0) {
+            a.rec->sumsq = acc;
+            a.rec->zeros = static_cast<double>(z);
+            decide_step(acc, static_cast<double>(z), cur, a.st, &s_rec, a.out, a.fa.max_norm);
+            a.sr->skip = s_rec.skip;
+            a.sr->inv_scale = s_rec.inv_scale;
+            a.sr->clip_on = s_rec.clip_on;
+            a.sr->clip = s_rec.clip;
+        }
+    }
+    if (h >= 0 && h < a.fa.nh) store_scalars(&s_rec, h, scal);
+    __syncthreads();
+    if (s_rec.skip) return;
+    if (h >= 0 && h < a.fa.nh) store_scalars(a.sr, h, scal);
+    // pass 2
+    const Hp hp = load_hp(&s_rec, t.t.packed >> 16);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        if (!group_lives(t.t, k, thread)) continue;
+        float p[kQuad], x[kQuad], y[kQuad], root[kQuad];
+        unpack4<DOPT_F32>(praw[k], p);
+        mom[k].decode(x, y);
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j)
+            root[j] = adamw_root(g[k][j], p[j], x[j], y[j], s_rec.inv_scale, s_rec.clip_on, s_rec.clip, hp);
+        Moments<ST>::store(a.s, L[k], x, y, root);
+        if (t.pd != DOPT_F32) store4<DOPT_F32>(master, L[k].arena, L[k].n, p);
+        store4_any(t.pd, t.p.param, L[k].e, L[k].n, p);
+    }
+}
+
 // ---- export, import, init -----------------------------------------------------------
 
 struct ExportArrays {
@@ -718,6 +880,54 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void 
     return check_launch("launch k_list_finish");
 }
 
+// Pass 2 over every class.
+static int launch_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const StateArrays &s, void *ws,
+                             hipStream_t stream) {
+    const StepRec *rec = reinterpret_cast<const StepRec *>(ws_ptr(ws, kWsStepRec));
+    for (const ListClass &C : P->classes)
+        for (const ListRange &r : C.apply) {
+            const ListPtrs a = slots(C, r, ts);
+            with_dtype(C.pd, [&](auto pd) {
+                with_dtype(C.gd, [&](auto gd) {
+                    with_state(P->state_kind, [&](auto st) {
+                        k_list_apply<decltype(pd)::value, decltype(gd)::value, decltype(st)::value>
+                            <<<r.grid, kBlock, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, s, rec, a);
+                    });
+                });
+            });
+            const int rc = check_launch("launch k_list_apply");
+            if (rc) return rc;
+        }
+    return DOPT_OK;
+}
+
+// Both passes of a list of at most kSmallTiles tiles.
+static int launch_list_small(const dopt_list *P, const dopt_list_ptrs *ts, const StateArrays &s, const FinalizeArgs &fa,
+                             void *ws, hipStream_t stream) {
+    SmallArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.s = s;
+    a.st = reinterpret_cast<DevState *>(ws_ptr(ws, kWsState));
+    a.rec = reinterpret_cast<Record *>(ws_ptr(ws, kWsRecord));
+    a.sr = reinterpret_cast<StepRec *>(ws_ptr(ws, kWsStepRec));
+    a.out = reinterpret_cast<dopt_stats *>(ws_ptr(ws, kWsStats));
+    a.fa = fa;
+    for (const ListClass &C : P->classes) {
+        const int n = static_cast<int>(C.tiles.size());
+        for (int t = 0; t < n; ++t) {
+            const int i = a.n_tiles + t;
+            const ListTile &d = C.tiles[static_cast<size_t>(t)];
+            a.tiles[i] = SmallTile{d, ts[C.tensors[d.index]], C.pd, C.gd};
+        }
+        for (int t = 0; t < n; t += kListStatsTiles)
+            a.runs[a.n_runs++] = SmallRun{a.n_tiles + t, std::min(kListStatsTiles, n - t)};
+        a.n_tiles += n;
+    }
+    if (P->state_kind == DOPT_STATE_E4M3) k_list_small<DOPT_STATE_E4M3><<<1, kSmallTiles * kBlock, 0, stream>>>(a);
+    else k_list_small<DOPT_STATE_F32><<<1, kSmallTiles * kBlock, 0, stream>>>(a);
+    return check_launch("launch k_list_small");
+}
+
 template <bool IMPORT>
 static int list_copy(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list_state *state, ExportArrays x,
                      void *ws, hipStream_t stream) {
@@ -814,21 +1024,7 @@ int dopt_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_lis
     StateArrays s;
     int rc = check_list(P, ws);
     if (rc || (rc = check_tensors(P, ts, true, true)) || (rc = check_state(P, state, s))) return rc;
-    const StepRec *rec = reinterpret_cast<const StepRec *>(ws_ptr(ws, kWsStepRec));
-    for (const ListClass &C : P->classes)
-        for (const ListRange &r : C.apply) {
-            const ListPtrs a = slots(C, r, ts);
-            with_dtype(C.pd, [&](auto pd) {
-                with_dtype(C.gd, [&](auto gd) {
-                    with_state(P->state_kind, [&](auto st) {
-                        k_list_apply<decltype(pd)::value, decltype(gd)::value, decltype(st)::value>
-                            <<<r.grid, kBlock, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, s, rec, a);
-                    });
-                });
-            });
-            if ((rc = check_launch("launch k_list_apply"))) return rc;
-        }
-    return DOPT_OK;
+    return launch_list_apply(P, ts, s, ws, stream);
 }
 
 int dopt_list_step(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list_state *state, const dopt_hparams *hp,
@@ -837,8 +1033,15 @@ int dopt_list_step(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
     StateArrays s;
     int rc = check_list(P, ws);
     if (rc || (rc = check_tensors(P, ts, true, true)) || (rc = check_state(P, state, s))) return rc;
-    if ((rc = dopt_list_prepare(P, ts, hp, n_hgroups, max_grad_norm, ws, stream))) return rc;
-    if ((rc = dopt_list_apply(P, ts, state, ws, stream))) return rc;
+    FinalizeArgs a;
+    if ((rc = build_finalize_args(P->max_hgroup, hp, n_hgroups, max_grad_norm, a))) return rc;
+    if (P->total_tiles > 0 && P->total_tiles <= kSmallTiles) {
+        rc = launch_list_small(P, ts, s, a, ws, stream);
+    } else {
+        rc = launch_list_stats(P, ts, ws, stream, &a);
+        if (rc == DOPT_OK) rc = launch_list_apply(P, ts, s, ws, stream);
+    }
+    if (rc) return rc;
     return out ? copy_stats(ws, stream, out) : DOPT_OK;
 }
 
