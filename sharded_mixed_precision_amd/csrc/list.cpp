@@ -16,10 +16,11 @@ static int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 static bool known_dtype(int32_t d) { return d == DOPT_F32 || d == DOPT_BF16 || d == DOPT_F16; }
 
-// Ranges of at most `slots` consecutive tensors and kListLaunchTiles tiles of
-// a class (a tensor of more tiles lies in several).
-static void cut(const ListClass &C, int slots, std::vector<ListRange> &out) {
+// Ranges of about as many consecutive tensors, at most `most`, and at most
+// `launch` tiles of a class (a tensor of more tiles lies in several).
+static void cut(const ListClass &C, int most, int64_t launch, std::vector<ListRange> &out) {
     const int32_t n = static_cast<int32_t>(C.tensors.size());
+    const int32_t parts = (n + most - 1) / most, slots = (n + parts - 1) / parts;
     const int64_t n_tiles = static_cast<int64_t>(C.tiles.size());
     int64_t t = 0;
     for (int32_t f = 0; f < n; f += slots) {
@@ -28,7 +29,7 @@ static void cut(const ListClass &C, int slots, std::vector<ListRange> &out) {
         r.count = std::min(slots, n - f);
         while (t < n_tiles && C.tiles[static_cast<size_t>(t)].index < uint32_t(f + r.count)) {
             r.t0 = t;
-            while (t < n_tiles && t - r.t0 < kListLaunchTiles && C.tiles[static_cast<size_t>(t)].index < uint32_t(f + r.count))
+            while (t < n_tiles && t - r.t0 < launch && C.tiles[static_cast<size_t>(t)].index < uint32_t(f + r.count))
                 ++t;
             r.t1 = t;
             out.push_back(r);
@@ -73,8 +74,8 @@ static int plan(dopt_list &P) {
     P.arena_numel = blocks * kListBlock;
     int32_t partials = 0;
     for (ListClass &C : P.classes) {
-        cut(C, kListSlots, C.apply);
-        cut(C, kListGradSlots, C.stats);
+        cut(C, kListSlots, list_launch_tiles(P.state_kind), C.apply);
+        cut(C, kListGradSlots, kListStatsLaunch, C.stats);
         for (ListRange &r : C.apply) r.grid = static_cast<int32_t>(r.t1 - r.t0);
         for (ListRange &r : C.stats) {
             r.grid = list_stats_grid(r.t1 - r.t0);
@@ -90,6 +91,8 @@ static int plan(dopt_list &P) {
         ws += up(int64_t(C.tiles.size()) * int64_t(sizeof(ListTile)), 256);
         C.ws_xoff = ws;
         ws += up(int64_t(C.xoff.size()) * 8, 256);
+        C.ws_addr = ws;
+        ws += up(int64_t(C.tensors.size()) * int64_t(sizeof(dopt_list_ptrs)), 256);
     }
     P.ws_bytes = ws;
     return DOPT_OK;

@@ -23,15 +23,34 @@ struct ListTile {
     uint32_t packed;  // elements (1 .. kTile) | hyper-group << 16
 };
 
-// Tensor addresses reach a kernel by value, in its arguments (4 KB hold
-// kListSlots param and grad pairs, or kListGradSlots grads beside pass 1's own);
-// a list of more tensors of one class takes a launch for each so many.  Nothing is copied
-// from the host and the addresses may change from call to call.
-constexpr int kListSlots = 240;
-constexpr int kListGradSlots = 400;
+// Tensor addresses reach a kernel by value, in its arguments: nothing is
+// copied from the host, the addresses may change from call to call, and a
+// captured call keeps its own.  The arguments hold 4 KB; as 32-bit distances
+// in elements from the lowest address of the launch, that is kListSlots param
+// and grad pairs, or kListGradSlots grads beside pass 1's own arguments.  A
+// class of more tensors takes more launches, of about as many tensors each.
+// If tensors of a launch lie further apart (8 GB for 16-bit types, 16 for
+// fp32), k_list_put writes the class's addresses into the workspace first,
+// kListPut at a time: the launches and the order of the sums stay the same.
+// 500 tensors of 1.8e7 elements in all were stepped in 77.6 us on MI355X, 86.0
+// with full addresses in the arguments (240 to a launch); the statistics of
+// 1500 tensors of 1.3e7 took 19.0 and 26.0 us.
+constexpr int kListSlots = 480;
+constexpr int kListGradSlots = 800;
+constexpr int kListPut = 240;
 
-// Tiles of one launch: 2^28 threads, below the 2^32 a launch may have.
-constexpr int64_t kListLaunchTiles = int64_t(1) << 20;
+// Tiles of one launch.  The XCDs take their workgroups of a long launch at
+// slightly different rates and drift apart along the arrays; pass 2 and the
+// copies, which write as much as they read, are therefore launched piece by
+// piece, of about 2e9 bytes.  On MI355X, per launch 2^20 / 2^18 / 2^17 / 2^16 /
+// 2^15 tiles: pass 2 of 1.1e9 bf16 params with fp32 moments 5.25 / 5.24 / 5.12 /
+// 5.05 / 5.03 ms, of 1.2e8 fp32 params 0.592 (to 2^16) / 0.576; with e4m3 moments
+// 1.0e9 params and fp32 grads 2.94 / 2.90 / 2.88 / 2.90 / 2.94, 1.2e8 bf16 0.333 (to
+// 2^16) / 0.338; export of 1.0e9 3.25 / 3.15 / 3.03 / 2.96 / 2.95.  Pass 1 only reads and
+// loses by it (1.1e9 bf16 grads 328 us in one launch, 435 at 2^15); its limit
+// keeps a launch below 2^32 threads.
+constexpr int64_t kListStatsLaunch = int64_t(1) << 20;
+inline int64_t list_launch_tiles(int state_kind) { return int64_t(1) << (state_kind == DOPT_STATE_E4M3 ? 16 : 15); }
 
 // Pass 2 and the copies take one workgroup per tile.  A workgroup of pass 1
 // reads kListStatsTiles tiles at a time and grid-strides, about 8 times on
@@ -69,7 +88,7 @@ struct ListClass {
     std::vector<ListTile> tiles;
     std::vector<int64_t> xoff;     // export offset per tensor of the class
     std::vector<ListRange> apply, stats;
-    int64_t ws_tiles = 0, ws_xoff = 0;  // byte offsets in the workspace
+    int64_t ws_tiles = 0, ws_xoff = 0, ws_addr = 0;  // byte offsets in the workspace
 };
 
 // A list of at most this many tiles is stepped by one launch of one workgroup

@@ -36,12 +36,47 @@ namespace dopt {
 
 // ---- tensor addresses ---------------------------------------------------------
 
-struct ListPtrs {
-    dopt_list_ptrs p[kListSlots];
+// The addresses of a launch's tensors: distances in elements from the lowest
+// of the launch, or a table of the class in the workspace.
+struct GradAddr {
+    const dopt_list_ptrs *table;
+    const char *grad0;
+    uint32_t grad[kListGradSlots];
 };
-struct GradPtrs {
-    const void *p[kListGradSlots];
+struct ListSlot {
+    uint32_t grad, param;
 };
+struct ListAddr {
+    const dopt_list_ptrs *table;
+    const char *grad0;
+    char *param0;
+    ListSlot s[kListSlots];
+};
+struct PutAddr {
+    dopt_list_ptrs p[kListPut];
+};
+
+__global__ void __launch_bounds__(kBlock) k_list_put(dopt_list_ptrs *__restrict__ dst, int32_t n, PutAddr a) {
+    if (static_cast<int>(threadIdx.x) < n) dst[threadIdx.x] = a.p[threadIdx.x];
+}
+static_assert(kListPut <= kBlock, "one thread an address");
+
+// Tensor `index` of the class, in a launch that begins with tensor `first`.
+// The distances are read whether they are used or not, beside the table's
+// address rather than after it.
+template <int PD, int GD>
+__device__ __forceinline__ dopt_list_ptrs ptrs_of(const ListAddr &a, uint32_t index, int32_t first) {
+    const ListSlot s = a.s[index - first];
+    dopt_list_ptrs p{a.grad0 + uint64_t(s.grad) * Elem<GD>::kBytes, a.param0 + uint64_t(s.param) * Elem<PD>::kBytes};
+    if (__builtin_expect(a.table != nullptr, 0)) p = a.table[index];
+    return p;
+}
+template <int GD>
+__device__ __forceinline__ const void *grad_of(const GradAddr &a, uint32_t index, int32_t first) {
+    const void *p = a.grad0 + uint64_t(a.grad[index - first]) * Elem<GD>::kBytes;
+    if (__builtin_expect(a.table != nullptr, 0)) p = a.table[index].grad;
+    return p;
+}
 
 // ---- element I/O at element alignment -------------------------------------------
 
@@ -78,15 +113,23 @@ __device__ __forceinline__ typename Quad<DT>::T down1(float x) {
     else return static_cast<uint16_t>(Elem<DT>::bits(x));
 }
 
+// A pointer into device memory, said to the compiler: one that came out of a
+// table would otherwise be accessed with flat instructions (pass 2 of 1.2e8
+// fp32 params on MI355X 603 us, 587 with global ones).
+template <class T>
+__device__ __forceinline__ __attribute__((address_space(1))) T *global(T *p) {
+    return (__attribute__((address_space(1))) T *)p;
+}
+
 // Elements i .. i+3 of a tensor, of which the first n exist (n <= 0: none);
 // the others read as 0.
 template <int DT>
 __device__ __forceinline__ typename Quad<DT>::Raw load4(const void *base, int64_t i, int n) {
     typedef Quad<DT> Q;
-    const typename Q::T *p = static_cast<const typename Q::T *>(base) + i;
+    const auto *p = global(static_cast<const typename Q::T *>(base)) + i;
     typename Q::Raw r{};
     if (n >= kQuad) {
-        r = __builtin_nontemporal_load(reinterpret_cast<const typename Q::At *>(p));
+        r = __builtin_nontemporal_load((const __attribute__((address_space(1))) typename Q::At *)p);
     } else {
 #pragma unroll
         for (int j = 0; j < kQuad - 1; ++j) {
@@ -111,7 +154,7 @@ __device__ __forceinline__ void unpack4(typename Quad<DT>::Raw r, float (&x)[kQu
 template <int DT>
 __device__ __forceinline__ void store4(void *base, int64_t i, int n, const float (&x)[kQuad]) {
     typedef Quad<DT> Q;
-    typename Q::T *p = static_cast<typename Q::T *>(base) + i;
+    auto *p = global(static_cast<typename Q::T *>(base)) + i;
     if (n >= kQuad) {
         typename Q::Raw r;
         if constexpr (DT == DOPT_F32) {
@@ -121,7 +164,7 @@ __device__ __forceinline__ void store4(void *base, int64_t i, int n, const float
             r[0] = Elem<DT>::bits(x[0]) | (Elem<DT>::bits(x[1]) << 16);
             r[1] = Elem<DT>::bits(x[2]) | (Elem<DT>::bits(x[3]) << 16);
         }
-        __builtin_nontemporal_store(r, reinterpret_cast<typename Q::At *>(p));
+        __builtin_nontemporal_store(r, (__attribute__((address_space(1))) typename Q::At *)p);
     } else {
 #pragma unroll
         for (int j = 0; j < kQuad - 1; ++j)
@@ -328,7 +371,7 @@ struct StatsArgs {
     dopt_stats *out;
     FinalizeArgs fa;
 };
-static_assert(sizeof(ListPtrs) <= 3840 && sizeof(GradPtrs) + sizeof(StatsArgs) <= 4096,
+static_assert(sizeof(ListAddr) <= 3936 && sizeof(GradAddr) + sizeof(StatsArgs) <= 4096,
               "addresses must fit the kernel argument space");
 
 // A wave's sums by a fixed butterfly.
@@ -416,7 +459,7 @@ __global__ void __launch_bounds__(THREADS) k_list_finish(StatsArgs a) {
 }
 
 template <int GD, bool FUSED>
-__global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradPtrs ptrs) {
+__global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradAddr addr) {
     const float inv = a.st->inv_scale;
     double acc = 0.0;
     uint32_t zeros = 0;  // of one lane: at most its share of 2^38 elements over its workgroup's 256
@@ -427,7 +470,7 @@ __global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradPtrs ptr
 #pragma unroll
         for (int u = 0; u < kListStatsTiles; ++u) {
             const ListTile d = a.tiles[t0 + u < a.t_end ? t0 + u : a.t_end - 1];
-            const void *g = ptrs.p[d.index - a.first];
+            const void *g = grad_of<GD>(addr, d.index, a.first);
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
                 const Place L = place_of(d, k, threadIdx.x);
@@ -492,10 +535,11 @@ __global__ void k_list_done(uint32_t *done) {
 template <int PD, int GD, int ST>
 __global__ void __launch_bounds__(kBlock) k_list_apply(const ListTile *__restrict__ tiles, int64_t t_begin,
                                                       int64_t t_end, int32_t first, StateArrays s,
-                                                      const StepRec *__restrict__ rec, ListPtrs ptrs) {
-    if (rec->skip) return;
+                                                      const StepRec *__restrict__ rec, ListAddr addr) {
+    const int skip = rec->skip;  // loaded beside the tile: a skipped step touches no data
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
-    const dopt_list_ptrs q = ptrs.p[d.index - first];
+    if (skip) return;
+    const dopt_list_ptrs q = ptrs_of<PD, GD>(addr, d.index, first);
     const Hp h = load_hp(rec, d.packed >> 16);
     const float inv = rec->inv_scale, clip = rec->clip;
     const int clip_on = rec->clip_on;
@@ -687,9 +731,9 @@ template <int PD, int ST>
 __global__ void __launch_bounds__(kBlock) k_list_export(const ListTile *__restrict__ tiles, int64_t t_begin,
                                                        int64_t t_end, int32_t first,
                                                        const int64_t *__restrict__ xoff, StateArrays s,
-                                                       ExportArrays x, ListPtrs ptrs) {
+                                                       ExportArrays x, ListAddr addr) {
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
-    const void *param = ptrs.p[d.index - first].param;
+    const void *param = ptrs_of<PD, PD>(addr, d.index, first).param;
     const int64_t o = xoff[d.index];
     Place L[kGroups];
     u32x4 praw[kGroups];
@@ -715,9 +759,9 @@ template <int PD, int ST>
 __global__ void __launch_bounds__(kBlock) k_list_import(const ListTile *__restrict__ tiles, int64_t t_begin,
                                                        int64_t t_end, int32_t first,
                                                        const int64_t *__restrict__ xoff, StateArrays s,
-                                                       ExportArrays x, ListPtrs ptrs) {
+                                                       ExportArrays x, ListAddr addr) {
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
-    void *param = ptrs.p[d.index - first].param;
+    void *param = ptrs_of<PD, PD>(addr, d.index, first).param;
     const int64_t o = xoff[d.index];
     Place L[kGroups];
     u32x4 praw[kGroups], araw[kGroups], braw[kGroups];
@@ -745,7 +789,7 @@ __global__ void __launch_bounds__(kBlock) k_list_import(const ListTile *__restri
 // Masters from the params, everything else zero, whole blocks of the arena.
 template <int PD, int ST>
 __global__ void __launch_bounds__(kBlock) k_list_init(const ListTile *__restrict__ tiles, int64_t t_begin,
-                                                     int32_t first, bool masters, StateArrays s, ListPtrs ptrs) {
+                                                     int32_t first, bool masters, StateArrays s, ListAddr addr) {
     const float z[kQuad] = {0, 0, 0, 0};
     const ListTile d = tiles[t_begin + blockIdx.x];
     const int whole = (static_cast<int>(d.packed & 0xffffu) + kListBlock - 1) / kListBlock * kListBlock;
@@ -756,7 +800,7 @@ __global__ void __launch_bounds__(kBlock) k_list_init(const ListTile *__restrict
         if (n <= 0) continue;
         if (masters) {
             float p[kQuad] = {0, 0, 0, 0};
-            if (PD != DOPT_F32) unpack4<PD>(load4<PD>(ptrs.p[d.index - first].param, L.e, L.n), p);
+            if (PD != DOPT_F32) unpack4<PD>(load4<PD>(ptrs_of<PD, PD>(addr, d.index, first).param, L.e, L.n), p);
             store4<DOPT_F32>(s.master, L.arena, n, p);
         }
         if constexpr (ST == DOPT_STATE_E4M3) {
@@ -815,11 +859,81 @@ static const ListTile *tiles_of(const ListClass &C, const void *ws) {
     return reinterpret_cast<const ListTile *>(static_cast<const char *>(ws) + C.ws_tiles);
 }
 
-static ListPtrs slots(const ListClass &C, const ListRange &r, const dopt_list_ptrs *ts) {
-    ListPtrs a;
+static int64_t bytes_of(int dt) { return dt == DOPT_F32 ? 4 : 2; }
+
+// Lowest address among n of a kind, and whether the others' distances from it
+// fit 32 bits.
+struct Span {
+    uintptr_t lo = UINTPTR_MAX, hi = 0;
+    void add(const void *p) {
+        lo = std::min(lo, reinterpret_cast<uintptr_t>(p));
+        hi = std::max(hi, reinterpret_cast<uintptr_t>(p));
+    }
+    bool fits(int dt) const { return hi < lo || (hi - lo) / bytes_of(dt) <= UINT32_MAX; }
+    uint32_t from(const void *p, int dt) const {
+        return static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) - lo) / bytes_of(dt));
+    }
+};
+
+// Whether the addresses of every launch of a class fit its arguments; if not,
+// writes them into the workspace.
+static int place_addresses(const ListClass &C, const std::vector<ListRange> &ranges, const dopt_list_ptrs *ts, bool grads,
+                           bool params, void *ws, hipStream_t stream, const dopt_list_ptrs *&table) {
+    table = nullptr;
+    bool fit = true;
+    for (const ListRange &r : ranges) {
+        Span g, p;
+        for (int32_t i = r.first; i < r.first + r.count; ++i) {
+            const dopt_list_ptrs &t = ts[C.tensors[static_cast<size_t>(i)]];
+            if (grads) g.add(t.grad);
+            if (params) p.add(t.param);
+        }
+        fit = fit && g.fits(C.gd) && p.fits(C.pd);
+    }
+    if (fit) return DOPT_OK;
+    dopt_list_ptrs *dst = reinterpret_cast<dopt_list_ptrs *>(ws_ptr(ws, C.ws_addr));
+    const int32_t n = static_cast<int32_t>(C.tensors.size());
+    for (int32_t f = 0; f < n; f += kListPut) {
+        PutAddr a;
+        std::memset(&a, 0, sizeof a);
+        const int32_t m = std::min(kListPut, n - f);
+        for (int32_t i = 0; i < m; ++i) a.p[i] = ts[C.tensors[static_cast<size_t>(f + i)]];
+        k_list_put<<<1, kBlock, 0, stream>>>(dst + f, m, a);
+        const int rc = check_launch("launch k_list_put");
+        if (rc) return rc;
+    }
+    table = dst;
+    return DOPT_OK;
+}
+
+static void fill(ListAddr &a, const ListClass &C, const ListRange &r, const dopt_list_ptrs *ts, bool grads,
+                 const dopt_list_ptrs *table) {
     std::memset(&a, 0, sizeof a);
-    for (int32_t i = 0; i < r.count; ++i) a.p[i] = ts[C.tensors[static_cast<size_t>(r.first + i)]];
-    return a;
+    a.table = table;
+    if (table) return;
+    Span g, p;
+    for (int32_t i = 0; i < r.count; ++i) {
+        const dopt_list_ptrs &t = ts[C.tensors[static_cast<size_t>(r.first + i)]];
+        if (grads) g.add(t.grad);
+        p.add(t.param);
+    }
+    a.grad0 = grads ? reinterpret_cast<const char *>(g.lo) : nullptr;
+    a.param0 = reinterpret_cast<char *>(p.lo);
+    for (int32_t i = 0; i < r.count; ++i) {
+        const dopt_list_ptrs &t = ts[C.tensors[static_cast<size_t>(r.first + i)]];
+        a.s[i] = ListSlot{grads ? g.from(t.grad, C.gd) : 0, p.from(t.param, C.pd)};
+    }
+}
+
+static void fill(GradAddr &a, const ListClass &C, const ListRange &r, const dopt_list_ptrs *ts,
+                 const dopt_list_ptrs *table) {
+    std::memset(&a, 0, sizeof a);
+    a.table = table;
+    if (table) return;
+    Span g;
+    for (int32_t i = 0; i < r.count; ++i) g.add(ts[C.tensors[static_cast<size_t>(r.first + i)]].grad);
+    a.grad0 = reinterpret_cast<const char *>(g.lo);
+    for (int32_t i = 0; i < r.count; ++i) a.grad[i] = g.from(ts[C.tensors[static_cast<size_t>(r.first + i)]].grad, C.gd);
 }
 
 // Calls f with an element type as a compile-time constant.
@@ -856,9 +970,12 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void 
     a.out = reinterpret_cast<dopt_stats *>(ws_ptr(ws, kWsStats));
     for (const ListClass &C : P->classes) {
         a.tiles = tiles_of(C, ws);
-        for (const ListRange &r : C.stats) {
-            GradPtrs g;
-            for (int32_t i = 0; i < r.count; ++i) g.p[i] = ts[C.tensors[static_cast<size_t>(r.first + i)]].grad;
+        const dopt_list_ptrs *table;
+        int rc = place_addresses(C, C.stats, ts, true, false, ws, stream, table);
+        for (size_t k = 0; rc == DOPT_OK && k < C.stats.size(); ++k) {
+            const ListRange &r = C.stats[k];
+            GradAddr g;
+            fill(g, C, r, ts, table);
             a.t_begin = r.t0;
             a.t_end = r.t1;
             a.first = r.first;
@@ -867,11 +984,11 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void 
                 if (fused) k_list_stats<decltype(gd)::value, true><<<r.grid, kBlock, 0, stream>>>(a, g);
                 else k_list_stats<decltype(gd)::value, false><<<r.grid, kBlock, 0, stream>>>(a, g);
             });
-            const int rc = check_launch("launch k_list_stats");
-            if (rc) {
-                k_list_done<<<1, 64, 0, stream>>>(a.done);  // the pass is not complete: forget its count
-                return rc;
-            }
+            rc = check_launch("launch k_list_stats");
+        }
+        if (rc) {
+            k_list_done<<<1, 64, 0, stream>>>(a.done);  // the pass is not complete: forget its count
+            return rc;
         }
     }
     if (fused) return DOPT_OK;
@@ -884,9 +1001,13 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void 
 static int launch_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const StateArrays &s, void *ws,
                              hipStream_t stream) {
     const StepRec *rec = reinterpret_cast<const StepRec *>(ws_ptr(ws, kWsStepRec));
-    for (const ListClass &C : P->classes)
+    for (const ListClass &C : P->classes) {
+        const dopt_list_ptrs *table;
+        int rc = place_addresses(C, C.apply, ts, true, true, ws, stream, table);
+        if (rc) return rc;
         for (const ListRange &r : C.apply) {
-            const ListPtrs a = slots(C, r, ts);
+            ListAddr a;
+            fill(a, C, r, ts, true, table);
             with_dtype(C.pd, [&](auto pd) {
                 with_dtype(C.gd, [&](auto gd) {
                     with_state(P->state_kind, [&](auto st) {
@@ -895,9 +1016,9 @@ static int launch_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const
                     });
                 });
             });
-            const int rc = check_launch("launch k_list_apply");
-            if (rc) return rc;
+            if ((rc = check_launch("launch k_list_apply"))) return rc;
         }
+    }
     return DOPT_OK;
 }
 
@@ -939,9 +1060,12 @@ static int list_copy(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_li
         if ((reinterpret_cast<uintptr_t>(x.p) | reinterpret_cast<uintptr_t>(x.m) | reinterpret_cast<uintptr_t>(x.v)) % 4)
             return fail(DOPT_ERR_INVALID, "export array not 4-byte aligned");
     }
-    for (const ListClass &C : P->classes)
+    for (const ListClass &C : P->classes) {
+        const dopt_list_ptrs *table;
+        if ((rc = place_addresses(C, C.apply, ts, false, true, ws, stream, table))) return rc;
         for (const ListRange &r : C.apply) {
-            const ListPtrs a = slots(C, r, ts);
+            ListAddr a;
+            fill(a, C, r, ts, false, table);
             const int64_t *xoff = reinterpret_cast<const int64_t *>(ws_ptr(ws, C.ws_xoff));
             with_dtype(C.pd, [&](auto pd) {
                 with_state(P->state_kind, [&](auto st) {
@@ -954,6 +1078,7 @@ static int list_copy(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_li
             });
             if ((rc = check_launch(IMPORT ? "launch k_list_import" : "launch k_list_export"))) return rc;
         }
+    }
     return DOPT_OK;
 }
 
@@ -978,8 +1103,11 @@ int dopt_list_init(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
                                       hipMemcpyHostToDevice, stream),
                        "copy list export offsets");
         if (rc) return rc;
+        const dopt_list_ptrs *table;
+        if ((rc = place_addresses(C, C.apply, ts, false, true, ws, stream, table))) return rc;
         for (const ListRange &r : C.apply) {
-            const ListPtrs a = slots(C, r, ts);
+            ListAddr a;
+            fill(a, C, r, ts, false, table);
             with_dtype(C.pd, [&](auto pd) {
                 with_state(P->state_kind, [&](auto st) {
                     k_list_init<decltype(pd)::value, decltype(st)::value><<<r.grid, kBlock, 0, stream>>>(

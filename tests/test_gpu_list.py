@@ -394,6 +394,48 @@ def test_ranks_with_8_bit_moments_exchange_their_record():
         assert D.dopt_step(lay, A.bufs, SHARD_HPS, 1.0, A.workspace, stream)["step_count"] == 2
 
 
+@pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("state", STATES)
+def test_tensors_far_apart(state, n):
+    """Params and grads in turn at either end of 10 GiB, so that no 32-bit
+    distance reaches from one to the next: the results, norm and checkpoint of
+    the same tensors side by side, bit for bit."""
+    rng = np.random.default_rng(n)
+    sizes = [9000] + [int(x) for x in rng.integers(1, 3000, n - 1)]
+    near, far = (H.ListCase(sizes, [("bf16", "bf16")], state, seed=14) for _ in range(2))
+    span, D = 10 << 30, near.D
+    field = torch.zeros(span, dtype=torch.uint8, device="cuda")
+    at = [0, span]
+    moved = {"params": [], "grads": []}
+    for i, x in enumerate(sizes):
+        for name, side in (("params", i % 2), ("grads", 1 - i % 2)):
+            if side:  # from the top down
+                at[1] -= 2 * x + 2
+                a = at[1]
+            else:
+                a = at[0]
+                at[0] += 2 * x + 2
+            v = field[a:a + 2 * x].view(torch.bfloat16)
+            v.copy_(getattr(far, name)[i])
+            moved[name].append(v)
+    far.params, far.grads, far.store = moved["params"], moved["grads"], []
+    far.t = D.list_tensors(far.L, far.params, far.grads, far.A.state)
+    for c in (near, far):
+        c.init()
+    for _ in range(2):
+        a, b = (D.dopt_list_step(c.L, c.t, c.hps, 1.0, c.A.workspace, c.stream) for c in (near, far))
+        assert a == b
+    for x, y in zip(near.snapshot(), far.snapshot()):
+        assert all(np.array_equal(x[k], y[k]) for k in x)
+    xs = [[torch.empty(c.L.numel, device="cuda") for _ in range(3)] for c in (near, far)]
+    for c, x in zip((near, far), xs):
+        D.dopt_list_export(c.L, c.t, *x, c.A.workspace, c.stream)
+        D.dopt_list_import(c.L, c.t, *x, c.A.workspace, c.stream)
+    assert all(torch.equal(u, v) for u, v in zip(*xs))
+    for x, y in zip(near.snapshot(), far.snapshot()):
+        assert all(np.array_equal(x[k], y[k]) for k in x)
+
+
 def test_offsets_beyond_32_bits():
     """A tensor of more than 2^32 bytes and 2^31 elements, and one after it: the
     first and last elements of both, and a stretch across the 2^31st."""
