@@ -249,7 +249,22 @@ _TORCH_DTYPE_NAMES = {"f32": "torch.float32", "bf16": "torch.bfloat16", "f16": "
                       "e4m3": "torch.float8_e4m3fn"}
 
 
-def _dev(x, what: str, dtype: Optional[str] = None, min_numel: int = 0, min_bytes: int = 0) -> int:
+_dtype_names: Dict = {}  # of the element types seen
+
+
+def _dtype_name(dt) -> str:
+    name = _dtype_names.get(dt)
+    if name is None:
+        name = _dtype_names[dt] = str(dt)
+    return name
+
+
+def _what(name) -> str:
+    """An argument's name: a text, or (word, index, word), joined only when it is needed."""
+    return name if isinstance(name, str) else "%s %d %s" % name
+
+
+def _dev(x, what, dtype: Optional[str] = None, min_numel: int = 0, min_bytes: int = 0) -> int:
     """Device address of ``x`` after checking it against what the library
     will touch: a contiguous device tensor of the given element type holding
     at least ``min_numel`` elements / ``min_bytes`` bytes.  The library cannot
@@ -257,20 +272,20 @@ def _dev(x, what: str, dtype: Optional[str] = None, min_numel: int = 0, min_byte
     make its kernels read or write past the end.  A raw integer address is
     passed through: its size and type are then the caller's to guarantee."""
     if x is None:
-        raise DoptError(DOPT_ERR_INVALID, f"{what}: missing")
+        raise DoptError(DOPT_ERR_INVALID, f"{_what(what)}: missing")
     if isinstance(x, int):
         return x
-    if dtype is not None and str(x.dtype) != _TORCH_DTYPE_NAMES[dtype]:
-        raise DoptError(DOPT_ERR_INVALID, f"{what}: dtype {x.dtype}, the layout needs {_TORCH_DTYPE_NAMES[dtype]}")
+    if dtype is not None and _dtype_name(x.dtype) != _TORCH_DTYPE_NAMES[dtype]:
+        raise DoptError(DOPT_ERR_INVALID, f"{_what(what)}: dtype {x.dtype}, the layout needs {_TORCH_DTYPE_NAMES[dtype]}")
     if x.numel() < min_numel:
-        raise DoptError(DOPT_ERR_INVALID, f"{what}: {x.numel()} elements, the layout needs at least {min_numel}")
+        raise DoptError(DOPT_ERR_INVALID, f"{_what(what)}: {x.numel()} elements, the layout needs at least {min_numel}")
     if x.numel() * x.element_size() < min_bytes:
         raise DoptError(DOPT_ERR_INVALID,
-                        f"{what}: {x.numel() * x.element_size()} bytes, the layout needs at least {min_bytes}")
+                        f"{_what(what)}: {x.numel() * x.element_size()} bytes, the layout needs at least {min_bytes}")
     if not x.is_contiguous():
-        raise DoptError(DOPT_ERR_INVALID, f"{what}: not contiguous")
+        raise DoptError(DOPT_ERR_INVALID, f"{_what(what)}: not contiguous")
     if not getattr(x, "is_cuda", False):
-        raise DoptError(DOPT_ERR_INVALID, f"{what}: not a device tensor")
+        raise DoptError(DOPT_ERR_INVALID, f"{_what(what)}: not a device tensor")
     return x.data_ptr()
 
 
@@ -694,10 +709,10 @@ class ListTensors:
         self._held = held
 
 
-def _spans(names_tensors):
-    """(first byte, past the last, name) of each tensor that holds any."""
-    return [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), name) for name, x in names_tensors
-            if x is not None and not isinstance(x, int) and x.numel() > 0]
+def _spans(named):
+    """(first byte, past the last, name) of each of the (name, tensor) that holds any, ascending."""
+    return sorted(((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), name) for name, x in named
+                   if x is not None and not isinstance(x, int) and x.numel() > 0), key=lambda span: span[:2])
 
 
 def list_tensors(lst: TensorList, params: Sequence, grads: Optional[Sequence], state: Dict) -> ListTensors:
@@ -713,38 +728,61 @@ def list_tensors(lst: TensorList, params: Sequence, grads: Optional[Sequence], s
     if grads is not None and len(grads) != len(infos):
         raise DoptError(DOPT_ERR_INVALID, f"{len(grads)} grads, the list has {len(infos)} tensors")
     ptrs = (dopt_list_ptrs * len(infos))()
-    for i, t in enumerate(infos):
-        for key, seq in (("param", params), ("grad", grads)):
-            if seq is None or (t["numel"] == 0 and seq[i] is None):
+    for key, seq in (("param", params), ("grad", grads)):
+        if seq is None:
+            continue
+        for i, (x, t) in enumerate(zip(seq, infos)):
+            n = t["numel"]
+            if n == 0 and x is None:
                 continue
-            x, what = seq[i], f"tensor {i} {key}"
-            addr = _dev(x, what, t[key + "_dtype"])
-            if not isinstance(x, int) and x.numel() != t["numel"]:
-                raise DoptError(DOPT_ERR_INVALID, f"{what}: {x.numel()} elements, the list has {t['numel']}")
-            setattr(ptrs[i], key, addr)
+            if x is not None and not isinstance(x, int) and x.numel() != n:
+                raise DoptError(DOPT_ERR_INVALID, f"tensor {i} {key}: {x.numel()} elements, the list has {n}")
+            setattr(ptrs[i], key, _dev(x, ("tensor", i, key), t[key + "_dtype"]))
     st = dopt_list_state()
     need = lst.state_arrays()
     for name in need:
         setattr(st, name, _dev(state.get(name), f"state {name}", need[name][0], need[name][1]))
-    mine = [(f"tensor {i} param", x) for i, x in enumerate(params)] + [(f"state {n}", state[n]) for n in need]
-    others = [(f"tensor {i} grad", x) for i, x in enumerate(grads or [])]
+    written = _spans([(f"state {n}", state[n]) for n in need] + [(("tensor", i, "param"), x) for i, x in enumerate(params)])
     end, last = 0, ""
-    for lo, hi, name in sorted(_spans(mine)):
+    for lo, hi, name in written:
         if lo < end:
-            raise DoptError(DOPT_ERR_INVALID, f"{name} overlaps {last}")
+            raise DoptError(DOPT_ERR_INVALID, f"{_what(name)} overlaps {_what(last)}")
         end, last = hi, name
-    written = sorted(_spans(mine))
     at = 0
-    for lo, hi, name in sorted(_spans(others)):  # grads may overlap one another: they are only read
+    for lo, hi, name in _spans((("tensor", i, "grad"), x) for i, x in enumerate(grads or [])):
+        # grads may overlap one another: they are only read
         while at < len(written) and written[at][1] <= lo:
             at += 1
         if at < len(written) and written[at][0] < hi:
-            raise DoptError(DOPT_ERR_INVALID, f"{name} overlaps {written[at][2]}")
+            raise DoptError(DOPT_ERR_INVALID, f"{_what(name)} overlaps {_what(written[at][2])}")
     held = list(params) + list(grads or []) + [state[n] for n in need]
     devices = {x.device.index for x in held if x is not None and not isinstance(x, int) and x.numel() > 0}
     if len(devices) > 1:
         raise DoptError(DOPT_ERR_INVALID, f"tensors on several devices: {sorted(devices)}")
     return ListTensors(lst, ptrs, st, grads is not None, devices.pop() if devices else None, held)
+
+
+_torch = None  # the module whose tensors and streams the calls are given
+
+
+def _list_ws(lst: TensorList, workspace, stream, device: Optional[int] = None):
+    """(workspace address, stream) of a call, which the library launches on the
+    current device: the workspace, the stream and the tensors' `device` have
+    to be there."""
+    global _torch
+    ws = _dev(workspace, "workspace", None, 0, lst.workspace_bytes)
+    at = [(device, "tensors")] if device is not None else []
+    at += [(x.device.index, what) for x, what in ((workspace, "workspace"), (stream, "stream"))
+           if x is not None and not isinstance(x, int)]
+    if at:
+        if _torch is None:
+            import torch
+            _torch = torch
+        current = _torch.cuda.current_device()
+        for index, what in at:
+            if index != current:
+                raise DoptError(DOPT_ERR_INVALID, f"{what} on device {index}, the current device is {current}")
+    return ws, _stream(stream)
 
 
 def _list_args(lst: TensorList, t: ListTensors, workspace, stream, need_grads: bool = True):
@@ -753,21 +791,7 @@ def _list_args(lst: TensorList, t: ListTensors, workspace, stream, need_grads: b
         raise DoptError(DOPT_ERR_INVALID, "tensors were marshalled for another list")
     if need_grads and not t.has_grads:
         raise DoptError(DOPT_ERR_INVALID, "tensors were marshalled without grads")
-    ws = _list_ws(lst, workspace)
-    if t.device is not None:
-        import torch  # owns the devices and streams the tensors came with
-        if torch.cuda.current_device() != t.device:
-            raise DoptError(DOPT_ERR_INVALID, f"tensors on device {t.device}, the current device is "
-                                              f"{torch.cuda.current_device()}")
-        for x, what in ((stream, "stream"), (workspace, "workspace")):
-            d = getattr(getattr(x, "device", None), "index", None)
-            if d is not None and d != t.device:
-                raise DoptError(DOPT_ERR_INVALID, f"{what} on device {d}, tensors on device {t.device}")
-    return t.ptrs, ws, _stream(stream)
-
-
-def _list_ws(lst: TensorList, workspace) -> int:
-    return _dev(workspace, "workspace", None, 0, lst.workspace_bytes)
+    return (t.ptrs, *_list_ws(lst, workspace, stream, t.device))
 
 
 def dopt_list_init(lst: TensorList, t: ListTensors, scaler: dopt_scaler_cfg, workspace, stream=None):
@@ -799,7 +823,7 @@ def dopt_list_stats(lst: TensorList, t: ListTensors, workspace, stream=None):
 
 def dopt_list_finalize(lst: TensorList, hparams, max_grad_norm: float, workspace, stream=None):
     hp = hparams if isinstance(hparams, ctypes.Array) else _hparams(hparams)
-    _check(_lib.dopt_list_finalize(lst.handle, hp, len(hp), max_grad_norm, _list_ws(lst, workspace), _stream(stream)))
+    _check(_lib.dopt_list_finalize(lst.handle, hp, len(hp), max_grad_norm, *_list_ws(lst, workspace, stream)))
 
 
 def dopt_list_apply(lst: TensorList, t: ListTensors, workspace, stream=None):
@@ -827,18 +851,18 @@ def dopt_list_import(lst: TensorList, t: ListTensors, master, exp_avg, exp_avg_s
 
 def dopt_list_scalars_get(lst: TensorList, workspace, stream=None) -> Dict:
     st = dopt_state_scalars()
-    _check(_lib.dopt_list_scalars_get(lst.handle, _list_ws(lst, workspace), _stream(stream), ctypes.byref(st)))
+    _check(_lib.dopt_list_scalars_get(lst.handle, *_list_ws(lst, workspace, stream), ctypes.byref(st)))
     return {name: getattr(st, name) for name, _ in st._fields_}
 
 
 def dopt_list_scalars_set(lst: TensorList, workspace, scalars: Dict, stream=None):
     st = dopt_state_scalars(**scalars)
-    _check(_lib.dopt_list_scalars_set(lst.handle, _list_ws(lst, workspace), _stream(stream), ctypes.byref(st)))
+    _check(_lib.dopt_list_scalars_set(lst.handle, *_list_ws(lst, workspace, stream), ctypes.byref(st)))
 
 
 def dopt_list_read_stats(lst: TensorList, workspace, stream=None) -> Dict:
     st = dopt_stats()
-    _check(_lib.dopt_list_read_stats(lst.handle, _list_ws(lst, workspace), _stream(stream), ctypes.byref(st)))
+    _check(_lib.dopt_list_read_stats(lst.handle, *_list_ws(lst, workspace, stream), ctypes.byref(st)))
     return st.as_dict()
 
 

@@ -108,6 +108,21 @@ def test_larger_than_one_grid(state):
 
 
 @pytest.mark.parametrize("state", STATES)
+@pytest.mark.parametrize("sizes", [[2048] * 4, [2048] * 5, [8192], [8193], [2048 * 256], [2048 * 256 + 1],
+                                   [3, 2048 * 128, 7, 2048 * 124]], ids=str)
+def test_launch_rules(sizes, state):
+    """On either side of a whole step in one launch (4 tiles), and of pass 1
+    finished by its last workgroup (64 partials of 4 tiles)."""
+    run(H.ListCase(sizes, [("bf16", "bf16")], state, seed=15, hgroups=[1, 0, 2]))
+
+
+@pytest.mark.parametrize("state", STATES)
+@pytest.mark.parametrize("pairs", [PAIRS[i:i + 4] for i in (0, 3, 5)], ids=lambda p: " ".join("-".join(x) for x in p))
+def test_one_launch_of_mixed_types(pairs, state):
+    run(H.ListCase([1000, 17, 2048, 5], pairs, state, seed=16, hgroups=[2, 0, 1], shift=3), steps=3)
+
+
+@pytest.mark.parametrize("state", STATES)
 def test_no_tensors(state):
     c = H.ListCase([], [("bf16", "bf16")], state)
     c.init()
@@ -244,10 +259,11 @@ def test_step_in_parts_is_the_step(state):
         assert all(np.array_equal(x[k], y[k]) and np.array_equal(x[k], z[k]) for k in x)
 
 
+@pytest.mark.parametrize("sizes", [[40_000, 70, 1, 300], [900, 70, 1], [600_000, 70]], ids=str)
 @pytest.mark.parametrize("state", STATES)
-def test_captured_step(state):
+def test_captured_step(state, sizes):
     """A captured step replayed, with eager work of two lists between the replays, against eager steps."""
-    a, b, other = (H.ListCase([40_000, 70, 1, 300], [("bf16", "bf16"), ("f32", "f32")], state, seed=12) for _ in range(3))
+    a, b, other = (H.ListCase(sizes, [("bf16", "bf16"), ("f32", "f32")], state, seed=12) for _ in range(3))
     D = a.D
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())

@@ -129,6 +129,10 @@ def test_overlaps_are_refused():
          "tensor 1 grad overlaps tensor 1 param")
     g = _dev(100)
     D.list_tensors(L, [b, a[:50]], [g, g[:50]], st)  # shared grads are only read
+    _err(lambda: D.list_tensors(L, [b, b[:50]], None, st), "tensor 0 param overlaps tensor 1 param")
+    both = D.dopt_list_build([D.TensorSpec(256, "f32", "f32")], "f32")
+    w = _dev(256, torch.float32)
+    _err(lambda: D.list_tensors(both, [w], None, {**_raw_state(both), "exp_avg": w}), "param overlaps state exp_avg")
     m = _dev(256, torch.float32)
     _err(lambda: D.list_tensors(L, [b, a[:50]], None, {**st, "exp_avg": m, "exp_avg_sq": m}), "overlaps state")
     _err(lambda: D.list_tensors(L, [b, a[:50]], [_dev(99), g[:50]], st), "tensor 0 grad", "99 elements")
@@ -172,6 +176,24 @@ def test_call_refusals():
     assert lib.dopt_list_step(L.handle, t.ptrs, ctypes.byref(t.state), None, 2, 1.0, 4096, None, None) == -1
     assert lib.dopt_list_step(None, t.ptrs, ctypes.byref(t.state), hp, 2, 1.0, 4096, None, None) == -1
     assert lib.dopt_list_read_stats(L.handle, None, None, None) == -1
+
+
+class _Elsewhere:
+    """Stands for a stream of another device than the current one."""
+    cuda_stream = 0
+
+    class device:
+        index = 5
+
+
+def test_other_devices_are_refused(monkeypatch):
+    L = D.dopt_list_build([spec(100)], "f32")
+    t = D.list_tensors(L, [4096], [4096], _raw_state(L))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    _err(lambda: D.dopt_list_step(L, t, HP, 1.0, 4096, _Elsewhere()), "stream on device 5", "current device is 3")
+    _err(lambda: D.dopt_list_finalize(L, HP, 1.0, 4096, _Elsewhere()), "stream on device 5")
+    t.device = 4
+    _err(lambda: D.dopt_list_apply(L, t, 4096), "tensors on device 4")
 
 
 # ---- the plain encoding that the GPU tests compare with ---------------------------------------
