@@ -581,9 +581,9 @@ __global__ void __launch_bounds__(kBlock) k_list_apply(const ListTile *__restric
 // there is here, and what four waves of a SIMD compute one after the other:
 // groups without elements are left out (pass 2 of a large list, where they
 // are rare, ran 1.5% slower with that test).  On MI355X, back to back, a step
-// of 2,608 bf16 elements in 4 tensors takes 8.8 us, 12 in two launches; four
-// whole tiles take 11.2 with e4m3 moments and 9.3 with fp32 ones, 11.6 and
-// 10.5 in two.
+// of 4 bf16 tensors of 500 elements takes 7.7 us with e4m3 moments and 6.8 with fp32
+// ones, 12.2 and 11.8 in two launches; four whole tiles take 11.3 and 9.3,
+// 11.6 and 10.5 in two.
 // Arrays of the arguments are indexed with scalars: their elements are whole
 // words, for scalar loads ignore the low two bits of each part of an address.
 struct SmallTile {
@@ -632,7 +632,10 @@ __global__ void __launch_bounds__(kSmallTiles * kBlock) k_list_small(SmallArgs a
     __shared__ unsigned long long s_z[kSmallTiles][kBlock / 64];
     __shared__ StepRec s_rec;
     const int mine = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kBlock);  // this quarter's tile
-    const int thread = threadIdx.x % kBlock;
+    // its threads, a wave further round in each quarter: wave w of a workgroup runs on
+    // SIMD w % 4, and the first waves of small tiles, often the only ones with work, would
+    // all wait for one
+    const int thread = (static_cast<int>(threadIdx.x) + mine * 64) % kBlock;
     const SmallTile t = a.tiles[mine];  // of no element beyond n_tiles
     float *const master = a.s.master;
     const DevState cur = *a.st;
