@@ -39,7 +39,9 @@
  * that use one workspace must not overlap in time.  dopt_list_stats,
  * _finalize, _prepare, _apply, _step (out == NULL), _export and _import only
  * launch kernels and may be captured into a HIP graph; a replay uses the
- * addresses that the captured call was given.
+ * addresses and hyper-parameters that the captured call was given.  A tensor
+ * without a grad in a step has no place in that step's list: a null grad is
+ * refused.
  */
 #ifndef DOPT_LIST_H
 #define DOPT_LIST_H

@@ -702,10 +702,10 @@ def shard_views(layout: Layout, lst: TensorList, bufs: Sequence[Dict]):
 class ListTensors:
     """A list's params, grads and state, checked and marshalled (make it once
     with list_tensors() and pass it to every call; make it anew when a tensor
-    is replaced).  Holds the tensors, so that their memory lives as long."""
+    is replaced).  Holds the list and the tensors, so that they live as long."""
 
     def __init__(self, lst: TensorList, ptrs, state, has_grads: bool, device: Optional[int], held):
-        self.handle, self.ptrs, self.state, self.has_grads, self.device = lst.handle.value, ptrs, state, has_grads, device
+        self.lst, self.ptrs, self.state, self.has_grads, self.device = lst, ptrs, state, has_grads, device
         self._held = held
 
 
@@ -787,7 +787,7 @@ def _list_ws(lst: TensorList, workspace, stream, device: Optional[int] = None):
 
 def _list_args(lst: TensorList, t: ListTensors, workspace, stream, need_grads: bool = True):
     """(tensors, workspace address, stream) of a call, after checking that they belong together."""
-    if t.handle != lst.handle.value:
+    if t.lst is not lst:
         raise DoptError(DOPT_ERR_INVALID, "tensors were marshalled for another list")
     if need_grads and not t.has_grads:
         raise DoptError(DOPT_ERR_INVALID, "tensors were marshalled without grads")

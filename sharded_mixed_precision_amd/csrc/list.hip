@@ -19,6 +19,7 @@
 //   a lane owns 4 elements in each half of its wave's 512, so that each
 //   16-byte access of a wave covers a whole KB, all accesses nontemporal 5.02 / 3.16 ms
 //   runs of 16 consecutive tiles on one XCD (tile_of)                    4.95 / 3.04 ms
+// (and launched in pieces, list_launch_tiles, 4% less for the first).
 // Nontemporal accesses lose in the first layout, whose instructions leave
 // half of every line they touch to the next one.
 //
@@ -250,8 +251,8 @@ __device__ __forceinline__ void store_codes(void *base, int64_t e, int n, uint32
 // The tile of workgroup b of n.  Workgroups go to the 8 XCDs in turn; runs of
 // kXcdRun consecutive tiles are dealt to one XCD, so that the lines two tiles
 // share (a tile's scales are half a line) meet in one L2, and each XCD's
-// requests run along the arrays.  On MI355X 16 was the best of 1 to 64 for
-// pass 2 with e4m3 moments (1.0e9 elements: 3.16 ms at 1, 3.34 at 4, 3.22 at 8, 3.04 at
+// requests run along the arrays.  On MI355X 16 and 32 were the best of 1 to 64
+// for pass 2 with e4m3 moments (1.0e9 elements: 3.16 ms at 1, 3.34 at 4, 3.22 at 8, 3.04 at
 // 16, 3.03 at 32, 3.09 at 64) and with fp32 moments (5.02, 4.99, 4.98, 4.95, 4.98, 5.16).
 constexpr int64_t kXcds = 8, kXcdRun = 16;
 __device__ __forceinline__ int64_t tile_of(int64_t b, int64_t n) {

@@ -178,6 +178,18 @@ def test_call_refusals():
     assert lib.dopt_list_read_stats(L.handle, None, None, None) == -1
 
 
+def test_tensors_of_a_freed_list_are_refused():
+    """Lists built and dropped in turn, whose handles may reuse an address:
+    tensors marshalled for one never pass for the next."""
+    old = []
+    for n in range(1, 40):
+        L = D.dopt_list_build([spec(n)], "f32")
+        for t in old:
+            _err(lambda: D.dopt_list_stats(L, t, 4096 + 128), "another list")
+        old.append(D.list_tensors(L, [4096], [4096], _raw_state(L)))
+        del L
+
+
 class _Elsewhere:
     """Stands for a stream of another device than the current one."""
     cuda_stream = 0
