@@ -53,19 +53,19 @@ REGION_ELEMS = 1 << 27  # arena elements per placement region
 # bytes_per_launch = FETCH_SIZE * 2.0 + WRITE_SIZE * 1.0 (KiB -> B), the scale
 # factors read off a 1 GiB fp32 copy.
 MEASURED_TRAFFIC = {
-    # FETCH_SIZE 106,556.68 KiB * 2.0 + WRITE_SIZE 213,569.33 KiB * 1.0, averaged over 523 dispatches
+    # FETCH_SIZE 106,598.47 KiB * 2.0 + WRITE_SIZE 213,623.38 KiB * 1.0, averaged over 37 dispatches
     # (profiles/k_apply_gpt2-small_kernel_trace.md)
-    "gpt2-small": {"src": "53d67aba3946e0d0", "bytes_per_launch": 436923071},
-    # FETCH_SIZE 46,269,131.90 KiB * 2.0 + WRITE_SIZE 92,127,420.10 KiB * 1.0, averaged over the 37
+    "gpt2-small": {"src": "615d4ab0446f599a", "bytes_per_launch": 437064008},
+    # FETCH_SIZE 46,269,127.59 KiB * 2.0 + WRITE_SIZE 92,127,649.05 KiB * 1.0, averaged over the 37
     # full-window dispatches that were not overflow-skipped (profiles/k_apply_dense-7b_kernel_trace.md)
-    "dense-7b": {"src": "53d67aba3946e0d0", "bytes_per_launch": 189097660323},
-    # k_apply_bnd: FETCH_SIZE 7,569,690.44 KiB * 2.0 + WRITE_SIZE 15,072,217.06 KiB * 1.0, averaged over 37
+    "dense-7b": {"src": "615d4ab0446f599a", "bytes_per_launch": 189097885932},
+    # k_apply_bnd: FETCH_SIZE 7,569,683.60 KiB * 2.0 + WRITE_SIZE 15,072,194.97 KiB * 1.0, averaged over 37
     # dispatches (profiles/k_apply_llama3-70b_kernel_trace.md)
-    "llama3-70b": {"src": "53d67aba3946e0d0", "bytes_per_launch": 30936676290},
+    "llama3-70b": {"src": "615d4ab0446f599a", "bytes_per_launch": 30936639662},
     # both buffers' launches of one step (the bf16-param / fp32-grad window and the fp32 norms):
-    # FETCH_SIZE 7,872,477.81 + 310.13 KiB * 2.0 + WRITE_SIZE 13,723,600.49 + 390.00 KiB * 1.0, averaged
+    # FETCH_SIZE 7,872,472.22 + 309.12 KiB * 2.0 + WRITE_SIZE 13,723,545.40 + 390.00 KiB * 1.0, averaged
     # over 37 dispatches each (profiles/k_apply_llama3-8b_kernel_trace.md)
-    "llama3-8b": {"src": "53d67aba3946e0d0", "bytes_per_launch": 30176835961},
+    "llama3-8b": {"src": "615d4ab0446f599a", "bytes_per_launch": 30176766034},
 }
 
 
@@ -76,8 +76,8 @@ def progress(msg: str):
 
 def _src_sha() -> str:
     h = hashlib.sha256()
-    for f in ("sharded_mixed_precision_amd/csrc/step.hip", "sharded_mixed_precision_amd/csrc/internal.h"):
-        with open(os.path.join(ROOT, f), "rb") as fh:
+    for f in ("step.hip", "device.h", "internal.h"):
+        with open(os.path.join(ROOT, "sharded_mixed_precision_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
 
