@@ -11,15 +11,15 @@
 //
 // Every pass streams its arrays once and is bound by HBM: pass 2 without its
 // arithmetic takes the same time.  A list is cut into tiles of 2048 elements,
-// one 256-thread workgroup each, and what the layout decides is how well the
+// one workgroup each, and what the layout decides is how well the
 // streams run.  Measured on MI355X, pass 2 of 1.1e9 bf16 params with fp32
 // moments / of 1.0e9 with fp32 grads and e4m3 moments:
 //   grid-stride over 16384 workgroups, 8 consecutive elements per lane   5.65 / 3.85 ms
 //   one workgroup per tile                                               5.46 / 3.52 ms
-//   a lane owns 4 elements in each half of its wave's 512, so that each
+//   a lane owns 4 elements in each half of its wave's 512: each
 //   16-byte access of a wave covers a whole KB, all accesses nontemporal 5.02 / 3.16 ms
 //   runs of 16 consecutive tiles on one XCD (tile_of)                    4.95 / 3.04 ms
-// (and launched in pieces, list_launch_tiles, 4% less for the first).
+//   512 threads to a tile, a lane with 4 elements, launched in pieces    4.95 / 2.85 ms
 // Nontemporal accesses lose in the first layout, whose instructions leave
 // half of every line they touch to the next one.
 //
@@ -85,7 +85,8 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kQuad = 4;               // consecutive elements of a lane
 constexpr int kGroup = 64 * kQuad;     // what a wave's access covers
-constexpr int kGroups = kVec / kQuad;  // groups of a wave, back to back
+constexpr int kGroups = kVec / kQuad;  // groups of a wave, back to back, where kBlock threads share a tile
+constexpr int kWide = kTile / kQuad;   // threads that share a tile with one group to a wave
 
 // The raw bytes of 4 consecutive elements, and their type at the element's alignment.
 template <int DT>
@@ -261,12 +262,6 @@ __device__ __forceinline__ int64_t tile_of(int64_t b, int64_t n) {
     return b / (kXcds * kXcdRun) * (kXcds * kXcdRun) + b % kXcds * kXcdRun + b / kXcds % kXcdRun;
 }
 
-// Whether a wave's group of a tile holds an element (wave-uniform).
-__device__ __forceinline__ bool group_lives(const ListTile &d, int group, int thread) {
-    return __builtin_amdgcn_readfirstlane(thread >> 6) * (kGroup * kGroups) + group * kGroup <
-           static_cast<int>(d.packed & 0xffffu);
-}
-
 // A lane's 4 elements of one group of its tile.
 struct Place {
     int64_t e;      // the first within the tensor
@@ -274,13 +269,22 @@ struct Place {
     int n;          // how many of them exist (<= 0: none)
 };
 
-// `thread`: among the kBlock that share the tile.
+// Where a lane's 4 elements of a group start in the tile; `thread` is among
+// the kTile / (GROUPS * kQuad) that share it.
+template <int GROUPS>
 __device__ __forceinline__ int lane_offset(int group, int thread) {
-    return (thread >> 6) * (kGroup * kGroups) + group * kGroup + (thread & 63) * kQuad;
+    return (thread >> 6) * (kGroup * GROUPS) + group * kGroup + (thread & 63) * kQuad;
 }
+template <int GROUPS>
 __device__ __forceinline__ Place place_of(const ListTile &d, int group, int thread) {
-    const int l = lane_offset(group, thread);
+    const int l = lane_offset<GROUPS>(group, thread);
     return Place{int64_t(d.tile) * kTile + l, int64_t(d.block) * kListBlock + l, static_cast<int>(d.packed & 0xffffu) - l};
+}
+
+// Whether a wave's group of a tile holds an element (wave-uniform).
+__device__ __forceinline__ bool group_lives(const ListTile &d, int group, int thread) {
+    return __builtin_amdgcn_readfirstlane(thread >> 6) * (kGroup * kGroups) + group * kGroup <
+           static_cast<int>(d.packed & 0xffffu);
 }
 
 struct StateArrays {
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradAddr add
             const void *g = grad_of<GD>(addr, d.index, a.first);
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
-                const Place L = place_of(d, k, threadIdx.x);
+                const Place L = place_of<kGroups>(d, k, threadIdx.x);
                 n[u][k] = t0 + u < a.t_end ? L.n : 0;
                 raw[u][k] = load4<GD>(g, L.e, n[u][k]);
             }
@@ -536,40 +540,33 @@ __global__ void k_list_done(uint32_t *done) {
 
 // ---- pass 2 -------------------------------------------------------------------------
 
+// 512 threads to a tile, one group to a wave: as fast as 256 with two for fp32
+// moments and faster for e4m3 ones (1.0e9 elements 2.85 and 2.92 ms, 1.8e7 in 500
+// tensors 56.9 and 59.0 us; 128 with four lose 1 to 8%).
 template <int PD, int GD, int ST>
-__global__ void __launch_bounds__(kBlock) k_list_apply(const ListTile *__restrict__ tiles, int64_t t_begin,
-                                                      int64_t t_end, int32_t first, StateArrays s,
-                                                      const StepRec *__restrict__ rec, ListAddr addr) {
+__global__ void __launch_bounds__(kWide) k_list_apply(const ListTile *__restrict__ tiles, int64_t t_begin,
+                                                     int64_t t_end, int32_t first, StateArrays s,
+                                                     const StepRec *__restrict__ rec, ListAddr addr) {
     const int skip = rec->skip;  // loaded beside the tile: a skipped step touches no data
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
     if (skip) return;
     const dopt_list_ptrs q = ptrs_of<PD, GD>(addr, d.index, first);
     const Hp h = load_hp(rec, d.packed >> 16);
-    const float inv = rec->inv_scale, clip = rec->clip;
-    const int clip_on = rec->clip_on;
-    Place L[kGroups];
-    typename Quad<GD>::Raw graw[kGroups];
-    u32x4 praw[kGroups];
-    Moments<ST> mom[kGroups];
+    const Place L = place_of<1>(d, 0, threadIdx.x);
+    const auto graw = load4<GD>(q.grad, L.e, L.n);
+    const u32x4 praw = PD == DOPT_F32 ? load4<DOPT_F32>(q.param, L.e, L.n) : load4<DOPT_F32>(s.master, L.arena, L.n);
+    Moments<ST> mom;
+    mom.load(s, L);
+    float g[kQuad], p[kQuad], a[kQuad], b[kQuad], r[kQuad];
+    unpack4<GD>(graw, g);
+    unpack4<DOPT_F32>(praw, p);
+    mom.decode(a, b);
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        L[k] = place_of(d, k, threadIdx.x);
-        graw[k] = load4<GD>(q.grad, L[k].e, L[k].n);
-        praw[k] = PD == DOPT_F32 ? load4<DOPT_F32>(q.param, L[k].e, L[k].n) : load4<DOPT_F32>(s.master, L[k].arena, L[k].n);
-        mom[k].load(s, L[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        float g[kQuad], p[kQuad], a[kQuad], b[kQuad], r[kQuad];
-        unpack4<GD>(graw[k], g);
-        unpack4<DOPT_F32>(praw[k], p);
-        mom[k].decode(a, b);
-#pragma unroll
-        for (int j = 0; j < kQuad; ++j) r[j] = adamw_root(g[j], p[j], a[j], b[j], inv, clip_on, clip, h);
-        Moments<ST>::store(s, L[k], a, b, r);
-        if (PD != DOPT_F32) store4<DOPT_F32>(s.master, L[k].arena, L[k].n, p);
-        store4<PD>(q.param, L[k].e, L[k].n, p);
-    }
+    for (int j = 0; j < kQuad; ++j)
+        r[j] = adamw_root(g[j], p[j], a[j], b[j], rec->inv_scale, rec->clip_on, rec->clip, h);
+    Moments<ST>::store(s, L, a, b, r);
+    if (PD != DOPT_F32) store4<DOPT_F32>(s.master, L.arena, L.n, p);
+    store4<PD>(q.param, L.e, L.n, p);
 }
 
 // ---- the whole step of a small list ---------------------------------------------------
@@ -646,7 +643,7 @@ __global__ void __launch_bounds__(kSmallTiles * kBlock) k_list_small(SmallArgs a
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
         if (!group_lives(t.t, k, thread)) continue;
-        L[k] = place_of(t.t, k, thread);
+        L[k] = place_of<kGroups>(t.t, k, thread);
         graw[k] = load4_any(t.gd, t.p.grad, L[k].e, L[k].n);
         praw[k] = t.pd == DOPT_F32 ? load4<DOPT_F32>(t.p.param, L[k].e, L[k].n)
                                    : load4<DOPT_F32>(master, L[k].arena, L[k].n);
@@ -676,7 +673,7 @@ __global__ void __launch_bounds__(kSmallTiles * kBlock) k_list_small(SmallArgs a
                 if (!group_lives(d, k, thread)) continue;  // it would add +0
 #pragma unroll
                 for (int j = 0; j < kQuad; ++j)
-                    add_grad(s_g[u][k][j][thread] * cur.inv_scale, lane_offset(k, thread) + j < count, acc, zeros);
+                    add_grad(s_g[u][k][j][thread] * cur.inv_scale, lane_offset<kGroups>(k, thread) + j < count, acc, zeros);
             }
         }
         unsigned long long z = zeros;
@@ -734,6 +731,10 @@ struct ExportArrays {
     float *p, *m, *v;
 };
 
+// The import takes a lane of a tile's 512 per 4 elements, as pass 2; the
+// export, which writes three arrays for one and a half that it reads, runs
+// better with 256 and two groups each (1.2e8 elements on MI355X: import 395 and
+// 411 us, export 401 and 377).
 template <int PD, int ST>
 __global__ void __launch_bounds__(kBlock) k_list_export(const ListTile *__restrict__ tiles, int64_t t_begin,
                                                        int64_t t_end, int32_t first,
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(kBlock) k_list_export(const ListTile *__restri
     Moments<ST> mom[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        L[k] = place_of(d, k, threadIdx.x);
+        L[k] = place_of<kGroups>(d, k, threadIdx.x);
         praw[k] = PD == DOPT_F32 ? load4<DOPT_F32>(param, L[k].e, L[k].n) : load4<DOPT_F32>(s.master, L[k].arena, L[k].n);
         mom[k].load(s, L[k]);
     }
@@ -763,64 +764,53 @@ __global__ void __launch_bounds__(kBlock) k_list_export(const ListTile *__restri
 }
 
 template <int PD, int ST>
-__global__ void __launch_bounds__(kBlock) k_list_import(const ListTile *__restrict__ tiles, int64_t t_begin,
-                                                       int64_t t_end, int32_t first,
-                                                       const int64_t *__restrict__ xoff, StateArrays s,
-                                                       ExportArrays x, ListAddr addr) {
+__global__ void __launch_bounds__(kWide) k_list_import(const ListTile *__restrict__ tiles, int64_t t_begin,
+                                                      int64_t t_end, int32_t first,
+                                                      const int64_t *__restrict__ xoff, StateArrays s,
+                                                      ExportArrays x, ListAddr addr) {
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
     void *param = ptrs_of<PD, PD>(addr, d.index, first).param;
     const int64_t o = xoff[d.index];
-    Place L[kGroups];
-    u32x4 praw[kGroups], araw[kGroups], braw[kGroups];
+    const Place L = place_of<1>(d, 0, threadIdx.x);
+    const u32x4 praw = load4<DOPT_F32>(x.p, o + L.e, L.n);
+    const u32x4 araw = load4<DOPT_F32>(x.m, o + L.e, L.n);
+    const u32x4 braw = load4<DOPT_F32>(x.v, o + L.e, L.n);
+    float p[kQuad], a[kQuad], b[kQuad], r[kQuad];
+    unpack4<DOPT_F32>(praw, p);
+    unpack4<DOPT_F32>(araw, a);
+    unpack4<DOPT_F32>(braw, b);
+    if (PD != DOPT_F32) store4<DOPT_F32>(s.master, L.arena, L.n, p);
+    store4<PD>(param, L.e, L.n, p);
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        L[k] = place_of(d, k, threadIdx.x);
-        praw[k] = load4<DOPT_F32>(x.p, o + L[k].e, L[k].n);
-        araw[k] = load4<DOPT_F32>(x.m, o + L[k].e, L[k].n);
-        braw[k] = load4<DOPT_F32>(x.v, o + L[k].e, L[k].n);
-    }
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        float p[kQuad], a[kQuad], b[kQuad], r[kQuad];
-        unpack4<DOPT_F32>(praw[k], p);
-        unpack4<DOPT_F32>(araw[k], a);
-        unpack4<DOPT_F32>(braw[k], b);
-        if (PD != DOPT_F32) store4<DOPT_F32>(s.master, L[k].arena, L[k].n, p);
-        store4<PD>(param, L[k].e, L[k].n, p);
-#pragma unroll
-        for (int j = 0; j < kQuad; ++j) r[j] = ST == DOPT_STATE_E4M3 ? sqrtf(b[j]) : 0.0f;
-        Moments<ST>::store(s, L[k], a, b, r);
-    }
+    for (int j = 0; j < kQuad; ++j) r[j] = ST == DOPT_STATE_E4M3 ? sqrtf(b[j]) : 0.0f;
+    Moments<ST>::store(s, L, a, b, r);
 }
 
 // Masters from the params, everything else zero, whole blocks of the arena.
 template <int PD, int ST>
-__global__ void __launch_bounds__(kBlock) k_list_init(const ListTile *__restrict__ tiles, int64_t t_begin,
-                                                     int32_t first, bool masters, StateArrays s, ListAddr addr) {
+__global__ void __launch_bounds__(kWide) k_list_init(const ListTile *__restrict__ tiles, int64_t t_begin,
+                                                    int32_t first, bool masters, StateArrays s, ListAddr addr) {
     const float z[kQuad] = {0, 0, 0, 0};
     const ListTile d = tiles[t_begin + blockIdx.x];
-    const int whole = (static_cast<int>(d.packed & 0xffffu) + kListBlock - 1) / kListBlock * kListBlock;
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        const Place L = place_of(d, k, threadIdx.x);
-        const int n = L.n + whole - static_cast<int>(d.packed & 0xffffu);  // slots of the tensor's blocks
-        if (n <= 0) continue;
-        if (masters) {
-            float p[kQuad] = {0, 0, 0, 0};
-            if (PD != DOPT_F32) unpack4<PD>(load4<PD>(ptrs_of<PD, PD>(addr, d.index, first).param, L.e, L.n), p);
-            store4<DOPT_F32>(s.master, L.arena, n, p);
+    const int count = static_cast<int>(d.packed & 0xffffu);
+    const Place L = place_of<1>(d, 0, threadIdx.x);
+    const int n = L.n + (count + kListBlock - 1) / kListBlock * kListBlock - count;  // slots of the tensor's blocks
+    if (n <= 0) return;
+    if (masters) {
+        float p[kQuad] = {0, 0, 0, 0};
+        if (PD != DOPT_F32) unpack4<PD>(load4<PD>(ptrs_of<PD, PD>(addr, d.index, first).param, L.e, L.n), p);
+        store4<DOPT_F32>(s.master, L.arena, n, p);
+    }
+    if constexpr (ST == DOPT_STATE_E4M3) {
+        store_codes(s.m, L.arena, n, 0);
+        store_codes(s.v, L.arena, n, 0);
+        if ((threadIdx.x & 31) == 0) {
+            s.ms[L.arena / kListBlock] = 0.0f;
+            s.vs[L.arena / kListBlock] = 0.0f;
         }
-        if constexpr (ST == DOPT_STATE_E4M3) {
-            store_codes(s.m, L.arena, n, 0);
-            store_codes(s.v, L.arena, n, 0);
-            if ((threadIdx.x & 31) == 0) {
-                s.ms[L.arena / kListBlock] = 0.0f;
-                s.vs[L.arena / kListBlock] = 0.0f;
-            }
-        } else {
-            store4<DOPT_F32>(s.m, L.arena, n, z);
-            store4<DOPT_F32>(s.v, L.arena, n, z);
-        }
+    } else {
+        store4<DOPT_F32>(s.m, L.arena, n, z);
+        store4<DOPT_F32>(s.v, L.arena, n, z);
     }
 }
 
@@ -1018,7 +1008,7 @@ static int launch_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const
                 with_dtype(C.gd, [&](auto gd) {
                     with_state(P->state_kind, [&](auto st) {
                         k_list_apply<decltype(pd)::value, decltype(gd)::value, decltype(st)::value>
-                            <<<r.grid, kBlock, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, s, rec, a);
+                            <<<r.grid, kWide, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, s, rec, a);
                     });
                 });
             });
@@ -1077,7 +1067,7 @@ static int list_copy(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_li
                 with_state(P->state_kind, [&](auto st) {
                     constexpr int PD = decltype(pd)::value, ST = decltype(st)::value;
                     if (IMPORT)
-                        k_list_import<PD, ST><<<r.grid, kBlock, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, xoff, s, x, a);
+                        k_list_import<PD, ST><<<r.grid, kWide, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, xoff, s, x, a);
                     else
                         k_list_export<PD, ST><<<r.grid, kBlock, 0, stream>>>(tiles_of(C, ws), r.t0, r.t1, r.first, xoff, s, x, a);
                 });
@@ -1116,7 +1106,7 @@ int dopt_list_init(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
             fill(a, C, r, ts, false, table);
             with_dtype(C.pd, [&](auto pd) {
                 with_state(P->state_kind, [&](auto st) {
-                    k_list_init<decltype(pd)::value, decltype(st)::value><<<r.grid, kBlock, 0, stream>>>(
+                    k_list_init<decltype(pd)::value, decltype(st)::value><<<r.grid, kWide, 0, stream>>>(
                         tiles_of(C, ws), r.t0, r.first, P->has_master, s, a);
                 });
             });
