@@ -81,6 +81,8 @@ struct ListRange {  // tiles [t0, t1) of `count` consecutive tensors of a class,
     int32_t partial_base = 0;
 };
 
+constexpr int kDtypes = 3;
+
 // The tensors of one (param dtype, grad dtype), empty ones left out.
 struct ListClass {
     int32_t pd = 0, gd = 0;

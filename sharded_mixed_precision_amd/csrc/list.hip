@@ -872,12 +872,14 @@ struct Span {
     }
 };
 
-// Whether the addresses of every launch of a class fit its arguments; if not,
-// writes them into the workspace.
-static int place_addresses(const ListClass &C, const std::vector<ListRange> &ranges, const dopt_list_ptrs *ts, bool grads,
-                           bool params, void *ws, hipStream_t stream, const dopt_list_ptrs *&table) {
-    table = nullptr;
-    bool fit = true;
+// Per class the table of its addresses in the workspace, or null where every
+// launch's addresses fit its arguments.
+struct Tables {
+    const dopt_list_ptrs *of[kDtypes * kDtypes];  // a class per pair of element types
+};
+
+static bool fits(const ListClass &C, const std::vector<ListRange> &ranges, const dopt_list_ptrs *ts, bool grads,
+                 bool params) {
     for (const ListRange &r : ranges) {
         Span g, p;
         for (int32_t i = r.first; i < r.first + r.count; ++i) {
@@ -885,21 +887,32 @@ static int place_addresses(const ListClass &C, const std::vector<ListRange> &ran
             if (grads) g.add(t.grad);
             if (params) p.add(t.param);
         }
-        fit = fit && g.fits(C.gd) && p.fits(C.pd);
+        if (!g.fits(C.gd) || !p.fits(C.pd)) return false;
     }
-    if (fit) return DOPT_OK;
-    dopt_list_ptrs *dst = reinterpret_cast<dopt_list_ptrs *>(ws_ptr(ws, C.ws_addr));
-    const int32_t n = static_cast<int32_t>(C.tensors.size());
-    for (int32_t f = 0; f < n; f += kListPut) {
-        PutAddr a;
-        std::memset(&a, 0, sizeof a);
-        const int32_t m = std::min(kListPut, n - f);
-        for (int32_t i = 0; i < m; ++i) a.p[i] = ts[C.tensors[static_cast<size_t>(f + i)]];
-        k_list_put<<<1, kBlock, 0, stream>>>(dst + f, m, a);
-        const int rc = check_launch("launch k_list_put");
-        if (rc) return rc;
+    return true;
+}
+
+// Writes the addresses of the classes that need it into the workspace, for
+// pass 1, pass 2 (or a copy, which takes no grads) or both.
+static int place_addresses(const dopt_list *P, const dopt_list_ptrs *ts, bool pass1, bool pass2, bool grads, void *ws,
+                           hipStream_t stream, Tables &tables) {
+    for (size_t c = 0; c < P->classes.size(); ++c) {
+        const ListClass &C = P->classes[c];
+        tables.of[c] = nullptr;
+        if ((!pass1 || fits(C, C.stats, ts, true, false)) && (!pass2 || fits(C, C.apply, ts, grads, true))) continue;
+        dopt_list_ptrs *dst = reinterpret_cast<dopt_list_ptrs *>(ws_ptr(ws, C.ws_addr));
+        const int32_t n = static_cast<int32_t>(C.tensors.size());
+        for (int32_t f = 0; f < n; f += kListPut) {
+            PutAddr a;
+            std::memset(&a, 0, sizeof a);
+            const int32_t m = std::min(kListPut, n - f);
+            for (int32_t i = 0; i < m; ++i) a.p[i] = ts[C.tensors[static_cast<size_t>(f + i)]];
+            k_list_put<<<1, kBlock, 0, stream>>>(dst + f, m, a);
+            const int rc = check_launch("launch k_list_put");
+            if (rc) return rc;
+        }
+        tables.of[c] = dst;
     }
-    table = dst;
     return DOPT_OK;
 }
 
@@ -951,8 +964,8 @@ static void with_state(int kind, F f) {
 }
 
 // Pass 1 over every class; fa null: the record only.
-static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void *ws, hipStream_t stream,
-                             const FinalizeArgs *fa) {
+static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, const Tables &tables, void *ws,
+                             hipStream_t stream, const FinalizeArgs *fa) {
     StatsArgs a;
     std::memset(&a, 0, sizeof a);
     a.total = P->total_partials;
@@ -965,14 +978,12 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void 
     a.rec = reinterpret_cast<Record *>(ws_ptr(ws, kWsRecord));
     a.sr = reinterpret_cast<StepRec *>(ws_ptr(ws, kWsStepRec));
     a.out = reinterpret_cast<dopt_stats *>(ws_ptr(ws, kWsStats));
-    for (const ListClass &C : P->classes) {
+    for (size_t c = 0; c < P->classes.size(); ++c) {
+        const ListClass &C = P->classes[c];
         a.tiles = tiles_of(C, ws);
-        const dopt_list_ptrs *table;
-        int rc = place_addresses(C, C.stats, ts, true, false, ws, stream, table);
-        for (size_t k = 0; rc == DOPT_OK && k < C.stats.size(); ++k) {
-            const ListRange &r = C.stats[k];
+        for (const ListRange &r : C.stats) {
             GradAddr g;
-            fill(g, C, r, ts, table);
+            fill(g, C, r, ts, tables.of[c]);
             a.t_begin = r.t0;
             a.t_end = r.t1;
             a.first = r.first;
@@ -981,11 +992,11 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void 
                 if (fused) k_list_stats<decltype(gd)::value, true><<<r.grid, kBlock, 0, stream>>>(a, g);
                 else k_list_stats<decltype(gd)::value, false><<<r.grid, kBlock, 0, stream>>>(a, g);
             });
-            rc = check_launch("launch k_list_stats");
-        }
-        if (rc) {
-            k_list_done<<<1, 64, 0, stream>>>(a.done);  // the pass is not complete: forget its count
-            return rc;
+            const int rc = check_launch("launch k_list_stats");
+            if (rc) {
+                k_list_done<<<1, 64, 0, stream>>>(a.done);  // the pass is not complete: forget its count
+                return rc;
+            }
         }
     }
     if (fused) return DOPT_OK;
@@ -994,16 +1005,14 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void 
 }
 
 // Pass 2 over every class.
-static int launch_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const StateArrays &s, void *ws,
-                             hipStream_t stream) {
+static int launch_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const Tables &tables, const StateArrays &s,
+                             void *ws, hipStream_t stream) {
     const StepRec *rec = reinterpret_cast<const StepRec *>(ws_ptr(ws, kWsStepRec));
-    for (const ListClass &C : P->classes) {
-        const dopt_list_ptrs *table;
-        int rc = place_addresses(C, C.apply, ts, true, true, ws, stream, table);
-        if (rc) return rc;
+    for (size_t c = 0; c < P->classes.size(); ++c) {
+        const ListClass &C = P->classes[c];
         for (const ListRange &r : C.apply) {
             ListAddr a;
-            fill(a, C, r, ts, true, table);
+            fill(a, C, r, ts, true, tables.of[c]);
             with_dtype(C.pd, [&](auto pd) {
                 with_dtype(C.gd, [&](auto gd) {
                     with_state(P->state_kind, [&](auto st) {
@@ -1012,7 +1021,8 @@ static int launch_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const
                     });
                 });
             });
-            if ((rc = check_launch("launch k_list_apply"))) return rc;
+            const int rc = check_launch("launch k_list_apply");
+            if (rc) return rc;
         }
     }
     return DOPT_OK;
@@ -1056,12 +1066,13 @@ static int list_copy(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_li
         if ((reinterpret_cast<uintptr_t>(x.p) | reinterpret_cast<uintptr_t>(x.m) | reinterpret_cast<uintptr_t>(x.v)) % 4)
             return fail(DOPT_ERR_INVALID, "export array not 4-byte aligned");
     }
-    for (const ListClass &C : P->classes) {
-        const dopt_list_ptrs *table;
-        if ((rc = place_addresses(C, C.apply, ts, false, true, ws, stream, table))) return rc;
+    Tables tables;
+    if ((rc = place_addresses(P, ts, false, true, false, ws, stream, tables))) return rc;
+    for (size_t c = 0; c < P->classes.size(); ++c) {
+        const ListClass &C = P->classes[c];
         for (const ListRange &r : C.apply) {
             ListAddr a;
-            fill(a, C, r, ts, false, table);
+            fill(a, C, r, ts, false, tables.of[c]);
             const int64_t *xoff = reinterpret_cast<const int64_t *>(ws_ptr(ws, C.ws_xoff));
             with_dtype(C.pd, [&](auto pd) {
                 with_state(P->state_kind, [&](auto st) {
@@ -1090,7 +1101,10 @@ int dopt_list_init(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
     int rc = check_list(P, ws);
     if (rc || (rc = check_tensors(P, ts, false, true)) || (rc = check_state(P, state, s)) || (rc = check_scaler(sc)))
         return rc;
-    for (const ListClass &C : P->classes) {
+    Tables tables;
+    if ((rc = place_addresses(P, ts, false, true, false, ws, stream, tables))) return rc;
+    for (size_t c = 0; c < P->classes.size(); ++c) {
+        const ListClass &C = P->classes[c];
         rc = hip_check(hipMemcpyAsync(ws_ptr(ws, C.ws_tiles), C.tiles.data(), C.tiles.size() * sizeof(ListTile),
                                       hipMemcpyHostToDevice, stream),
                        "copy list tiles");
@@ -1099,11 +1113,9 @@ int dopt_list_init(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
                                       hipMemcpyHostToDevice, stream),
                        "copy list export offsets");
         if (rc) return rc;
-        const dopt_list_ptrs *table;
-        if ((rc = place_addresses(C, C.apply, ts, false, true, ws, stream, table))) return rc;
         for (const ListRange &r : C.apply) {
             ListAddr a;
-            fill(a, C, r, ts, false, table);
+            fill(a, C, r, ts, false, tables.of[c]);
             with_dtype(C.pd, [&](auto pd) {
                 with_state(P->state_kind, [&](auto st) {
                     k_list_init<decltype(pd)::value, decltype(st)::value><<<r.grid, kWide, 0, stream>>>(
@@ -1122,7 +1134,9 @@ int dopt_list_init(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
 int dopt_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, void *ws, hipStream_t stream) {
     int rc = check_list(P, ws);
     if (rc || (rc = check_tensors(P, ts, true, false))) return rc;
-    return launch_list_stats(P, ts, ws, stream, nullptr);
+    Tables tables;
+    if ((rc = place_addresses(P, ts, true, false, true, ws, stream, tables))) return rc;
+    return launch_list_stats(P, ts, tables, ws, stream, nullptr);
 }
 
 int dopt_list_finalize(const dopt_list *P, const dopt_hparams *hp, int32_t n_hgroups, double max_grad_norm, void *ws,
@@ -1140,7 +1154,9 @@ int dopt_list_prepare(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_h
     if (rc || (rc = check_tensors(P, ts, true, false)) ||
         (rc = build_finalize_args(P->max_hgroup, hp, n_hgroups, max_grad_norm, a)))
         return rc;
-    return launch_list_stats(P, ts, ws, stream, &a);
+    Tables tables;
+    if ((rc = place_addresses(P, ts, true, false, true, ws, stream, tables))) return rc;
+    return launch_list_stats(P, ts, tables, ws, stream, &a);
 }
 
 int dopt_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list_state *state, void *ws,
@@ -1148,7 +1164,9 @@ int dopt_list_apply(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_lis
     StateArrays s;
     int rc = check_list(P, ws);
     if (rc || (rc = check_tensors(P, ts, true, true)) || (rc = check_state(P, state, s))) return rc;
-    return launch_list_apply(P, ts, s, ws, stream);
+    Tables tables;
+    if ((rc = place_addresses(P, ts, false, true, true, ws, stream, tables))) return rc;
+    return launch_list_apply(P, ts, tables, s, ws, stream);
 }
 
 int dopt_list_step(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list_state *state, const dopt_hparams *hp,
@@ -1162,8 +1180,10 @@ int dopt_list_step(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list
     if (P->total_tiles > 0 && P->total_tiles <= kSmallTiles) {
         rc = launch_list_small(P, ts, s, a, ws, stream);
     } else {
-        rc = launch_list_stats(P, ts, ws, stream, &a);
-        if (rc == DOPT_OK) rc = launch_list_apply(P, ts, s, ws, stream);
+        Tables tables;
+        rc = place_addresses(P, ts, true, true, true, ws, stream, tables);  // once for both passes
+        if (rc == DOPT_OK) rc = launch_list_stats(P, ts, tables, ws, stream, &a);
+        if (rc == DOPT_OK) rc = launch_list_apply(P, ts, tables, s, ws, stream);
     }
     if (rc) return rc;
     return out ? copy_stats(ws, stream, out) : DOPT_OK;
