@@ -37,11 +37,12 @@ namespace dopt {
 
 // ---- tensor addresses ---------------------------------------------------------
 
-// The addresses of a launch's tensors: distances in elements from the lowest
-// of the launch, or a table of the class in the workspace.
+// The addresses of a launch's tensors: distances from the lowest of the
+// launch in units of 2^shift bytes, or a table of the class in the workspace.
 struct GradAddr {
     const dopt_list_ptrs *table;
     const char *grad0;
+    uint32_t grad_shift, pad;
     uint32_t grad[kListGradSlots];
 };
 struct ListSlot {
@@ -51,6 +52,7 @@ struct ListAddr {
     const dopt_list_ptrs *table;
     const char *grad0;
     char *param0;
+    uint32_t grad_shift, param_shift;
     ListSlot s[kListSlots];
 };
 struct PutAddr {
@@ -65,16 +67,14 @@ static_assert(kListPut <= kBlock, "one thread an address");
 // Tensor `index` of the class, in a launch that begins with tensor `first`.
 // The distances are read whether they are used or not, beside the table's
 // address rather than after it.
-template <int PD, int GD>
 __device__ __forceinline__ dopt_list_ptrs ptrs_of(const ListAddr &a, uint32_t index, int32_t first) {
     const ListSlot s = a.s[index - first];
-    dopt_list_ptrs p{a.grad0 + uint64_t(s.grad) * Elem<GD>::kBytes, a.param0 + uint64_t(s.param) * Elem<PD>::kBytes};
+    dopt_list_ptrs p{a.grad0 + (uint64_t(s.grad) << a.grad_shift), a.param0 + (uint64_t(s.param) << a.param_shift)};
     if (__builtin_expect(a.table != nullptr, 0)) p = a.table[index];
     return p;
 }
-template <int GD>
 __device__ __forceinline__ const void *grad_of(const GradAddr &a, uint32_t index, int32_t first) {
-    const void *p = a.grad0 + uint64_t(a.grad[index - first]) * Elem<GD>::kBytes;
+    const void *p = a.grad0 + (uint64_t(a.grad[index - first]) << a.grad_shift);
     if (__builtin_expect(a.table != nullptr, 0)) p = a.table[index].grad;
     return p;
 }
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradAddr add
 #pragma unroll
         for (int u = 0; u < kListStatsTiles; ++u) {
             const ListTile d = a.tiles[t0 + u < a.t_end ? t0 + u : a.t_end - 1];
-            const void *g = grad_of<GD>(addr, d.index, a.first);
+            const void *g = grad_of(addr, d.index, a.first);
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
                 const Place L = place_of<kGroups>(d, k, threadIdx.x);
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kWide) k_list_apply(const ListTile *__restrict
     const int skip = rec->skip;  // loaded beside the tile: a skipped step touches no data
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
     if (skip) return;
-    const dopt_list_ptrs q = ptrs_of<PD, GD>(addr, d.index, first);
+    const dopt_list_ptrs q = ptrs_of(addr, d.index, first);
     const Hp h = load_hp(rec, d.packed >> 16);
     const Place L = place_of<1>(d, 0, threadIdx.x);
     const auto graw = load4<GD>(q.grad, L.e, L.n);
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kBlock) k_list_export(const ListTile *__restri
                                                        const int64_t *__restrict__ xoff, StateArrays s,
                                                        ExportArrays x, ListAddr addr) {
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
-    const void *param = ptrs_of<PD, PD>(addr, d.index, first).param;
+    const void *param = ptrs_of(addr, d.index, first).param;
     const int64_t o = xoff[d.index];
     Place L[kGroups];
     u32x4 praw[kGroups];
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kWide) k_list_import(const ListTile *__restric
                                                       const int64_t *__restrict__ xoff, StateArrays s,
                                                       ExportArrays x, ListAddr addr) {
     const ListTile d = tiles[t_begin + tile_of(blockIdx.x, t_end - t_begin)];
-    void *param = ptrs_of<PD, PD>(addr, d.index, first).param;
+    void *param = ptrs_of(addr, d.index, first).param;
     const int64_t o = xoff[d.index];
     const Place L = place_of<1>(d, 0, threadIdx.x);
     const u32x4 praw = load4<DOPT_F32>(x.p, o + L.e, L.n);
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kWide) k_list_init(const ListTile *__restrict_
     if (n <= 0) return;
     if (masters) {
         float p[kQuad] = {0, 0, 0, 0};
-        if (PD != DOPT_F32) unpack4<PD>(load4<PD>(ptrs_of<PD, PD>(addr, d.index, first).param, L.e, L.n), p);
+        if (PD != DOPT_F32) unpack4<PD>(load4<PD>(ptrs_of(addr, d.index, first).param, L.e, L.n), p);
         store4<DOPT_F32>(s.master, L.arena, n, p);
     }
     if constexpr (ST == DOPT_STATE_E4M3) {
@@ -856,21 +856,31 @@ static const ListTile *tiles_of(const ListClass &C, const void *ws) {
     return reinterpret_cast<const ListTile *>(static_cast<const char *>(ws) + C.ws_tiles);
 }
 
-static int64_t bytes_of(int dt) { return dt == DOPT_F32 ? 4 : 2; }
-
-// Lowest address among n of a kind, and whether the others' distances from it
-// fit 32 bits.
+// The lowest address of n of a kind, and the others' distances from it in
+// units of the largest power of two that divides them all.
 struct Span {
-    uintptr_t lo = UINTPTR_MAX, hi = 0;
-    void add(const void *p) {
-        lo = std::min(lo, reinterpret_cast<uintptr_t>(p));
-        hi = std::max(hi, reinterpret_cast<uintptr_t>(p));
+    uintptr_t lo = UINTPTR_MAX, hi = 0, bits = 0;
+    template <class At>  // the i-th address
+    Span(int32_t n, At at) {
+        for (int32_t i = 0; i < n; ++i) {
+            lo = std::min(lo, reinterpret_cast<uintptr_t>(at(i)));
+            hi = std::max(hi, reinterpret_cast<uintptr_t>(at(i)));
+        }
+        for (int32_t i = 0; i < n; ++i) bits |= reinterpret_cast<uintptr_t>(at(i)) - lo;
     }
-    bool fits(int dt) const { return hi < lo || (hi - lo) / bytes_of(dt) <= UINT32_MAX; }
-    uint32_t from(const void *p, int dt) const {
-        return static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) - lo) / bytes_of(dt));
+    uint32_t shift() const { return bits ? static_cast<uint32_t>(__builtin_ctzll(bits)) : 0; }
+    bool fits() const { return !bits || (hi - lo) >> shift() <= UINT32_MAX; }
+    uint32_t from(const void *p) const {
+        return static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) - lo) >> shift());
     }
 };
+
+static Span grad_span(const ListClass &C, const ListRange &r, const dopt_list_ptrs *ts) {
+    return Span(r.count, [&](int32_t i) { return ts[C.tensors[static_cast<size_t>(r.first + i)]].grad; });
+}
+static Span param_span(const ListClass &C, const ListRange &r, const dopt_list_ptrs *ts) {
+    return Span(r.count, [&](int32_t i) { return ts[C.tensors[static_cast<size_t>(r.first + i)]].param; });
+}
 
 // Per class the table of its addresses in the workspace, or null where every
 // launch's addresses fit its arguments.
@@ -880,15 +890,8 @@ struct Tables {
 
 static bool fits(const ListClass &C, const std::vector<ListRange> &ranges, const dopt_list_ptrs *ts, bool grads,
                  bool params) {
-    for (const ListRange &r : ranges) {
-        Span g, p;
-        for (int32_t i = r.first; i < r.first + r.count; ++i) {
-            const dopt_list_ptrs &t = ts[C.tensors[static_cast<size_t>(i)]];
-            if (grads) g.add(t.grad);
-            if (params) p.add(t.param);
-        }
-        if (!g.fits(C.gd) || !p.fits(C.pd)) return false;
-    }
+    for (const ListRange &r : ranges)
+        if ((grads && !grad_span(C, r, ts).fits()) || (params && !param_span(C, r, ts).fits())) return false;
     return true;
 }
 
@@ -921,18 +924,15 @@ static void fill(ListAddr &a, const ListClass &C, const ListRange &r, const dopt
     std::memset(&a, 0, sizeof a);
     a.table = table;
     if (table) return;
-    Span g, p;
-    for (int32_t i = 0; i < r.count; ++i) {
-        const dopt_list_ptrs &t = ts[C.tensors[static_cast<size_t>(r.first + i)]];
-        if (grads) g.add(t.grad);
-        p.add(t.param);
-    }
-    a.grad0 = grads ? reinterpret_cast<const char *>(g.lo) : nullptr;
+    const Span p = param_span(C, r, ts);
     a.param0 = reinterpret_cast<char *>(p.lo);
-    for (int32_t i = 0; i < r.count; ++i) {
-        const dopt_list_ptrs &t = ts[C.tensors[static_cast<size_t>(r.first + i)]];
-        a.s[i] = ListSlot{grads ? g.from(t.grad, C.gd) : 0, p.from(t.param, C.pd)};
-    }
+    a.param_shift = p.shift();
+    for (int32_t i = 0; i < r.count; ++i) a.s[i].param = p.from(ts[C.tensors[static_cast<size_t>(r.first + i)]].param);
+    if (!grads) return;
+    const Span g = grad_span(C, r, ts);
+    a.grad0 = reinterpret_cast<const char *>(g.lo);
+    a.grad_shift = g.shift();
+    for (int32_t i = 0; i < r.count; ++i) a.s[i].grad = g.from(ts[C.tensors[static_cast<size_t>(r.first + i)]].grad);
 }
 
 static void fill(GradAddr &a, const ListClass &C, const ListRange &r, const dopt_list_ptrs *ts,
@@ -940,10 +940,10 @@ static void fill(GradAddr &a, const ListClass &C, const ListRange &r, const dopt
     std::memset(&a, 0, sizeof a);
     a.table = table;
     if (table) return;
-    Span g;
-    for (int32_t i = 0; i < r.count; ++i) g.add(ts[C.tensors[static_cast<size_t>(r.first + i)]].grad);
+    const Span g = grad_span(C, r, ts);
     a.grad0 = reinterpret_cast<const char *>(g.lo);
-    for (int32_t i = 0; i < r.count; ++i) a.grad[i] = g.from(ts[C.tensors[static_cast<size_t>(r.first + i)]].grad, C.gd);
+    a.grad_shift = g.shift();
+    for (int32_t i = 0; i < r.count; ++i) a.grad[i] = g.from(ts[C.tensors[static_cast<size_t>(r.first + i)]].grad);
 }
 
 // Calls f with an element type as a compile-time constant.

@@ -410,12 +410,14 @@ def test_ranks_with_8_bit_moments_exchange_their_record():
         assert D.dopt_step(lay, A.bufs, SHARD_HPS, 1.0, A.workspace, stream)["step_count"] == 2
 
 
+@pytest.mark.parametrize("unit", [2, 512])
 @pytest.mark.parametrize("n", [3, 300])
 @pytest.mark.parametrize("state", STATES)
-def test_tensors_far_apart(state, n):
+def test_tensors_far_apart(state, n, unit):
     """Params and grads in turn at either end of 10 GiB, so that no 32-bit
-    distance reaches from one to the next: the results, norm and checkpoint of
-    the same tensors side by side, bit for bit."""
+    number of elements reaches from one to the next, at odd offsets and at
+    offsets of a common 512 bytes: the results, norm and checkpoint of the
+    same tensors side by side, bit for bit."""
     rng = np.random.default_rng(n)
     sizes = [9000] + [int(x) for x in rng.integers(1, 3000, n - 1)]
     near, far = (H.ListCase(sizes, [("bf16", "bf16")], state, seed=14) for _ in range(2))
@@ -426,11 +428,11 @@ def test_tensors_far_apart(state, n):
     for i, x in enumerate(sizes):
         for name, side in (("params", i % 2), ("grads", 1 - i % 2)):
             if side:  # from the top down
-                at[1] -= 2 * x + 2
+                at[1] -= -(-(2 * x + 2) // unit) * unit
                 a = at[1]
             else:
                 a = at[0]
-                at[0] += 2 * x + 2
+                at[0] += -(-(2 * x + 2) // unit) * unit
             v = field[a:a + 2 * x].view(torch.bfloat16)
             v.copy_(getattr(far, name)[i])
             moved[name].append(v)
