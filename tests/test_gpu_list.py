@@ -312,6 +312,64 @@ def test_two_lists_on_two_streams():
             assert all(np.array_equal(x[i], y[i]) for i in x)
 
 
+@pytest.mark.parametrize("state", STATES)
+def test_a_modules_params(state):
+    """The params of a module as the allocator placed them, with the grads of
+    its backward pass, stepped through the default stream; init again begins
+    anew."""
+    import sharded_mixed_precision_amd as D
+    from sharded_mixed_precision_amd.arena import ListArrays
+    torch.manual_seed(0)
+    net = torch.nn.Sequential(torch.nn.Linear(96, 130), torch.nn.GELU(), torch.nn.Linear(130, 33)).cuda()
+    params = list(net.parameters())
+    net(torch.randn(8, 96, device="cuda")).square().sum().backward()
+    L = D.dopt_list_build([D.TensorSpec(p.numel(), "f32", "f32") for p in params], state)
+    A, hp = ListArrays(L), (1e-2, 0.9, 0.999, 1e-8, 0.01)
+    t = D.list_tensors(L, params, [p.grad for p in params], A.state)
+    begin = [p.detach().clone() for p in params]
+    for _ in range(2):
+        for p, b in zip(params, begin):
+            p.data.copy_(b)
+        D.dopt_list_init(L, t, D.scaler_cfg(), A.workspace)
+        st = D.dopt_list_step(L, t, [hp], 1.0, A.workspace)
+        assert st["step_count"] == 1
+        clip = st["clip_coef"] if st["clip_applied"] else None
+        for p, b in zip(params, begin):
+            z = np.zeros(p.numel(), np.float32)
+            want = H.step_f32(p.grad.cpu().numpy().reshape(-1), b.cpu().numpy().reshape(-1), z, z, hp, 1, 1.0, clip)[0]
+            assert np.array_equal(p.detach().cpu().numpy().reshape(-1), want)
+
+
+@pytest.mark.parametrize("state", STATES)
+@pytest.mark.parametrize("count", [16, 40])
+def test_all_hyper_groups(state, count):
+    """A list over all 16 hyper-groups, in one launch's and in two launches' form."""
+    c = H.ListCase([100 + 37 * i for i in range(count)], [("bf16", "f32")], state, seed=17, hgroups=list(range(16)))
+    c.hps = [(1e-3 * (i + 1), 0.9 - 0.01 * i, 0.99 - 0.005 * i, 1e-8 * 4 ** i, 0.01 * i) for i in range(16)]
+    run(c)
+    s = H.ListCase([100, 2000, 5], [("bf16", "f32")], state, seed=17, hgroups=[15, 3, 8])
+    s.hps = c.hps
+    run(s)
+
+
+def test_shared_grads_and_empty_copies():
+    import sharded_mixed_precision_amd as D
+    c = H.ListCase([3000, 3000], [("bf16", "bf16")], "e4m3", seed=18)
+    c.grads[1] = c.grads[0]
+    c.t = D.list_tensors(c.L, c.params, c.grads, c.A.state)
+    c.init()
+    before = c.snapshot()
+    c.check_step(before, D.dopt_list_step(c.L, c.t, c.hps, 1.0, c.A.workspace, c.stream))
+    for sizes in ([], [0, 0]):
+        e = H.ListCase(sizes, [("bf16", "bf16")], "e4m3")
+        e.init()
+        x = [torch.empty(0, device="cuda")] * 3
+        D.dopt_list_export(e.L, e.t, *x, e.A.workspace, e.stream)
+        D.dopt_list_import(e.L, e.t, *x, e.A.workspace, e.stream)
+        D.dopt_list_stats(e.L, e.t, e.A.workspace, e.stream)
+        D.dopt_list_apply(e.L, e.t, e.A.workspace, e.stream)
+
+
 SHARDED = [ParamSpec("emb", 100_003, "bf16", "f32", 1, 0), ParamSpec("w1", 70_001, "bf16", "bf16", 0, 0),
            ParamSpec("n1", 4096, "f32", "f32", 0, 1), ParamSpec("h1", 33_333, "f16", "f16", 0, 0),
            ParamSpec("w2", 123_456, "bf16", "bf16", 0, 1), ParamSpec("n2", 100, "f32", "f32", 0, 0)]
