@@ -45,12 +45,12 @@ constexpr int kListPut = 240;
 // slightly different rates and drift apart along the arrays; pass 2 and the
 // copies, which write as much as they read, are therefore launched piece by
 // piece, of about 2e9 bytes.  On MI355X, per launch 2^20 / 2^18 / 2^17 / 2^16 /
-// 2^15 tiles: pass 2 of 1.1e9 bf16 params with fp32 moments 5.25 / 5.24 / 5.12 /
-// 5.05 / 5.03 ms, of 1.2e8 fp32 params 0.592 (to 2^16) / 0.576; with e4m3 moments
-// 1.0e9 params and fp32 grads 2.94 / 2.90 / 2.88 / 2.90 / 2.94, 1.2e8 bf16 0.333 (to
-// 2^16) / 0.338; export of 1.0e9 3.25 / 3.15 / 3.03 / 2.96 / 2.95.  Pass 1 only reads and
-// loses by it (1.1e9 bf16 grads 328 us in one launch, 435 at 2^15); its limit
-// keeps a launch below 2^32 threads.
+// 2^15 tiles (with 256 threads to a tile; with 512 the last three order alike):
+// pass 2 of 1.1e9 bf16 params with fp32 moments 5.25 / 5.24 / 5.12 / 5.05 / 5.03 ms, of
+// 1.2e8 fp32 params 0.592 (to 2^16) / 0.576; with e4m3 moments 1.0e9 params and fp32
+// grads 2.94 / 2.90 / 2.88 / 2.90 / 2.94, 1.2e8 bf16 0.333 (to 2^16) / 0.338; export of 1.0e9
+// 3.25 / 3.15 / 3.03 / 2.96 / 2.95.  Pass 1 only reads and loses by it (1.1e9 bf16 grads 328 us
+// in one launch, 435 at 2^15); its limit keeps a launch below 2^32 threads.
 constexpr int64_t kListStatsLaunch = int64_t(1) << 20;
 inline int64_t list_launch_tiles(int state_kind) { return int64_t(1) << (state_kind == DOPT_STATE_E4M3 ? 16 : 15); }
 

@@ -252,9 +252,9 @@ __device__ __forceinline__ void store_codes(void *base, int64_t e, int n, uint32
 // The tile of workgroup b of n.  Workgroups go to the 8 XCDs in turn; runs of
 // kXcdRun consecutive tiles are dealt to one XCD, so that the lines two tiles
 // share (a tile's scales are half a line) meet in one L2, and each XCD's
-// requests run along the arrays.  On MI355X 16 and 32 were the best of 1 to 64
-// for pass 2 with e4m3 moments (1.0e9 elements: 3.16 ms at 1, 3.34 at 4, 3.22 at 8, 3.04 at
-// 16, 3.03 at 32, 3.09 at 64) and with fp32 moments (5.02, 4.99, 4.98, 4.95, 4.98, 5.16).
+// requests run along the arrays.  On MI355X, runs of 4 / 8 / 16 / 32 / 64 tiles:
+// pass 2 with e4m3 moments of 1.0e9 elements 3.05 / 2.91 / 2.91 / 2.90 / 2.91 ms, with fp32
+// ones of 1.1e9 4.94 / 4.90 / 4.90 / 4.91 / 5.00, export of 1.0e9 2.98 / 3.00 / 2.90 / 2.96 / 3.07.
 constexpr int64_t kXcds = 8, kXcdRun = 16;
 __device__ __forceinline__ int64_t tile_of(int64_t b, int64_t n) {
     const int64_t whole = n / (kXcds * kXcdRun) * (kXcds * kXcdRun);
