@@ -34,6 +34,9 @@
  * 2^-9 * scale for a sqrt(v) raised to the smallest code).  A NaN in a block
  * makes its scale, and so every element of the block, NaN.
  *
+ * A workspace belongs to the list it was initialised for (dopt_list_init):
+ * another list's tables in it would lead the kernels astray.
+ *
  * Conventions as in dopt.h: 0 or a negative DOPT_ERR_* code, stream-ordered,
  * nothing allocated on the device, no synchronization unless stated.  Calls
  * that use one workspace must not overlap in time.  dopt_list_stats,

@@ -771,18 +771,26 @@ def _list_ws(lst: TensorList, workspace, stream, device: Optional[int] = None):
     to be there."""
     global _torch
     ws = _dev(workspace, "workspace", None, 0, lst.workspace_bytes)
-    at = [(device, "tensors")] if device is not None else []
-    at += [(x.device.index, what) for x, what in ((workspace, "workspace"), (stream, "stream"))
-           if x is not None and not isinstance(x, int)]
-    if at:
-        if _torch is None:
-            import torch
-            _torch = torch
-        current = _torch.cuda.current_device()
-        for index, what in at:
-            if index != current:
-                raise DoptError(DOPT_ERR_INVALID, f"{what} on device {index}, the current device is {current}")
-    return ws, _stream(stream)
+    if _torch is None:
+        if device is None and isinstance(workspace, int) and (stream is None or isinstance(stream, int)):
+            return ws, stream
+        import torch
+        _torch = torch
+    current = _torch.cuda.current_device() if device is not None or workspace is not ws else None
+    if device is not None and device != current:
+        _elsewhere("tensors", device)
+    if workspace is not ws and workspace.get_device() != current:
+        _elsewhere("workspace", workspace.get_device())
+    if stream is None or isinstance(stream, int):
+        return ws, stream
+    index = stream.device.index
+    if index != (_torch.cuda.current_device() if current is None else current):
+        _elsewhere("stream", index)
+    return ws, stream.cuda_stream
+
+
+def _elsewhere(what: str, index: int):
+    raise DoptError(DOPT_ERR_INVALID, f"{what} on device {index}, the current device is {_torch.cuda.current_device()}")
 
 
 def _list_args(lst: TensorList, t: ListTensors, workspace, stream, need_grads: bool = True):
