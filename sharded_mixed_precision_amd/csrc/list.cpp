@@ -47,6 +47,7 @@ static int plan(dopt_list &P) {
         T.arena = blocks * kListBlock;
         T.xoff = numel;
         numel += T.numel;
+        P.grad_bytes += T.numel * (T.gd == DOPT_F32 ? 4 : 2);
         if (numel > kListMaxNumel) return fail(DOPT_ERR_INVALID, "the tensors hold more than 2^38 elements in total");
         blocks += (T.numel + kListBlock - 1) / kListBlock;
         P.max_hgroup = std::max(P.max_hgroup, T.hgroup);

@@ -73,6 +73,14 @@ inline int32_t list_stats_grid(int64_t tiles) {
 // with and without: 6.7 / 8.6 us at 8 partials, 7.7 / 8.2 at 64, 8.5 / 8.2 at
 // 100, 10.8 / 8.2 at 200.
 constexpr int32_t kListFused = 64;
+// Pass 1 reads grads of at most this many bytes (twice the last-level cache)
+// with ordinary loads, which leave them to pass 2, and more of them with
+// nontemporal ones, which read faster.  A step on MI355X, nontemporal / ordinary
+// loads, at 160 / 320 / 640 / 960 MB of grads: fp32 grads with e4m3 moments 148 / 137,
+// 282 / 270, 561 / 555, 826 / 833 us; bf16 ones with e4m3 moments 243 / 235, 477 / 469,
+// 943 / 947 us to 640 MB, with fp32 moments 397 / 375, 788 / 753, 1641 / 1619 us.
+// Pass 1 alone: 160 MB in 31 / 34 us, 2 GB in 293 / 330.
+constexpr int64_t kListKeep = int64_t(512) << 20;
 // Where the workspace counts pass 1's finished workgroups.
 constexpr int64_t kWsListDone = kWsRecord + 64;
 
@@ -111,7 +119,7 @@ struct dopt_list {
     bool has_master = false;
     std::vector<dopt::ListTensor> tensors;
     std::vector<dopt::ListClass> classes;
-    int64_t numel = 0, arena_numel = 0, ws_bytes = 0;
+    int64_t numel = 0, arena_numel = 0, ws_bytes = 0, grad_bytes = 0;
     int32_t total_partials = 0;
     int64_t total_tiles = 0;
 };

@@ -21,7 +21,9 @@
 //   runs of 16 consecutive tiles on one XCD (tile_of)                    4.95 / 3.04 ms
 //   512 threads to a tile, a lane with 4 elements, launched in pieces    4.95 / 2.85 ms
 // Nontemporal accesses lose in the first layout, whose instructions leave
-// half of every line they touch to the next one.
+// half of every line they touch to the next one.  Pass 1 reads the grads of a
+// list that is not too long with ordinary loads (kListKeep in list.h): pass 2
+// then finds them in the last-level cache.
 //
 // A block of 128 elements is then a half-wave: the DPP lane permutes reduce
 // over 16 lanes, one swizzle joins the two halves, and LDS is not used.
@@ -124,14 +126,17 @@ __device__ __forceinline__ __attribute__((address_space(1))) T *global(T *p) {
 }
 
 // Elements i .. i+3 of a tensor, of which the first n exist (n <= 0: none);
-// the others read as 0.
-template <int DT>
+// the others read as 0.  KEEP: an ordinary load, for what a later pass reads
+// again from the last-level cache.
+template <int DT, bool KEEP = false>
 __device__ __forceinline__ typename Quad<DT>::Raw load4(const void *base, int64_t i, int n) {
     typedef Quad<DT> Q;
     const auto *p = global(static_cast<const typename Q::T *>(base)) + i;
     typename Q::Raw r{};
     if (n >= kQuad) {
-        r = __builtin_nontemporal_load((const __attribute__((address_space(1))) typename Q::At *)p);
+        const auto *q = (const __attribute__((address_space(1))) typename Q::At *)p;
+        if constexpr (KEEP) r = *q;
+        else r = __builtin_nontemporal_load(q);
     } else {
 #pragma unroll
         for (int j = 0; j < kQuad - 1; ++j) {
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(THREADS) k_list_finish(StatsArgs a) {
     finish_stats<THREADS, BATCH, false>(a);
 }
 
-template <int GD, bool FUSED>
+template <int GD, bool FUSED, bool KEEP>
 __global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradAddr addr) {
     const float inv = a.st->inv_scale;
     double acc = 0.0;
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kBlock) k_list_stats(StatsArgs a, GradAddr add
             for (int k = 0; k < kGroups; ++k) {
                 const Place L = place_of<kGroups>(d, k, threadIdx.x);
                 n[u][k] = t0 + u < a.t_end ? L.n : 0;
-                raw[u][k] = load4<GD>(g, L.e, n[u][k]);
+                raw[u][k] = load4<GD, KEEP>(g, L.e, n[u][k]);
             }
         }
 #pragma unroll
@@ -971,6 +976,7 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, const
     a.total = P->total_partials;
     const bool fused = a.total > 0 && a.total <= kListFused;
     a.finalize = fa != nullptr;
+    const bool keep = P->grad_bytes <= kListKeep;
     if (fa) a.fa = *fa;
     a.st = reinterpret_cast<DevState *>(ws_ptr(ws, kWsState));
     a.part = reinterpret_cast<Partial *>(ws_ptr(ws, kWsPartials));
@@ -989,8 +995,10 @@ static int launch_list_stats(const dopt_list *P, const dopt_list_ptrs *ts, const
             a.first = r.first;
             a.part0 = r.partial_base;
             with_dtype(C.gd, [&](auto gd) {
-                if (fused) k_list_stats<decltype(gd)::value, true><<<r.grid, kBlock, 0, stream>>>(a, g);
-                else k_list_stats<decltype(gd)::value, false><<<r.grid, kBlock, 0, stream>>>(a, g);
+                constexpr int GD = decltype(gd)::value;
+                if (fused) k_list_stats<GD, true, true><<<r.grid, kBlock, 0, stream>>>(a, g);
+                else if (keep) k_list_stats<GD, false, true><<<r.grid, kBlock, 0, stream>>>(a, g);
+                else k_list_stats<GD, false, false><<<r.grid, kBlock, 0, stream>>>(a, g);
             });
             const int rc = check_launch("launch k_list_stats");
             if (rc) {
