@@ -34,13 +34,41 @@
  * 2^-9 * scale for a sqrt(v) raised to the smallest code).  A NaN in a block
  * makes its scale, and so every element of the block, NaN.
  *
+ * Over a run, nearest rounding does not follow the grads: an update moves
+ * sqrt(v) by (1 - beta2)/2 * (g^2/v - 1) of itself, 0.05% with beta2 = 0.999, and
+ * what stays below half a step of its code (3 to 6%) is lost every time, while
+ * the scale follows the block's largest element and takes the others with it.
+ * Against fp32 moments, Gaussian grads: sqrt(v) is off by 0.63 to 1.6 times (1st to 99th
+ * percentile) and stays so; where the grads of half a block fall to a tenth,
+ * their sqrt(v) is 8.6 times too large (median) 6500 steps later.
+ * DOPT_STATE_E4M3 is thus for a few updates at a time (grads whose size does not
+ * move, a state that is loaded, updated and compared).
+ *
+ * DOPT_STATE_E4M3_SR holds the same codes and scales and is for whole runs: the
+ * code is one of the two that x * (1 / scale) lies between, the farther one
+ * with the probability that leaves the mean unchanged, so small changes add
+ * up. sqrt(v) then stays within 0.7 to 1.4 times that of fp32 moments
+ * (1st to 99th percentile) with a mean within 2%, and follows grads that grow or fall.
+ * A nonzero sqrt(v) keeps a nonzero code here too. The random
+ * numbers are a function of the list's seed (dopt_list_set_seed), the number of the step and
+ * the element's place in the arena, and of nothing else: a
+ * run that is repeated, resumed from a checkpoint of its codes or replayed from a captured graph takes
+ * the same ones, and replicas with one seed stay equal. With k the element's arena
+ * index, w the k % 4th word of Philox4x32-7 (Salmon, Moraes, Dror, Shaw: Parallel
+ * random numbers: as easy as 1, 2, 3, 2011) of counter {k / 4, its high word, t, t's high word} and key
+ * {seed, its high word}, t the step count after the step, and u = w mod 2^16 for m, w / 2^16 for sqrt(v):
+ *     y = |q| + 2^-6 if |q| < 2^-6 else |q|,   q = clamp(x * (1 / scale), -448, 448)
+ *     the bits of y, plus 16 u + 8, without their lowest 20, are those of the code's magnitude (+ 2^-6)
+ * An element is thereby within a step of e4m3 of its value (2^-3 of it, or 2^-9 * scale).
+ * dopt_list_import rounds to nearest in both kinds.
+ *
  * A workspace belongs to the list it was initialised for (dopt_list_init):
  * another list's tables in it would lead the kernels astray.
  *
  * Conventions as in dopt.h: 0 or a negative DOPT_ERR_* code, stream-ordered,
  * nothing allocated on the device, no synchronization unless stated.  Calls
  * that use one workspace must not overlap in time.  dopt_list_stats,
- * _finalize, _prepare, _apply, _step (out == NULL), _export and _import only
+ * _finalize, _prepare, _apply, _step (out == NULL), _export, _import and _set_seed only
  * launch kernels and may be captured into a HIP graph; a replay uses the
  * addresses and hyper-parameters that the captured call was given.  A tensor
  * without a grad in a step has no place in that step's list: a null grad is
@@ -56,7 +84,8 @@ extern "C" {
 #endif
 
 /* ---- how the Adam moments are held ---- */
-enum { DOPT_STATE_F32 = 0, DOPT_STATE_E4M3 = 1 };
+/* (_SR adds 2, unbiased rounding, to e4m3; fp32 moments have no such form.) */
+enum { DOPT_STATE_F32 = 0, DOPT_STATE_E4M3 = 1, DOPT_STATE_E4M3_SR = 3 };
 
 /* Elements per block of an 8-bit moment; every tensor's arena_offset is a multiple. */
 #define DOPT_LIST_BLOCK 128
@@ -129,13 +158,13 @@ typedef struct dopt_list_state {
     float *master;           /* arena_numel fp32; NULL if no param is 16-bit (slots of fp32 params are unused) */
     void *exp_avg;           /* arena_numel: fp32, or e4m3 codes (1 byte each) */
     void *exp_avg_sq;        /* arena_numel: fp32 v, or e4m3 codes of sqrt(v) */
-    float *exp_avg_scale;    /* DOPT_STATE_E4M3: n_blocks fp32; else NULL */
-    float *exp_avg_sq_scale; /* DOPT_STATE_E4M3: n_blocks fp32; else NULL */
+    float *exp_avg_scale;    /* DOPT_STATE_E4M3, _SR: n_blocks fp32; else NULL */
+    float *exp_avg_sq_scale; /* DOPT_STATE_E4M3, _SR: n_blocks fp32; else NULL */
 } dopt_list_state;
 
 /*
  * dopt_list_init -- master = upcast of the 16-bit params, moments = 0, step
- * count 0, loss scale scaler->initial_scale; loads the list's tables into the
+ * count 0, loss scale scaler->initial_scale, seed 0; loads the list's tables into the
  * workspace.  tensors: host array of n_tensors entries.  Synchronizes
  * `stream`.  Errors: DOPT_ERR_INVALID (null or misaligned pointers, bad
  * scaler), DOPT_ERR_HIP.
@@ -180,6 +209,13 @@ int dopt_list_export(const dopt_list *list, const dopt_list_ptrs *tensors, const
 int dopt_list_import(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_list_state *state,
                      const float *master, const float *exp_avg, const float *exp_avg_sq, void *workspace,
                      hipStream_t stream);
+
+/*
+ * dopt_list_set_seed -- the seed of a DOPT_STATE_E4M3_SR list's rounding, from the next
+ * step on. Errors: DOPT_ERR_INVALID (null or misaligned pointers, a list of
+ * another kind), DOPT_ERR_HIP.
+ */
+int dopt_list_set_seed(const dopt_list *list, uint64_t seed, void *workspace, hipStream_t stream);
 
 /* As dopt_state_scalars_get / _set and dopt_read_stats, of a list's workspace. */
 int dopt_list_scalars_get(const dopt_list *list, const void *workspace, hipStream_t stream, dopt_state_scalars *out);

@@ -28,8 +28,9 @@ DOPT_ARENA_ALIGN = 2048
 DOPT_PTR_ALIGN = 256
 
 
-DOPT_STATE_F32, DOPT_STATE_E4M3 = 0, 1
-STATE_KINDS = {"f32": DOPT_STATE_F32, "e4m3": DOPT_STATE_E4M3}
+DOPT_STATE_F32, DOPT_STATE_E4M3, DOPT_STATE_E4M3_SR = 0, 1, 3
+STATE_KINDS = {"f32": DOPT_STATE_F32, "e4m3": DOPT_STATE_E4M3, "e4m3_sr": DOPT_STATE_E4M3_SR}
+STATE_NAMES = {v: k for k, v in STATE_KINDS.items()}
 DOPT_LIST_BLOCK = 128
 
 
@@ -189,6 +190,7 @@ def _load():
         "dopt_list_apply": ([VP, P(dopt_list_ptrs), P(dopt_list_state), VP, VP], ctypes.c_int),
         "dopt_list_export": ([VP, P(dopt_list_ptrs), P(dopt_list_state), VP, VP, VP, VP, VP], ctypes.c_int),
         "dopt_list_import": ([VP, P(dopt_list_ptrs), P(dopt_list_state), VP, VP, VP, VP, VP], ctypes.c_int),
+        "dopt_list_set_seed": ([VP, ctypes.c_uint64, VP, VP], ctypes.c_int),
         "dopt_list_scalars_get": ([VP, VP, VP, P(dopt_state_scalars)], ctypes.c_int),
         "dopt_list_scalars_set": ([VP, VP, VP, P(dopt_state_scalars)], ctypes.c_int),
         "dopt_list_read_stats": ([VP, VP, VP, P(dopt_stats)], ctypes.c_int),
@@ -221,7 +223,7 @@ EXPORTED = ("dopt_build_ranges", "dopt_layout_free", "dopt_layout_num_buffers", 
             "dopt_last_error",
             "dopt_list_build", "dopt_list_from_layout", "dopt_list_free", "dopt_list_query", "dopt_list_tensor",
             "dopt_list_init", "dopt_list_step", "dopt_list_prepare", "dopt_list_stats", "dopt_list_finalize",
-            "dopt_list_apply", "dopt_list_export", "dopt_list_import", "dopt_list_scalars_get",
+            "dopt_list_apply", "dopt_list_export", "dopt_list_import", "dopt_list_set_seed", "dopt_list_scalars_get",
             "dopt_list_scalars_set", "dopt_list_read_stats",
             "dopt_vmm_granularity", "dopt_vmm_reserve", "dopt_vmm_free", "dopt_vmm_create", "dopt_vmm_map",
             "dopt_vmm_set_access", "dopt_vmm_unmap", "dopt_vmm_release")
@@ -619,7 +621,7 @@ class TensorList:
         _check(_lib.dopt_list_query(handle, ctypes.byref(o)))
         self.n_tensors, self.numel, self.arena_numel, self.n_blocks = o.n_tensors, o.numel, o.arena_numel, o.n_blocks
         self.workspace_bytes, self.stats_record_offset = o.workspace_bytes, o.stats_record_offset
-        self.state_kind = "e4m3" if o.state_kind == DOPT_STATE_E4M3 else "f32"
+        self.state_kind = STATE_NAMES[o.state_kind]
         self.has_master = bool(o.has_master)
 
     def __del__(self):
@@ -647,7 +649,7 @@ class TensorList:
 
     def state_arrays(self) -> Dict[str, Tuple[str, int]]:
         """The state arrays a list needs: name -> (element type, elements)."""
-        e = self.state_kind == "e4m3"
+        e = self.state_kind != "f32"
         out = {"master": ("f32", self.arena_numel)} if self.has_master else {}
         out.update(exp_avg=("e4m3" if e else "f32", self.arena_numel),
                    exp_avg_sq=("e4m3" if e else "f32", self.arena_numel))
@@ -664,8 +666,10 @@ def _state_kind(state: str) -> int:
 
 def dopt_list_build(specs: Sequence, state: str = "f32") -> TensorList:
     """specs: objects with numel, param_dtype, grad_dtype ('f32'|'bf16'|'f16')
-    and optional hgroup, in the order of the list; state: 'f32' or 'e4m3'
-    (8-bit moments)."""
+    and optional hgroup, in the order of the list; state: 'f32', or 8-bit
+    moments, 'e4m3_sr' for whole runs (rounded by chance with the mean kept)
+    and 'e4m3' (rounded to nearest: over a run sqrt(v) does not follow the
+    grads)."""
     n = len(specs)
     arr = (dopt_tensor_desc * n)()
     for i, p in enumerate(specs):
@@ -855,6 +859,13 @@ def dopt_list_export(lst: TensorList, t: ListTensors, master, exp_avg, exp_avg_s
 def dopt_list_import(lst: TensorList, t: ListTensors, master, exp_avg, exp_avg_sq, workspace, stream=None):
     """Inverse of dopt_list_export; also rewrites the params from the master."""
     _list_copy(_lib.dopt_list_import, "import", lst, t, master, exp_avg, exp_avg_sq, workspace, stream)
+
+
+def dopt_list_set_seed(lst: TensorList, seed: int, workspace, stream=None):
+    """The seed of an 'e4m3_sr' list's rounding, 0 after init; takes 64 bits."""
+    if not 0 <= seed < 1 << 64:
+        raise DoptError(DOPT_ERR_INVALID, f"seed {seed}: not in [0, 2^64)")
+    _check(_lib.dopt_list_set_seed(lst.handle, seed, *_list_ws(lst, workspace, stream)))
 
 
 def dopt_list_scalars_get(lst: TensorList, workspace, stream=None) -> Dict:

@@ -103,7 +103,8 @@ static int plan(dopt_list &P) {
 template <class Fill>
 static int make_list(int32_t state_kind, dopt_list **out, Fill fill) {
     *out = nullptr;
-    if (state_kind != DOPT_STATE_F32 && state_kind != DOPT_STATE_E4M3) return fail(DOPT_ERR_INVALID, "bad state kind");
+    if (state_kind != DOPT_STATE_F32 && state_kind != DOPT_STATE_E4M3 && state_kind != DOPT_STATE_E4M3_SR)
+        return fail(DOPT_ERR_INVALID, "bad state kind");
     dopt_list *P = new (std::nothrow) dopt_list();
     if (!P) return fail(DOPT_ERR_NOMEM, "out of host memory");
     int rc;

@@ -52,7 +52,7 @@ constexpr int kListPut = 240;
 // 3.25 / 3.15 / 3.03 / 2.96 / 2.95.  Pass 1 only reads and loses by it (1.1e9 bf16 grads 328 us
 // in one launch, 435 at 2^15); its limit keeps a launch below 2^32 threads.
 constexpr int64_t kListStatsLaunch = int64_t(1) << 20;
-inline int64_t list_launch_tiles(int state_kind) { return int64_t(1) << (state_kind == DOPT_STATE_E4M3 ? 16 : 15); }
+inline int64_t list_launch_tiles(int state_kind) { return int64_t(1) << (state_kind != DOPT_STATE_F32 ? 16 : 15); }
 
 // Pass 2 and the copies take one workgroup per tile.  A workgroup of pass 1
 // reads kListStatsTiles tiles at a time and grid-strides, about 8 times on
@@ -83,6 +83,9 @@ constexpr int32_t kListFused = 64;
 constexpr int64_t kListKeep = int64_t(512) << 20;
 // Where the workspace counts pass 1's finished workgroups.
 constexpr int64_t kWsListDone = kWsRecord + 64;
+// The seed of a list that rounds its moments by chance.
+constexpr int64_t kWsListSeed = kWsRecord + 128;
+static_assert(kWsListSeed + 8 <= kWsPartials, "the records end before the partials");
 
 struct ListRange {  // tiles [t0, t1) of `count` consecutive tensors of a class, from tensor `first`
     int32_t first = 0, count = 0;
