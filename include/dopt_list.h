@@ -202,7 +202,10 @@ int dopt_list_apply(const dopt_list *list, const dopt_list_ptrs *tensors, const 
  * dopt_state_export.  _import also rewrites the params from the master, as the
  * step's copy-back would, and holds m and v in the list's kind (8 bits: as
  * after an update; a negative v is NaN).  The arrays need 4-byte alignment
- * only.  The workspace must have been through dopt_list_init.
+ * only.  Refused with DOPT_ERR_INVALID: an array that overlaps the state or a
+ * param (but for a master array whose elements are the fp32 param's own), and
+ * arrays of an _export that overlap one another.  The workspace must have been
+ * through dopt_list_init.
  */
 int dopt_list_export(const dopt_list *list, const dopt_list_ptrs *tensors, const dopt_list_state *state,
                      float *master, float *exp_avg, float *exp_avg_sq, void *workspace, hipStream_t stream);

@@ -793,8 +793,16 @@ def _list_ws(lst: TensorList, workspace, stream, device: Optional[int] = None):
     return ws, stream.cuda_stream
 
 
+def _current_device() -> int:
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda.current_device()
+
+
 def _elsewhere(what: str, index: int):
-    raise DoptError(DOPT_ERR_INVALID, f"{what} on device {index}, the current device is {_torch.cuda.current_device()}")
+    raise DoptError(DOPT_ERR_INVALID, f"{what} on device {index}, the current device is {_current_device()}")
 
 
 def _list_args(lst: TensorList, t: ListTensors, workspace, stream, need_grads: bool = True):
@@ -845,8 +853,11 @@ def dopt_list_apply(lst: TensorList, t: ListTensors, workspace, stream=None):
 
 def _list_copy(fn, word: str, lst: TensorList, t: ListTensors, master, exp_avg, exp_avg_sq, workspace, stream):
     p, ws, s = _list_args(lst, t, workspace, stream, False)
-    x = [_dev(a, f"{word} {name}", "f32", lst.numel)
-         for a, name in ((master, "master"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq"))]
+    x = []
+    for a, name in ((master, "master"), (exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")):
+        x.append(_dev(a, f"{word} {name}", "f32", lst.numel))
+        if not isinstance(a, int) and a.numel() > 0 and a.get_device() != _current_device():
+            _elsewhere(f"{word} {name}", a.get_device())
     _check(fn(lst.handle, p, ctypes.byref(t.state), *x, ws, s))
 
 

@@ -933,6 +933,51 @@ static int check_state(const dopt_list *P, const dopt_list_state *s, StateArrays
     return DOPT_OK;
 }
 
+static bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + static_cast<uint64_t>(b_bytes) && y < x + static_cast<uint64_t>(a_bytes);
+}
+
+// The arrays of an export or import against one another, the params and the
+// state, which the same launches read and write in another order.  A master
+// array may be the fp32 params themselves: their elements go onto themselves.
+static int check_copies(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_list_state *st, const float *const (&x)[3],
+                        bool written) {
+    static const char *const kNames[3] = {"master", "exp_avg", "exp_avg_sq"};
+    const int64_t bytes = P->numel * 4;
+    if (P->numel == 0) return DOPT_OK;
+    for (const float *p : x)
+        if (!p) return fail(DOPT_ERR_INVALID, "null export array");
+    for (const float *p : x)
+        if (reinterpret_cast<uintptr_t>(p) % 4) return fail(DOPT_ERR_INVALID, "export array not 4-byte aligned");
+    const bool e = P->state_kind != DOPT_STATE_F32;
+    const int64_t held = P->arena_numel * (e ? 1 : 4), scales = e ? P->arena_numel / kListBlock * 4 : 0;
+    const struct {
+        const char *name;
+        const void *p;
+        int64_t bytes;
+    } state[] = {{"master", st->master, P->has_master ? P->arena_numel * 4 : 0},
+                 {"exp_avg", st->exp_avg, held},
+                 {"exp_avg_sq", st->exp_avg_sq, held},
+                 {"exp_avg_scale", st->exp_avg_scale, scales},
+                 {"exp_avg_sq_scale", st->exp_avg_sq_scale, scales}};
+    for (int i = 0; i < 3; ++i) {
+        for (int k = 0; written && k < i; ++k)
+            if (overlap(x[i], bytes, x[k], bytes))
+                return fail(DOPT_ERR_INVALID, std::string(kNames[i]) + " array overlaps the " + kNames[k] + " array");
+        for (const auto &s : state)
+            if (s.bytes > 0 && overlap(x[i], bytes, s.p, s.bytes))
+                return fail(DOPT_ERR_INVALID, std::string(kNames[i]) + " array overlaps state " + s.name);
+        for (size_t t = 0; t < P->tensors.size(); ++t) {
+            const ListTensor &T = P->tensors[t];
+            if (T.numel == 0 || !overlap(x[i], bytes, ts[t].param, T.numel * (T.pd == DOPT_F32 ? 4 : 2))) continue;
+            if (i == 0 && T.pd == DOPT_F32 && static_cast<const void *>(x[0] + T.xoff) == ts[t].param) continue;
+            return fail(DOPT_ERR_INVALID, std::string(kNames[i]) + " array overlaps param " + std::to_string(t));
+        }
+    }
+    return DOPT_OK;
+}
+
 static const ListTile *tiles_of(const ListClass &C, const void *ws) {
     return reinterpret_cast<const ListTile *>(static_cast<const char *>(ws) + C.ws_tiles);
 }
@@ -1153,11 +1198,7 @@ static int list_copy(const dopt_list *P, const dopt_list_ptrs *ts, const dopt_li
     StateArrays s;
     int rc = check_list(P, ws);
     if (rc || (rc = check_tensors(P, ts, false, true)) || (rc = check_state(P, state, s))) return rc;
-    if (P->numel > 0) {
-        if (!x.p || !x.m || !x.v) return fail(DOPT_ERR_INVALID, "null export array");
-        if ((reinterpret_cast<uintptr_t>(x.p) | reinterpret_cast<uintptr_t>(x.m) | reinterpret_cast<uintptr_t>(x.v)) % 4)
-            return fail(DOPT_ERR_INVALID, "export array not 4-byte aligned");
-    }
+    if ((rc = check_copies(P, ts, state, {x.p, x.m, x.v}, !IMPORT))) return rc;
     Tables tables;
     if ((rc = place_addresses(P, ts, false, true, false, ws, stream, tables))) return rc;
     for (size_t c = 0; c < P->classes.size(); ++c) {

@@ -39,3 +39,31 @@ def test_import_of_infinities_and_nans_block_by_block(state):
     # sqrt(3e38), within half a step of its code (it is its block's largest) and 4 roundings of v
     assert math.isclose(v[4, 8], 3e38, rel_tol=2 ** -22)
     assert np.isfinite(np.delete(scale[1], [2, 3])).all() and np.isnan(scale[1][[2, 3]]).all()
+
+
+@pytest.mark.parametrize("state", ["f32", "e4m3"])
+def test_a_flat_fp32_buffer_is_its_own_master_array(state):
+    """fp32 params back to back in list order may be the checkpoint's master
+    array: export and import leave them as they are and move the moments."""
+    import sharded_mixed_precision_amd as D
+    from sharded_mixed_precision_amd.arena import ListArrays
+    sizes = [5000, 3, 0, 4096, 777]
+    flat = torch.randn(sum(sizes), device="cuda")
+    begin = flat.clone()
+    L = D.dopt_list_build([D.TensorSpec(n, "f32", "f32") for n in sizes], state)
+    A, stream = ListArrays(L), torch.cuda.current_stream()
+    t = D.list_tensors(L, list(flat.split(sizes)), None, A.state)
+    D.dopt_list_init(L, t, D.scaler_cfg(), A.workspace, stream)
+    m, v = torch.randn(L.numel, device="cuda"), torch.randn(L.numel, device="cuda").square()
+    D.dopt_list_import(L, t, flat, m, v, A.workspace, stream)
+    x, y = torch.empty_like(m), torch.empty_like(v)
+    D.dopt_list_export(L, t, flat, x, y, A.workspace, stream)
+    assert torch.equal(flat, begin)
+    if state == "f32":
+        assert torch.equal(x, m) and torch.equal(y, v)
+    with pytest.raises(D.DoptError, match="overlaps param 0"):
+        D.dopt_list_export(L, t, x, flat, y, A.workspace, stream)
+    with pytest.raises(D.DoptError, match="overlaps the master array"):
+        D.dopt_list_export(L, t, x, x, y, A.workspace, stream)
+    with pytest.raises(D.DoptError, match="overlaps"):
+        D.dopt_list_export(L, t, x, A.state["exp_avg"].data_ptr(), y, A.workspace, stream)
