@@ -50,7 +50,8 @@ constexpr int kListPut = 240;
 // 1.2e8 fp32 params 0.592 (to 2^16) / 0.576; with e4m3 moments 1.0e9 params and fp32
 // grads 2.94 / 2.90 / 2.88 / 2.90 / 2.94, 1.2e8 bf16 0.333 (to 2^16) / 0.338; export of 1.0e9
 // 3.25 / 3.15 / 3.03 / 2.96 / 2.95.  Pass 1 only reads and loses by it (1.1e9 bf16 grads 328 us
-// in one launch, 435 at 2^15); its limit keeps a launch below 2^32 threads.
+// in one launch, 435 at 2^15): it takes a new launch, with partials of its own, after
+// 2^31 elements of a type pair only.  Its grid is bounded without that (list_stats_grid).
 constexpr int64_t kListStatsLaunch = int64_t(1) << 20;
 inline int64_t list_launch_tiles(int state_kind) { return int64_t(1) << (state_kind != DOPT_STATE_F32 ? 16 : 15); }
 
@@ -79,7 +80,9 @@ constexpr int32_t kListFused = 64;
 // loads, at 160 / 320 / 640 / 960 MB of grads: fp32 grads with e4m3 moments 148 / 137,
 // 282 / 270, 561 / 555, 826 / 833 us; bf16 ones with e4m3 moments 243 / 235, 477 / 469,
 // 943 / 947 us to 640 MB, with fp32 moments 397 / 375, 788 / 753, 1641 / 1619 us.
-// Pass 1 alone: 160 MB in 31 / 34 us, 2 GB in 293 / 330.
+// Pass 1 alone: 160 MB in 31 / 34 us, 2 GB in 293 / 330.  dopt_list_stats, which does not
+// know whether dopt_list_apply follows, goes by the same rule: a call for the norm alone
+// pays the 3 us, a step in parts gains the 7 to 11.
 constexpr int64_t kListKeep = int64_t(512) << 20;
 // Where the workspace counts pass 1's finished workgroups.
 constexpr int64_t kWsListDone = kWsRecord + 64;
