@@ -35,28 +35,29 @@
  * makes its scale, and so every element of the block, NaN.
  *
  * Over a run, nearest rounding does not follow the grads: an update moves
- * sqrt(v) by (1 - beta2)/2 * (g^2/v - 1) of itself, 0.05% with beta2 = 0.999, and
- * what stays below half a step of its code (3 to 6%) is lost every time, while
- * the scale follows the block's largest element and takes the others with it.
- * Against fp32 moments, Gaussian grads: sqrt(v) is off by 0.63 to 1.6 times (1st to 99th
- * percentile) and stays so; where the grads of half a block fall to a tenth,
- * their sqrt(v) is 8.6 times too large (median) 6500 steps later.
- * DOPT_STATE_E4M3 is thus for a few updates at a time (grads whose size does not
- * move, a state that is loaded, updated and compared).
+ * sqrt(v) by (1 - beta2)/2 * (g^2/v - 1) of itself, 0.05% with beta2 = 0.999,
+ * and what stays below half a step of its code (3 to 6%) is lost every time,
+ * while the scale follows the block's largest element and takes the others with
+ * it. Against fp32 moments, Gaussian grads: sqrt(v) is off by 0.63 to 1.6 times
+ * (1st to 99th percentile) and stays so; where the grads of half a block fall
+ * to a tenth, their sqrt(v) is 8.6 times too large (median) 6500 steps later.
+ * DOPT_STATE_E4M3 is thus for a few updates at a time (grads whose size does
+ * not move, a state that is loaded, updated and compared).
  *
  * DOPT_STATE_E4M3_SR holds the same codes and scales and is for whole runs: the
- * code is one of the two that x * (1 / scale) lies between, the farther one
- * with the probability that leaves the mean unchanged, so small changes add
- * up. sqrt(v) then stays within 0.7 to 1.4 times that of fp32 moments
- * (1st to 99th percentile) with a mean within 2%, and follows grads that grow or fall.
- * A nonzero sqrt(v) keeps a nonzero code here too. The random
- * numbers are a function of the list's seed (dopt_list_set_seed), the number of the step and
- * the element's place in the arena, and of nothing else: a
- * run that is repeated, resumed from a checkpoint of its codes or replayed from a captured graph takes
- * the same ones, and replicas with one seed stay equal. With k the element's arena
- * index, w the k % 4th word of Philox4x32-7 (Salmon, Moraes, Dror, Shaw: Parallel
- * random numbers: as easy as 1, 2, 3, 2011) of counter {k / 4, its high word, t, t's high word} and key
- * {seed, its high word}, t the step count after the step, and u = w mod 2^16 for m, w / 2^16 for sqrt(v):
+ * code is one of the two that x * (1 / scale) lies between, each with the
+ * probability that keeps the mean, so that small changes add up.
+ * sqrt(v) then stays within 0.7 to 1.4 times that of fp32 moments (1st to 99th
+ * percentile) with a mean within 2%, and follows grads that grow or fall. A
+ * nonzero sqrt(v) keeps a nonzero code here too. The random numbers are a
+ * function of the list's seed (dopt_list_set_seed), the number of the step and
+ * the element's place in the arena, and of nothing else: a run that is
+ * repeated, resumed from its codes, scales, step count and seed, or replayed
+ * from a captured graph takes the same ones, and replicas with one seed stay equal. With k the
+ * element's arena index, w word k % 4 of Philox4x32-7 (Salmon, Moraes,
+ * Dror, Shaw: Parallel random numbers: as easy as 1, 2, 3, 2011) of counter {k
+ * / 4, its high word, t, t's high word} and key {seed, its high word}, t the
+ * step count after the step, and u = w mod 2^16 for m, w / 2^16 for sqrt(v):
  *     y = |q| + 2^-6 if |q| < 2^-6 else |q|,   q = clamp(x * (1 / scale), -448, 448)
  *     the bits of y, plus 16 u + 8, without their lowest 20, are those of the code's magnitude (+ 2^-6)
  * An element is thereby within a step of e4m3 of its value (2^-3 of it, or 2^-9 * scale).
@@ -68,8 +69,8 @@
  * Conventions as in dopt.h: 0 or a negative DOPT_ERR_* code, stream-ordered,
  * nothing allocated on the device, no synchronization unless stated.  Calls
  * that use one workspace must not overlap in time.  dopt_list_stats,
- * _finalize, _prepare, _apply, _step (out == NULL), _export, _import and _set_seed only
- * launch kernels and may be captured into a HIP graph; a replay uses the
+ * _finalize, _prepare, _apply, _step (out == NULL), _export, _import and
+ * _set_seed only launch kernels and may be captured into a HIP graph; a replay uses the
  * addresses and hyper-parameters that the captured call was given.  A tensor
  * without a grad in a step has no place in that step's list: a null grad is
  * refused.
