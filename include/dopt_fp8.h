@@ -1,0 +1,143 @@
+/*
+ * dopt_fp8.h -- the 8-bit operators on either side of the step: the cast of
+ * params, activations and output grads to block-scaled e4m3, the product of
+ * two matrices so held, and the RMS norm with an 8-bit output and its backward
+ * pass.
+ *
+ * dopt.h and dopt_list.h step the params of a layer from its grads.  A linear
+ * layer that trains in 8 bits runs, between two steps,
+ *     y  = x W^T       dopt_rmsnorm (x in 8 bits), dopt_fp8_gemm
+ *     dx = dy W        dopt_fp8_cast of dy, dopt_fp8_gemm with the transposed W
+ *     dW += dy^T x     dopt_fp8_cast (transposed) of dy and x, dopt_fp8_gemm
+ * where W is cast once after each step from the params that the step wrote (or
+ * from its fp32 masters), and dW is added in place to the fp32 (or 16-bit)
+ * grads that the next step reads.  An inf or NaN anywhere on the way reaches
+ * dW as a NaN, where the step's overflow check finds it.
+ *
+ * The 8-bit format.  A matrix of rows x cols is cut into blocks that share a
+ * scale: DOPT_FP8_ROW, 128 consecutive elements of a row (activations and
+ * grads, whose rows differ in size), or DOPT_FP8_TILE, 128 x 128 elements
+ * (weights, so that the transposed weight has the same scales).  With A the
+ * largest magnitude among a block's finite elements and e the least integer
+ * >= -126 with A <= 448 * 2^e,
+ *     scale = 2^e, held in OCP e8m0 (one byte, e + 127)
+ *     code  = e4m3(x * 2^-e), nearest, ties to even; NaN for NaN and infinities
+ * (OCP e4m3: 1 sign, 4 exponent, 3 mantissa bits; largest 448).  The scaling
+ * is exact, so an element is within 2^-4 of its value, or within 2^-10 * scale
+ * if that is more.  A power of two costs no precision over A / 448 except to
+ * elements 2^-14 of the largest and smaller, of which it may cut one bit, and
+ * the matrix cores apply it without an instruction of its own.
+ *
+ * In memory (dopt_fp8_layout): rows of codes, `ld` bytes apart, of which the
+ * first cols rounded up to 128 belong to the matrix (the cast fills those past
+ * cols with zeros, and the product reads them); and for every 128 columns one
+ * row of scales, `scale_ld` bytes apart, with a byte per matrix row (ROW) or
+ * per 128 of them (TILE).  Scales past the matrix's last row belong to none:
+ * no call writes them and no result depends on them.  Rows i to j of a matrix
+ * are a matrix, with codes + i * ld and scales + i (ROW: i a multiple of 4) or
+ * scales + i / 128 (TILE: i a multiple of 128) and the same ld and scale_ld.
+ *
+ * Conventions as in dopt.h: 0 or a negative DOPT_ERR_* code, stream-ordered,
+ * nothing allocated, nothing synchronized.  Every call only launches kernels
+ * and may be captured into a HIP graph.  Calls that are given one workspace
+ * must not overlap in time.  A workspace needs no initialisation.  Results do
+ * not depend on timing: no atomics, sums in a fixed order.  Sizes may be 0.
+ * An output may not overlap an input or another output, but where a call says
+ * so; DOPT_ERR_INVALID otherwise.
+ */
+#ifndef DOPT_FP8_H
+#define DOPT_FP8_H
+
+#include "dopt.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum { DOPT_FP8_ROW = 0, DOPT_FP8_TILE = 1 };
+
+/* Elements along a row, and for TILE rows, of a block. */
+#define DOPT_FP8_BLOCK 128
+/* Columns of a matrix of either kind are at most this many; rows at most 2^31 - 1. */
+#define DOPT_FP8_MAX_COLS (1 << 22)
+
+/* A matrix in the 8-bit format (device addresses). */
+typedef struct dopt_fp8_matrix {
+    void *codes;      /* 16-byte aligned */
+    void *scales;     /* 4-byte aligned (ROW) */
+    int64_t rows, cols;
+    int64_t ld;       /* bytes, a multiple of 16, >= cols rounded up to 128, <= DOPT_FP8_MAX_COLS */
+    int64_t scale_ld; /* bytes, >= rows (ROW: a multiple of 4) or ceil(rows / 128) (TILE) */
+    int32_t kind, reserved;
+} dopt_fp8_matrix;
+
+/* A matrix of fp32, bf16 or fp16 elements, aligned to its element; columns lie next to each other. */
+typedef struct dopt_dense {
+    void *data;
+    int64_t rows, cols;
+    int64_t ld;       /* elements between rows, >= cols, < 2^23 */
+    int32_t dtype, reserved;
+} dopt_dense;
+
+typedef struct dopt_fp8_sizes {
+    int64_t ld, scale_ld;              /* cols rounded up to 128; rows rounded up to 16, or ceil(rows / 128) */
+    int64_t codes_bytes, scales_bytes; /* of allocations that hold the matrix */
+} dopt_fp8_sizes;
+
+/* dopt_fp8_layout -- the usual layout of a matrix of rows x cols.  Errors: DOPT_ERR_INVALID. */
+int dopt_fp8_layout(int64_t rows, int64_t cols, int32_t kind, dopt_fp8_sizes *out);
+
+/*
+ * dopt_fp8_cast -- x to 8 bits: `codes` receives x (x->rows x x->cols) and
+ * `transposed` its transpose (x->cols x x->rows); either may be NULL, and
+ * both are of one kind.  With row_factor and col_factor (x->rows fp32 and
+ * x->cols elements of col_dtype; both or neither), what is cast is
+ * (x[r][c] * row_factor[r]) * col_factor[c], each product rounded to fp32:
+ * with dopt_rmsnorm's rstd and weight, the norm's output from its kept input.
+ */
+int dopt_fp8_cast(const dopt_dense *x, const float *row_factor, const void *col_factor, int32_t col_dtype,
+                  const dopt_fp8_matrix *codes, const dopt_fp8_matrix *transposed, hipStream_t stream);
+
+/*
+ * dopt_fp8_gemm -- out[m][n] = sum over k of a[m][k] * b[n][k], plus
+ * out[m][n] if `accumulate`.  a (kind ROW) is M x K, b (either kind) N x K, out
+ * M x N; sums in fp32, one rounding to out's type.  The workspace holds
+ * dopt_fp8_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned; where that is
+ * 0 it may be NULL.
+ */
+int64_t dopt_fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int dopt_fp8_gemm(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, const dopt_dense *out, int32_t accumulate,
+                  void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * dopt_rmsnorm -- per row of x (and residual, NULL: none), of one type:
+ *     h    = x + residual, rounded to their type
+ *     rstd = 1 / sqrt(mean(h^2) + eps)
+ *     y    = (h * rstd) * weight, each product rounded to fp32
+ * h (NULL: not kept; may be x or residual itself), rstd (fp32, one per row;
+ * NULL: not kept) and y: `y` in x's type, `q` in 8 bits (kind ROW), or both.
+ * The weight is x->cols elements of weight_dtype.  Statistics in fp32.
+ */
+int dopt_rmsnorm(const dopt_dense *x, const dopt_dense *residual, const void *weight, int32_t weight_dtype, double eps,
+                 const dopt_dense *h, const dopt_dense *y, const dopt_fp8_matrix *q, float *rstd, hipStream_t stream);
+
+/*
+ * dopt_rmsnorm_grad -- the backward pass, from the grad dy of y (h's type or
+ * fp32) and what the forward pass kept.  Per row, with g = dy * weight:
+ *     dx = dh + rstd * (g - h * (rstd^2 * mean(g * h)))
+ *     dweight[c] = sum over rows of dy[r][c] * (h[r][c] * rstd[r]), plus dweight[c] if `accumulate`
+ * dh (NULL: 0) is the grad that reaches h past the norm, in h's type; dx, in
+ * h's type, is the grad of x and of the residual, and may be dh or dy itself.  dweight is
+ * h->cols elements of dweight_dtype, sums in fp32.  The workspace holds
+ * dopt_rmsnorm_grad_workspace_bytes(rows, cols) bytes, 16-byte aligned.
+ */
+int64_t dopt_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
+int dopt_rmsnorm_grad(const dopt_dense *dy, const dopt_dense *h, const dopt_dense *dh, const void *weight,
+                      int32_t weight_dtype, const float *rstd, const dopt_dense *dx, void *dweight,
+                      int32_t dweight_dtype, int32_t accumulate, void *workspace, int64_t workspace_bytes,
+                      hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

@@ -1,10 +1,11 @@
 """Python binding of libdopt.so, the shard-local mixed-precision AdamW step
-of a ZeRO-1 distributed optimizer for AMD Instinct MI355X (gfx950), and the
-same step over a list of separate tensors with fp32 or 8-bit moments.
+of a ZeRO-1 distributed optimizer for AMD Instinct MI355X (gfx950), the
+same step over a list of separate tensors with fp32 or 8-bit moments, and the
+8-bit operators around it: casts, products and RMS norms.
 
 Argument marshalling only: every computation happens in the library (host
 range mapper in C++, the step in HIP kernels).  Function names match the C
-ABI in include/dopt.h and include/dopt_list.h.  Device buffers may be given as PyTorch CUDA tensors
+ABI in include/dopt.h, include/dopt_list.h and include/dopt_fp8.h.  Device buffers may be given as PyTorch CUDA tensors
 or raw integer addresses; PyTorch is used only to own device memory and
 streams.  There is no fallback: if the library is not built, import fails.
 """
@@ -32,6 +33,10 @@ DOPT_STATE_F32, DOPT_STATE_E4M3, DOPT_STATE_E4M3_SR = 0, 1, 3
 STATE_KINDS = {"f32": DOPT_STATE_F32, "e4m3": DOPT_STATE_E4M3, "e4m3_sr": DOPT_STATE_E4M3_SR}
 STATE_NAMES = {v: k for k, v in STATE_KINDS.items()}
 DOPT_LIST_BLOCK = 128
+
+DOPT_FP8_ROW, DOPT_FP8_TILE = 0, 1
+FP8_KINDS = {"row": DOPT_FP8_ROW, "tile": DOPT_FP8_TILE}
+DOPT_FP8_BLOCK = 128
 
 
 class DoptError(RuntimeError):
@@ -141,6 +146,22 @@ class dopt_list_state(ctypes.Structure):
                 ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p)]
 
 
+class dopt_fp8_matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("scale_ld", ctypes.c_int64),
+                ("kind", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class dopt_dense(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class dopt_fp8_sizes(ctypes.Structure):
+    _fields_ = [("ld", ctypes.c_int64), ("scale_ld", ctypes.c_int64), ("codes_bytes", ctypes.c_int64),
+                ("scales_bytes", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() or "
@@ -194,6 +215,15 @@ def _load():
         "dopt_list_scalars_get": ([VP, VP, VP, P(dopt_state_scalars)], ctypes.c_int),
         "dopt_list_scalars_set": ([VP, VP, VP, P(dopt_state_scalars)], ctypes.c_int),
         "dopt_list_read_stats": ([VP, VP, VP, P(dopt_stats)], ctypes.c_int),
+        "dopt_fp8_layout": ([I64, I64, I32, P(dopt_fp8_sizes)], ctypes.c_int),
+        "dopt_fp8_cast": ([P(dopt_dense), VP, VP, I32, P(dopt_fp8_matrix), P(dopt_fp8_matrix), VP], ctypes.c_int),
+        "dopt_fp8_gemm_workspace_bytes": ([I64, I64, I64], I64),
+        "dopt_fp8_gemm": ([P(dopt_fp8_matrix), P(dopt_fp8_matrix), P(dopt_dense), I32, VP, I64, VP], ctypes.c_int),
+        "dopt_rmsnorm": ([P(dopt_dense), P(dopt_dense), VP, I32, D, P(dopt_dense), P(dopt_dense), P(dopt_fp8_matrix),
+                          VP, VP], ctypes.c_int),
+        "dopt_rmsnorm_grad_workspace_bytes": ([I64, I64], I64),
+        "dopt_rmsnorm_grad": ([P(dopt_dense), P(dopt_dense), P(dopt_dense), VP, I32, VP, P(dopt_dense), VP, I32, I32, VP,
+                               I64, VP], ctypes.c_int),
         "dopt_vmm_granularity": ([I32, P(ctypes.c_size_t)], ctypes.c_int),
         "dopt_vmm_reserve": ([ctypes.c_size_t, ctypes.c_size_t, P(ctypes.c_uint64)], ctypes.c_int),
         "dopt_vmm_free": ([ctypes.c_uint64, ctypes.c_size_t], ctypes.c_int),
@@ -225,6 +255,8 @@ EXPORTED = ("dopt_build_ranges", "dopt_layout_free", "dopt_layout_num_buffers", 
             "dopt_list_init", "dopt_list_step", "dopt_list_prepare", "dopt_list_stats", "dopt_list_finalize",
             "dopt_list_apply", "dopt_list_export", "dopt_list_import", "dopt_list_set_seed", "dopt_list_scalars_get",
             "dopt_list_scalars_set", "dopt_list_read_stats",
+            "dopt_fp8_layout", "dopt_fp8_cast", "dopt_fp8_gemm_workspace_bytes", "dopt_fp8_gemm", "dopt_rmsnorm",
+            "dopt_rmsnorm_grad_workspace_bytes", "dopt_rmsnorm_grad",
             "dopt_vmm_granularity", "dopt_vmm_reserve", "dopt_vmm_free", "dopt_vmm_create", "dopt_vmm_map",
             "dopt_vmm_set_access", "dopt_vmm_unmap", "dopt_vmm_release")
 
@@ -894,6 +926,193 @@ def dopt_list_read_stats(lst: TensorList, workspace, stream=None) -> Dict:
     st = dopt_stats()
     _check(_lib.dopt_list_read_stats(lst.handle, *_list_ws(lst, workspace, stream), ctypes.byref(st)))
     return st.as_dict()
+
+
+# ---- the 8-bit operators around the step (include/dopt_fp8.h) ----
+
+_dtype_ids: Dict = {}  # torch element type -> DOPT_* of the types seen
+
+
+def _dtype_id(dt, what) -> int:
+    i = _dtype_ids.get(dt)
+    if i is None:
+        i = {"torch.float32": DOPT_F32, "torch.bfloat16": DOPT_BF16, "torch.float16": DOPT_F16}.get(str(dt))
+        if i is None:
+            raise DoptError(DOPT_ERR_INVALID, f"{what}: dtype {dt} is not fp32, bf16 or fp16")
+        _dtype_ids[dt] = i
+    return i
+
+
+def _here(x, what, device: int):
+    """Refuses a tensor that is not on the device that the call is launched on."""
+    if not x.is_cuda:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: not a device tensor")
+    if x.get_device() != device:
+        _elsewhere(what, x.get_device())
+
+
+def _dense(x, what, device: int) -> Optional[dopt_dense]:
+    """A 2-d tensor whose rows' elements lie next to each other."""
+    if x is None:
+        return None
+    if x.dim() != 2:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: {x.dim()} dimensions, a matrix has 2")
+    rows, cols = x.shape
+    ld, step = x.stride()
+    if cols > 1 and step != 1:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: the elements of a row do not lie next to each other")
+    if rows > 1 and ld < cols:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: rows overlap")
+    _here(x, what, device)
+    return dopt_dense(x.data_ptr(), rows, cols, ld if rows > 1 else cols, _dtype_id(x.dtype, what), 0)
+
+
+def _vector(x, what, n: int, device: int, dtype=None):
+    """(address, DOPT_* type) of a contiguous vector of n elements."""
+    if x is None:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: missing")
+    i = _dtype_id(x.dtype, what)
+    if dtype is not None and i != dtype:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: dtype {x.dtype}, {DTYPE_NAMES[dtype]} is needed")
+    if x.numel() != n:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: {x.numel()} elements, {n} are needed")
+    if not x.is_contiguous():
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: not contiguous")
+    _here(x, what, device)
+    return x.data_ptr(), i
+
+
+def _scratch(x, device: int):
+    """(address, bytes) of a workspace."""
+    if x is None:
+        return None, 0
+    if not x.is_contiguous():
+        raise DoptError(DOPT_ERR_INVALID, "workspace: not contiguous")
+    _here(x, "workspace", device)
+    return x.data_ptr(), x.numel() * x.element_size()
+
+
+def _on(stream, device: int) -> Optional[int]:
+    if stream is None or isinstance(stream, int):
+        return stream
+    if stream.device.index != device:
+        _elsewhere("stream", stream.device.index)
+    return stream.cuda_stream
+
+
+class Fp8Matrix:
+    """A matrix in the 8-bit format: .codes (rows x at least cols rounded up to
+    128, torch.float8_e4m3fn or uint8), .scales (a row per 128 columns,
+    torch.float8_e8m0fnu or uint8), .rows, .cols and .kind ('row' | 'tile').
+    Make it with fp8_matrix() or arena.fp8_alloc()."""
+
+    def __init__(self, codes, scales, rows: int, cols: int, kind: str, struct: dopt_fp8_matrix, device: int):
+        self.codes, self.scales, self.rows, self.cols, self.kind = codes, scales, rows, cols, kind
+        self.struct, self.device = struct, device
+
+
+def fp8_matrix(codes, scales, rows: int, cols: int, kind: str = "row") -> Fp8Matrix:
+    """Codes and scales, checked against the sizes, as the matrix that the calls
+    take.  Rows of both may be farther apart than they are long."""
+    if kind not in FP8_KINDS:
+        raise DoptError(DOPT_ERR_INVALID, f"kind {kind!r}: one of {sorted(FP8_KINDS)}")
+    groups, row = -(-cols // DOPT_FP8_BLOCK), kind == "row"
+    for x, what, shape in ((codes, "codes", (rows, groups * DOPT_FP8_BLOCK)),
+                           (scales, "scales", (groups, -(-rows // 4) * 4 if row else -(-rows // DOPT_FP8_BLOCK)))):
+        if x.element_size() != 1 or x.dim() != 2:
+            raise DoptError(DOPT_ERR_INVALID, f"{what}: not a matrix of bytes")
+        if x.shape[0] != shape[0] or x.shape[1] < shape[1]:
+            raise DoptError(DOPT_ERR_INVALID, f"{what}: {tuple(x.shape)}, {shape} is needed")
+        if not x.is_cuda:
+            raise DoptError(DOPT_ERR_INVALID, f"{what}: not a device tensor")
+        if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+            raise DoptError(DOPT_ERR_INVALID, f"{what}: the elements of a row do not lie next to each other, or rows overlap")
+    if codes.get_device() != scales.get_device():
+        raise DoptError(DOPT_ERR_INVALID, "codes and scales are on different devices")
+    ld = codes.stride(0) if rows > 1 else groups * DOPT_FP8_BLOCK
+    scale_ld = scales.stride(0) if groups > 1 else (-(-rows // 4) * 4 if row else -(-rows // DOPT_FP8_BLOCK))
+    st = dopt_fp8_matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, ld, scale_ld, FP8_KINDS[kind], 0)
+    return Fp8Matrix(codes, scales, rows, cols, kind, st, codes.get_device())
+
+
+def dopt_fp8_layout(rows: int, cols: int, kind: str = "row") -> Dict:
+    if kind not in FP8_KINDS:
+        raise DoptError(DOPT_ERR_INVALID, f"kind {kind!r}: one of {sorted(FP8_KINDS)}")
+    o = dopt_fp8_sizes()
+    _check(_lib.dopt_fp8_layout(rows, cols, FP8_KINDS[kind], ctypes.byref(o)))
+    return {name: getattr(o, name) for name, _ in o._fields_}
+
+
+def _fp8(x: Optional[Fp8Matrix], what, device: int) -> Optional[dopt_fp8_matrix]:
+    if x is None:
+        return None
+    if x.device != device:
+        _elsewhere(what, x.device)
+    return x.struct
+
+
+def dopt_fp8_cast(x, codes: Optional[Fp8Matrix] = None, transposed: Optional[Fp8Matrix] = None, row_factor=None,
+                  col_factor=None, stream=None):
+    """x (a matrix of fp32, bf16 or fp16) to 8 bits, its transpose, or both,
+    with x[r][c] * row_factor[r] * col_factor[c] in x's place if factors are given."""
+    d = _current_device()
+    xd = _dense(x, "x", d)
+    if (row_factor is None) != (col_factor is None):
+        raise DoptError(DOPT_ERR_INVALID, "row and column factors come together")
+    r, c, ct = None, None, DOPT_F32
+    if row_factor is not None:
+        r, _ = _vector(row_factor, "row_factor", xd.rows, d, DOPT_F32)
+        c, ct = _vector(col_factor, "col_factor", xd.cols, d)
+    _check(_lib.dopt_fp8_cast(xd, r, c, ct, _fp8(codes, "codes", d), _fp8(transposed, "transposed", d), _on(stream, d)))
+
+
+def _bytes(n: int) -> int:
+    if n < 0:
+        _check(int(n))
+    return int(n)
+
+
+def dopt_fp8_gemm_workspace_bytes(m: int, n: int, k: int) -> int:
+    return _bytes(_lib.dopt_fp8_gemm_workspace_bytes(m, n, k))
+
+
+def dopt_fp8_gemm(a: Fp8Matrix, b: Fp8Matrix, out, accumulate: bool = False, workspace=None, stream=None):
+    """out (+)= a b^T; a of kind 'row', b of either, both with k as columns."""
+    d = _current_device()
+    ws, nbytes = _scratch(workspace, d)
+    _check(_lib.dopt_fp8_gemm(_fp8(a, "a", d), _fp8(b, "b", d), _dense(out, "out", d), accumulate, ws, nbytes,
+                              _on(stream, d)))
+
+
+def dopt_rmsnorm(x, weight, eps: float, residual=None, h=None, y=None, q: Optional[Fp8Matrix] = None, rstd=None,
+                 stream=None):
+    """The RMS norm of x + residual: y in x's type, q in 8 bits, or both; h (the
+    sum, which may be x or residual itself) and rstd are what the backward pass takes."""
+    d = _current_device()
+    xd = _dense(x, "x", d)
+    w, wt = _vector(weight, "weight", xd.cols, d)
+    r = None if rstd is None else _vector(rstd, "rstd", xd.rows, d, DOPT_F32)[0]
+    _check(_lib.dopt_rmsnorm(xd, _dense(residual, "residual", d), w, wt, eps, _dense(h, "h", d), _dense(y, "y", d),
+                             _fp8(q, "q", d), r, _on(stream, d)))
+
+
+def dopt_rmsnorm_grad_workspace_bytes(rows: int, cols: int) -> int:
+    return _bytes(_lib.dopt_rmsnorm_grad_workspace_bytes(rows, cols))
+
+
+def dopt_rmsnorm_grad(dy, h, weight, rstd, dx, dweight, dh=None, accumulate: bool = False, workspace=None, stream=None):
+    """The norm's backward pass: dx (the grad of x and of the residual, dh
+    added; may be dh or dy itself) and dweight, added to with `accumulate`."""
+    d = _current_device()
+    hd = _dense(h, "h", d)
+    if hd is None:
+        raise DoptError(DOPT_ERR_INVALID, "h: missing")
+    w, wt = _vector(weight, "weight", hd.cols, d)
+    g, gt = _vector(dweight, "dweight", hd.cols, d)
+    r, _ = _vector(rstd, "rstd", hd.rows, d, DOPT_F32)
+    ws, nbytes = _scratch(workspace, d)
+    _check(_lib.dopt_rmsnorm_grad(_dense(dy, "dy", d), hd, _dense(dh, "dh", d), w, wt, r, _dense(dx, "dx", d), g, gt,
+                                  accumulate, ws, nbytes, _on(stream, d)))
 
 
 # ---- device-memory placement helpers (include/dopt_vmm.h) ----

@@ -40,7 +40,8 @@ from typing import Dict, List, Optional, Tuple
 
 import torch
 
-from . import DOPT_MAX_HGROUPS, DTYPE_NAMES, Layout, TensorList
+from . import (DOPT_FP8_BLOCK, DOPT_MAX_HGROUPS, DTYPE_NAMES, Fp8Matrix, Layout, TensorList, dopt_fp8_layout,
+               fp8_matrix)
 
 TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 ES = {"f32": 4, "bf16": 2, "f16": 2}
@@ -444,3 +445,12 @@ class ListArrays:
 
     def state_bytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in self.state.values()) + self.workspace.numel()
+
+
+def fp8_alloc(rows: int, cols: int, kind: str = "row", device: str = "cuda") -> Fp8Matrix:
+    """A matrix in the 8-bit format, plain PyTorch allocations (uninitialised)."""
+    at = dopt_fp8_layout(rows, cols, kind)
+    codes = torch.empty(rows, at["ld"], dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+    groups = -(-cols // DOPT_FP8_BLOCK)
+    scales = torch.empty(groups, at["scale_ld"], dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
+    return fp8_matrix(codes, scales, rows, cols, kind)

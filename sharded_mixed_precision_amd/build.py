@@ -10,7 +10,8 @@ ROOT = os.path.dirname(HERE)
 SO = os.path.join(HERE, "libdopt.so")
 SOURCES = [os.path.join(HERE, "csrc", "mapper.cpp"), os.path.join(HERE, "csrc", "step.hip"),
            os.path.join(HERE, "csrc", "list.cpp"), os.path.join(HERE, "csrc", "list.hip"),
-           os.path.join(HERE, "csrc", "vmm.cpp")]
+           os.path.join(HERE, "csrc", "fp8.hip"), os.path.join(HERE, "csrc", "gemm.hip"),
+           os.path.join(HERE, "csrc", "norm.hip"), os.path.join(HERE, "csrc", "vmm.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,502 @@
+// The product of two matrices of block-scaled e4m3 (dopt_fp8_gemm).
+#include <algorithm>
+#include <string>
+#include <utility>
+
+#include "fp8.h"
+
+namespace dopt {
+
+using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
+using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
+
+constexpr int kStep = DOPT_FP8_BLOCK;  // bytes of a row, and elements of k, per step
+
+struct GemmArgs {
+    const uint8_t *a, *b, *as, *bs;
+    void *out;
+    float *part;  // splits > 1: fp32 sums, [splits][m][part_ld]
+    int64_t as_ld, bs_ld, out_ld, part_ld;
+    int32_t a_ld, b_ld;
+    int32_t m, n, steps;  // steps of 128 along k
+    int32_t tiles_m, tiles_n, splits, split_steps;
+    int32_t dtype, accumulate;
+};
+
+// ---- output -----------------------------------------------------------------------
+
+struct __attribute__((packed, aligned(4))) Float4 {
+    f32x4 v;
+};
+
+template <int T>
+__device__ __forceinline__ void put4_as(void *out, int64_t e, int n, f32x4 x, bool add) {
+    if constexpr (T == DOPT_F32) {
+        float *p = static_cast<float *>(out) + e;
+        if (n >= 4) {
+            Float4 *w = reinterpret_cast<Float4 *>(p);
+            if (add) x += w->v;
+            w->v = x;
+        } else {
+            for (int i = 0; i < n; ++i) p[i] = add ? p[i] + x[i] : x[i];
+        }
+    } else {
+        uint16_t *p = static_cast<uint16_t *>(out) + e;
+        if (n >= 4) {
+            Bytes8 *w = reinterpret_cast<Bytes8 *>(p);
+            if (add) {
+                const u32x2 o = w->v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] += to_float<T>(i % 2 ? o[i / 2] >> 16 : o[i / 2] & 0xffffu);
+            }
+            u32x2 r;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) r[i] = from_float<T>(x[2 * i]) | from_float<T>(x[2 * i + 1]) << 16;
+            w->v = r;
+        } else {
+            for (int i = 0; i < n; ++i) p[i] = static_cast<uint16_t>(from_float<T>(add ? to_float<T>(p[i]) + x[i] : x[i]));
+        }
+    }
+}
+
+// Elements [col, col + 4) of out's row, as far as they exist.
+__device__ __forceinline__ void put4(const GemmArgs &A, int row, int col, f32x4 x) {
+    if (row >= A.m || col >= A.n) return;
+    const int64_t e = static_cast<int64_t>(row) * A.out_ld + col;
+    const int n = A.n - col;
+    if (A.dtype == DOPT_F32) put4_as<DOPT_F32>(A.out, e, n, x, A.accumulate);
+    else if (A.dtype == DOPT_BF16) put4_as<DOPT_BF16>(A.out, e, n, x, A.accumulate);
+    else put4_as<DOPT_F16>(A.out, e, n, x, A.accumulate);
+}
+
+// A split's sums; rows of part are padded to 4.
+__device__ __forceinline__ void put4_part(const GemmArgs &A, int split, int row, int col, f32x4 x) {
+    if (row >= A.m || col >= A.n) return;
+    *reinterpret_cast<f32x4 *>(A.part + (static_cast<int64_t>(split) * A.m + row) * A.part_ld + col) = x;
+}
+
+__global__ __launch_bounds__(256) void k_gemm_join(GemmArgs A) {
+    const int per_row = static_cast<int>(A.part_ld / 4);
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= static_cast<int64_t>(A.m) * per_row) return;
+    const int row = static_cast<int>(i / per_row), col = static_cast<int>(i % per_row) * 4;
+    f32x4 x = {0, 0, 0, 0};
+    for (int s = 0; s < A.splits; ++s)
+        x += *reinterpret_cast<const f32x4 *>(A.part + (static_cast<int64_t>(s) * A.m + row) * A.part_ld + col);
+    put4(A, row, col, x);
+}
+
+// ---- one step's products ------------------------------------------------------------
+
+// Two ways to multiply, chosen by the output's type.
+//
+// 16-bit outputs: the matrix instruction that takes e4m3 codes and applies the
+// scales itself.  It adds 8 neighbouring products of k with 14 bits below the
+// largest of them, and such sums to one another and to the accumulator in
+// fp32 (measured: a product 2^-14 of the largest in its 8 is lost, one 2^-23 of it in
+// another 8 is kept).  On random operands a result is thereby off by 3 to 5e-5 of
+// the output's root mean square, a fifth of fp16's own rounding and a fortieth of bf16's.
+//
+// fp32 outputs, which would keep that error: the codes become bf16 with their
+// scale applied (exact: 4 bits of mantissa, and the scale is a power of two)
+// in registers, and the bf16 instruction multiplies, whose products and sums are
+// fp32's (1e-7 of the result), at half the codes' rate.
+//
+// A lane holds 32 codes of row (lane % 16) of either operand; which of a step's 128
+// does not matter as long as both take the same.
+__device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The scale in byte I of a dword.
+template <int I>
+__device__ __forceinline__ float scale_of(int bytes) {
+    return __uint_as_float((static_cast<uint32_t>(bytes) >> (8 * I) & 0xffu) << 23);
+}
+
+// c += a x b over 128 of k; a's and b's scales are byte I and J of a dword per lane.
+template <int I, int J>
+__device__ __forceinline__ f32x4 mfma(i32x8 a, i32x8 b, f32x4 c, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, I, sa, J, sb);
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// f(0) to f(3) with numbers that the compiler knows, as the byte selectors have to be.
+template <class F>
+__device__ __forceinline__ void each4(const F &f) {
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
+}
+
+// ---- tiles ------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)p));
+}
+
+// 16 (or 4) bytes per lane from base + offset to shared memory at `to` + 16 (4) * lane, past
+// the registers.  The compiler does not know of the load: the kernel waits for it.
+__device__ __forceinline__ void load_lds16(uint32_t to, uint32_t offset, const uint8_t *base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds4(uint32_t to, uint32_t offset, const uint8_t *base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+
+// A workgroup forms BM x BN of the output with WM x WN waves, each a part of
+// (BM / WM) x (BN / WN).  Per step of 128 along k, both operands' rows come
+// to shared memory, the next step's while this one's are multiplied.
+//
+// In shared memory a group of 64 rows lies in the order 0, 4, 8, .. 60, 1, 5, ..:
+// slot 16 i + r holds row 4 r + i.  The matrix instruction that takes slots 16 i
+// to 16 i + 15 thereby finds its rows' scales in byte i of the dword of row
+// 4 r, one dword for four instructions, and a lane's four results along
+// a row of the output are neighbours, which are stored at once.  Within a slot's
+// 128 bytes the 16-byte chunk c lies at c ^ (r / 2), which spreads the
+// 16 rows that a quarter of a wave reads over all banks.
+template <int BM, int BN, int WM, int WN, bool BROW, bool EXACT>
+__global__ __launch_bounds__(WM *WN * 64, 2) void k_gemm_tile(GemmArgs A) {
+    constexpr int kWaves = WM * WN;
+    constexpr int GA = BM / WM / 64, GB = BN / WN / 64;
+    constexpr int kA = BM * kStep, kB = BN * kStep;
+    constexpr int kBuffer = kA + kB + 512;  // and 256 bytes of scales for each
+    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;
+    __shared__ __align__(16) uint8_t s_mem[2 * kBuffer];
+
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = wave / WN, wn = wave % WN;
+
+    // each XCD takes neighbouring tiles, in bands of 8 tile rows, so that its L2 serves them all
+    int tile;
+    {
+        const int total = A.tiles_m * A.tiles_n, q = total / 8, rem = total % 8;
+        const int x = blockIdx.x % 8, i = blockIdx.x / 8;
+        tile = x * q + min(x, rem) + i;
+    }
+    constexpr int kBand = 8;
+    const int band = tile / (kBand * A.tiles_n), in_band = tile % (kBand * A.tiles_n);
+    const int height = min(kBand, A.tiles_m - band * kBand);
+    const int m0 = (band * kBand + in_band % height) * BM, n0 = in_band / height * BN;
+
+    const int split = blockIdx.y;
+    const int first = split * A.split_steps, steps = min(A.split_steps, A.steps - first);
+
+    // rows past the last are read as the last: their results are not stored
+    const uint8_t *pa = A.a + static_cast<int64_t>(m0) * A.a_ld + static_cast<int64_t>(first) * kStep;
+    const uint8_t *pb = A.b + static_cast<int64_t>(n0) * A.b_ld + static_cast<int64_t>(first) * kStep;
+    uint32_t off_a[kLoadsA], off_b[kLoadsB];
+    const auto place = [&](int load, int rows, int ld) {  // where a lane's 16 bytes of a load lie in the operand
+        const int slot = 8 * load + lane / 8, r = slot % 16;
+        const int row = min(slot / 64 * 64 + 4 * r + slot % 64 / 16, rows - 1);
+        return static_cast<uint32_t>(row) * static_cast<uint32_t>(ld) + 16u * ((lane % 8) ^ (r / 2));
+    };
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i) off_a[i] = place(wave * kLoadsA + i, A.m - m0, A.a_ld);
+#pragma unroll
+    for (int i = 0; i < kLoadsB; ++i) off_b[i] = place(wave * kLoadsB + i, A.n - n0, A.b_ld);
+    const uint8_t *psa = A.as + first * A.as_ld, *psb = A.bs + first * A.bs_ld;
+    const uint32_t off_sa = min(m0 + 4 * lane, (A.m + 3) / 4 * 4 - 4);
+    const uint32_t off_sb = min(n0 + 4 * lane, (A.n + 3) / 4 * 4 - 4);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(s_mem));
+
+    const auto fetch = [&](int buffer) {
+        const uint32_t to = lds + buffer * kBuffer;
+#pragma unroll
+        for (int i = 0; i < kLoadsA; ++i) load_lds16(to + 1024 * (wave * kLoadsA + i), off_a[i], pa);
+#pragma unroll
+        for (int i = 0; i < kLoadsB; ++i) load_lds16(to + kA + 1024 * (wave * kLoadsB + i), off_b[i], pb);
+        if (wave == 0) load_lds4(to + kA + kB, off_sa, psa);
+        if (BROW && wave == 1) load_lds4(to + kA + kB + 256, off_sb, psb);
+        pa += kStep;
+        pb += kStep;
+        psa += A.as_ld;
+        psb += A.bs_ld;
+    };
+    const auto settle = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+    f32x4 acc[4 * GA][4 * GB];
+#pragma unroll
+    for (int i = 0; i < 4 * GA; ++i)
+#pragma unroll
+        for (int j = 0; j < 4 * GB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    const int r = lane % 16, quarter = lane / 16;
+    // a lane takes chunks quarter and quarter + 4 of its row
+    const uint32_t low = r * kStep + 16 * (quarter ^ (r / 2)), high = r * kStep + 16 * ((quarter + 4) ^ (r / 2));
+    // TILE: lane l holds the scale of the wave's columns at step 64 j + l
+    const int block = min(n0 + wn * (BN / WN), A.n - 1) / DOPT_FP8_BLOCK;
+    int tile_scales = 0;
+
+    if (steps > 0) fetch(0);
+    settle();
+    for (int k = 0; k < steps; ++k) {
+        if (!BROW && k % 64 == 0) {
+            tile_scales = A.bs[static_cast<int64_t>(first + min(k + lane, steps - 1)) * A.bs_ld + block];
+            asm volatile("" : "+v"(tile_scales));  // waited for here, before the step's loads are under way
+        }
+        if (k + 1 < steps) fetch((k + 1) & 1);
+        const uint8_t *mem = s_mem + (k & 1) * kBuffer;
+        const uint8_t *ma = mem + wm * (BM / WM) * kStep, *mb = mem + kA + wn * (BN / WN) * kStep;
+        const uint8_t *ms = mem + kA + kB;
+        int sa[GA], sb[GB];
+#pragma unroll
+        for (int g = 0; g < GA; ++g) sa[g] = *reinterpret_cast<const int *>(ms + wm * (BM / WM) + 64 * g + 4 * r);
+#pragma unroll
+        for (int g = 0; g < GB; ++g) {
+            if (BROW) sb[g] = *reinterpret_cast<const int *>(ms + 256 + wn * (BN / WN) + 64 * g + 4 * r);
+            else sb[g] = __builtin_amdgcn_readlane(tile_scales, k % 64) * 0x01010101;
+        }
+        if constexpr (EXACT) {
+            // half a step at a time, so that the widened codes fit the registers
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t at = half ? high : low;
+                bf16x8 b[4 * GB][2];
+                each4([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+#pragma unroll
+                    for (int h = 0; h < GB; ++h) {
+                        const i32x4 w = *reinterpret_cast<const i32x4 *>(mb + 16 * (4 * h + j) * kStep + at);
+                        const float scale = scale_of<j>(sb[h]);
+                        b[4 * h + j][0] = widen8(w[0], w[1], scale);
+                        b[4 * h + j][1] = widen8(w[2], w[3], scale);
+                    }
+                });
+#pragma unroll
+                for (int g = 0; g < GA; ++g)
+                    each4([&](auto I) {
+                        constexpr int i = decltype(I)::value;
+                        const i32x4 w = *reinterpret_cast<const i32x4 *>(ma + 16 * (4 * g + i) * kStep + at);
+                        const float scale = scale_of<i>(sa[g]);
+                        const bf16x8 a0 = widen8(w[0], w[1], scale), a1 = widen8(w[2], w[3], scale);
+#pragma unroll
+                        for (int j = 0; j < 4 * GB; ++j) acc[4 * g + i][j] = mfma(a0, b[j][0], acc[4 * g + i][j]);
+#pragma unroll
+                        for (int j = 0; j < 4 * GB; ++j) acc[4 * g + i][j] = mfma(a1, b[j][1], acc[4 * g + i][j]);
+                    });
+            }
+        } else {
+            i32x8 b[4 * GB];
+#pragma unroll
+            for (int j = 0; j < 4 * GB; ++j)
+                b[j] = join(*reinterpret_cast<const i32x4 *>(mb + 16 * j * kStep + low), *reinterpret_cast<const i32x4 *>(mb + 16 * j * kStep + high));
+#pragma unroll
+            for (int g = 0; g < GA; ++g)
+                each4([&](auto I) {
+                    constexpr int i = decltype(I)::value;
+                    const uint8_t *p = ma + 16 * (4 * g + i) * kStep;
+                    const i32x8 a = join(*reinterpret_cast<const i32x4 *>(p + low), *reinterpret_cast<const i32x4 *>(p + high));
+#pragma unroll
+                    for (int h = 0; h < GB; ++h)
+                        each4([&](auto J) {
+                            constexpr int j = decltype(J)::value;
+                            acc[4 * g + i][4 * h + j] = mfma<i, j>(a, b[4 * h + j], acc[4 * g + i][4 * h + j], sa[g], sb[h]);
+                        });
+                });
+        }
+        settle();
+    }
+
+    // result register v of a lane: row 4 * quarter + v of the instruction's 16, column lane % 16
+#pragma unroll
+    for (int i = 0; i < 4 * GA; ++i) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int row = m0 + wm * (BM / WM) + i / 4 * 64 + 4 * (4 * quarter + v) + i % 4;
+#pragma unroll
+            for (int h = 0; h < GB; ++h) {
+                const int col = n0 + wn * (BN / WN) + 64 * h + 4 * r;
+                const f32x4 x = {acc[i][4 * h][v], acc[i][4 * h + 1][v], acc[i][4 * h + 2][v], acc[i][4 * h + 3][v]};
+                if (A.splits > 1) put4_part(A, split, row, col, x);
+                else put4(A, row, col, x);
+            }
+        }
+    }
+}
+
+// ---- few rows ---------------------------------------------------------------------
+
+constexpr int kFewWaves = 8;
+
+// Up to 16 * MT rows of a: b is read once, and what bounds the call is how
+// fast.  A workgroup takes 16 columns of the output, its waves share the
+// steps along k, and their sums are joined through shared memory.
+template <int MT, bool BROW, bool EXACT>
+__global__ __launch_bounds__(kFewWaves * 64) void k_gemm_few(GemmArgs A) {
+    __shared__ __align__(16) float s_sum[kFewWaves][MT][256];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int r = lane % 16, quarter = lane / 16;
+    const int n0 = blockIdx.x * 16, split = blockIdx.y;
+    const int first = split * A.split_steps, end = min(first + A.split_steps, A.steps);
+    const int col = min(n0 + r, A.n - 1);
+    const uint8_t *pb = A.b + static_cast<int64_t>(col) * A.b_ld + 16 * quarter;
+    const uint8_t *pa[MT];
+    int row[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        row[i] = min(16 * i + r, A.m - 1);
+        pa[i] = A.a + static_cast<int64_t>(row[i]) * A.a_ld + 16 * quarter;
+    }
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+    const int scale_col = BROW ? col : col / DOPT_FP8_BLOCK;
+#pragma unroll 4
+    for (int k = first + wave; k < end; k += kFewWaves) {
+        const int64_t at = static_cast<int64_t>(k) * kStep;
+        const i32x8 b = join(*reinterpret_cast<const i32x4 *>(pb + at), *reinterpret_cast<const i32x4 *>(pb + at + 64));
+        const int sb = A.bs[k * A.bs_ld + scale_col];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const i32x8 a = join(*reinterpret_cast<const i32x4 *>(pa[i] + at), *reinterpret_cast<const i32x4 *>(pa[i] + at + 64));
+            const int sa = A.as[k * A.as_ld + row[i]];
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i] = mfma(widen8(a[2 * j], a[2 * j + 1], scale_of<0>(sa)), widen8(b[2 * j], b[2 * j + 1], scale_of<0>(sb)), acc[i]);
+            } else {
+                acc[i] = mfma<0, 0>(a, b, acc[i], sa, sb);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s_sum[wave][i][(4 * quarter + v) * 16 + r] = acc[i][v];
+    __syncthreads();
+    if (threadIdx.x >= MT * 64) return;
+    const int i = threadIdx.x / 64, e = threadIdx.x % 64 * 4;
+    f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) x += *reinterpret_cast<const f32x4 *>(&s_sum[w][i][e]);
+    if (A.splits > 1) put4_part(A, split, 16 * i + e / 16, n0 + e % 16, x);
+    else put4(A, 16 * i + e / 16, n0 + e % 16, x);
+}
+
+// ---- which kernel -------------------------------------------------------------------
+
+struct Plan {
+    int rows, cols;  // of a tile
+    bool few;
+    int splits, split_steps;
+};
+
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+static Plan plan_of(int64_t m, int64_t n, int64_t k) {
+    Plan p{};
+    const int64_t steps = ceil_div(k, kStep);
+    p.few = m <= 64;
+    if (p.few) {
+        p.rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+        p.cols = 16;
+    } else {
+        p.rows = p.cols = ceil_div(m, 256) * ceil_div(n, 256) >= 192 ? 256 : 128;
+    }
+    const int64_t tiles = ceil_div(m, p.rows) * ceil_div(n, p.cols);
+    int64_t splits = 1;
+    if (p.rows != 256) {
+        const int64_t want = p.few ? 256 : 512, least = p.few ? kFewWaves : 4;
+        splits = std::max<int64_t>(1, std::min(want / std::max<int64_t>(tiles, 1), steps / least));
+    }
+    p.split_steps = static_cast<int>(ceil_div(std::max<int64_t>(steps, 1), splits));
+    p.splits = static_cast<int>(ceil_div(std::max<int64_t>(steps, 1), p.split_steps));
+    return p;
+}
+
+static int64_t part_ld_of(int64_t n) { return (n + 3) / 4 * 4; }
+
+template <bool BROW, bool EXACT>
+static void launch_gemm(const GemmArgs &A, const Plan &p, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(A.tiles_m * A.tiles_n), static_cast<unsigned>(A.splits));
+    if (p.few) {
+        if (p.rows == 16) k_gemm_few<1, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
+        else if (p.rows == 32) k_gemm_few<2, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
+        else k_gemm_few<4, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
+    } else if (p.rows == 256) {
+        k_gemm_tile<256, 256, 2, 4, BROW, EXACT><<<grid, 512, 0, stream>>>(A);
+    } else {
+        k_gemm_tile<128, 128, 2, 2, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
+    }
+}
+
+static bool size_ok(int64_t m, int64_t n, int64_t k) {
+    return m >= 0 && n >= 0 && k >= 0 && m <= INT32_MAX - 256 && n < (1 << 23) && k <= DOPT_FP8_MAX_COLS;
+}
+
+}  // namespace dopt
+
+using namespace dopt;
+
+extern "C" int64_t dopt_fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (!size_ok(m, n, k)) return fail(DOPT_ERR_INVALID, "bad size");
+    if (m == 0 || n == 0) return 0;
+    const Plan p = plan_of(m, n, k);
+    return p.splits > 1 ? int64_t(p.splits) * m * part_ld_of(n) * 4 : 0;
+}
+
+extern "C" int dopt_fp8_gemm(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, const dopt_dense *out, int32_t accumulate,
+                             void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (int rc = check_fp8("a", a)) return rc;
+    if (int rc = check_fp8("b", b)) return rc;
+    if (int rc = check_dense("out", out)) return rc;
+    if (a->kind != DOPT_FP8_ROW) return fail(DOPT_ERR_INVALID, "a: not of kind ROW");
+    if (a->cols != b->cols) return fail(DOPT_ERR_INVALID, "a and b differ in columns");
+    if (out->rows != a->rows || out->cols != b->rows) return fail(DOPT_ERR_INVALID, "out: not of a's rows x b's rows");
+    const int64_t m = a->rows, n = b->rows, k = a->cols;
+    if (!size_ok(m, n, k)) return fail(DOPT_ERR_INVALID, "too large");
+    if (m == 0 || n == 0 || (k == 0 && accumulate)) return DOPT_OK;
+    const int64_t need = dopt_fp8_gemm_workspace_bytes(m, n, k);
+    if (need > 0 && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16))
+        return fail(DOPT_ERR_INVALID, "workspace: null, not 16-byte aligned or too small (" + std::to_string(need) + " bytes)");
+    const Span o[] = {dense_span("out", out), span_of("workspace", workspace, need)};
+    const Span in[] = {codes_span("a", a), scales_span("a's scales", a), codes_span("b", b), scales_span("b's scales", b)};
+    if (int rc = check_apart(o, 2, in, 4)) return rc;
+
+    const Plan p = plan_of(m, n, k);
+    const int64_t tiles_m = ceil_div(m, p.rows), tiles_n = ceil_div(n, p.cols);
+    if (tiles_m * tiles_n > INT32_MAX) return fail(DOPT_ERR_INVALID, "too large");
+    GemmArgs A{};
+    A.a = static_cast<const uint8_t *>(a->codes);
+    A.b = static_cast<const uint8_t *>(b->codes);
+    A.as = static_cast<const uint8_t *>(a->scales);
+    A.bs = static_cast<const uint8_t *>(b->scales);
+    A.out = out->data;
+    A.part = static_cast<float *>(workspace);
+    A.as_ld = a->scale_ld;
+    A.bs_ld = b->scale_ld;
+    A.out_ld = out->ld;
+    A.part_ld = part_ld_of(n);
+    A.a_ld = static_cast<int32_t>(a->ld);
+    A.b_ld = static_cast<int32_t>(b->ld);
+    A.m = static_cast<int32_t>(m);
+    A.n = static_cast<int32_t>(n);
+    A.steps = static_cast<int32_t>(ceil_div(k, kStep));
+    A.tiles_m = static_cast<int32_t>(tiles_m);
+    A.tiles_n = static_cast<int32_t>(tiles_n);
+    A.splits = p.splits;
+    A.split_steps = p.split_steps;
+    A.dtype = out->dtype;
+    A.accumulate = accumulate != 0;
+    const bool row = b->kind == DOPT_FP8_ROW, exact = out->dtype == DOPT_F32;
+    if (row && exact) launch_gemm<true, true>(A, p, stream);
+    else if (row) launch_gemm<true, false>(A, p, stream);
+    else if (exact) launch_gemm<false, true>(A, p, stream);
+    else launch_gemm<false, false>(A, p, stream);
+    if (int rc = launched("dopt_fp8_gemm")) return rc;
+    if (p.splits > 1) {
+        const int64_t vectors = m * (A.part_ld / 4);
+        k_gemm_join<<<static_cast<unsigned>(ceil_div(vectors, 256)), 256, 0, stream>>>(A);
+        return launched("dopt_fp8_gemm");
+    }
+    return DOPT_OK;
+}

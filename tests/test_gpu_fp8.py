@@ -1,0 +1,630 @@
+"""The 8-bit operators against their definitions in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import sharded_mixed_precision_amd as D
+from sharded_mixed_precision_amd.arena import ListArrays, fp8_alloc
+from tests import fp8_harness as F
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24  # half a step of fp32
+# 16-bit outputs: 8 neighbouring products of k are added with bits down to 2^-13 of the largest one's power of two (one
+# 2^-13 of it is kept and one 2^-14 is lost), so each of the other 7 is cut by less than 2^-13 of the largest: in all
+# 7 * 2^-13 * max |a||b| over each 8, at most that of the sum of |a||b|.
+IN_EIGHT = 7 * 2.0 ** -13
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def stream():
+    return torch.cuda.current_stream()
+
+
+def poisoned(rows, cols, kind="row"):
+    """An allocation for the matrix whose bytes are all 0x55."""
+    m = fp8_alloc(rows, cols, kind)
+    m.codes.view(torch.uint8).fill_(0x55)
+    m.scales.view(torch.uint8).fill_(0x55)
+    return m
+
+
+def held(x, kind="row"):
+    """x cast by the library."""
+    m = poisoned(*x.shape, kind)
+    D.dopt_fp8_cast(x, m, stream=stream())
+    return m
+
+
+def same_codes(m, x, kind):
+    c, e = F.encode(x, kind)
+    got = F.codes(m)
+    assert torch.equal(F.exponents(m), e)
+    assert torch.equal(torch.isnan(got), torch.isnan(c))
+    assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(c))
+    assert F.padding_is_zero(m)
+    # scales past the last row are left as they were
+    rows = m.rows if kind == "row" else -(-m.rows // 128)
+    assert bool((m.scales.view(torch.uint8)[:, rows:] == 0x55).all())
+
+
+# ---- cast -----------------------------------------------------------------------------------------------------------
+
+SIZES = [(1, 1), (1, 128), (1, 4096), (3, 127), (128, 128), (129, 255), (131, 300), (257, 1000), (640, 1), (1023, 129)]
+
+
+@pytest.mark.parametrize("kind", ["row", "tile"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_cast(rows, cols, dtype, kind):
+    x = F.tokens(gen(rows * 7 + cols), rows, cols, 0.3, "cuda").to(F.TYPES[dtype])
+    both = poisoned(rows, cols, kind), poisoned(cols, rows, kind)
+    D.dopt_fp8_cast(x, *both, stream=stream())
+    for m, want in zip(both, (x, x.t())):
+        same_codes(m, want, kind)
+    alone = poisoned(rows, cols, kind), poisoned(cols, rows, kind)
+    D.dopt_fp8_cast(x, codes=alone[0], stream=stream())
+    D.dopt_fp8_cast(x, transposed=alone[1], stream=stream())
+    for m, n in zip(both, alone):
+        assert torch.equal(m.codes.view(torch.uint8), n.codes.view(torch.uint8))
+        assert torch.equal(m.scales.view(torch.uint8), n.scales.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", ["row", "tile"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_cast_special_values(dtype, kind):
+    """Infinities and NaN in some blocks, blocks of zeros only, of one value, of the type's largest and smallest."""
+    t = F.TYPES[dtype]
+    x = torch.randn(300, 400, generator=gen(1), device="cuda").to(t)
+    x[0, 0], x[1, 130], x[2, 5], x[290, 390] = math.inf, -math.inf, math.nan, math.nan
+    x[5, :] = 0
+    x[6, :128] = math.inf
+    x[7, 0:256] = 0
+    x[7, 140] = torch.finfo(t).max
+    x[8, 256:384] = torch.finfo(t).smallest_normal
+    x[9, 256:384] = torch.finfo(t).smallest_normal * torch.finfo(t).eps  # the least number of the type
+    x[10, 0:128] = 448.0
+    x[11, 0:128] = 450.0
+    x[128:256, 128:256] = 0
+    x[128:256, 256:384] = math.nan
+    both = poisoned(300, 400, kind), poisoned(400, 300, kind)
+    D.dopt_fp8_cast(x, *both, stream=stream())
+    same_codes(both[0], x, kind)
+    same_codes(both[1], x.t(), kind)
+
+
+def test_cast_every_16_bit_number():
+    """All 65536 values of bf16 and fp16, by themselves (the others of the block are zeros) and next to 448."""
+    for t in (torch.bfloat16, torch.float16):
+        v = torch.arange(65536, device="cuda", dtype=torch.int32).to(torch.uint16).view(t)
+        x = torch.zeros(65536, 128, dtype=t, device="cuda")
+        x[:, 77] = v
+        same_codes(held(x), x, "row")
+        x[:, 3] = 448.0
+        same_codes(held(x), x, "row")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_cast_strides(dtype):
+    """Rows farther apart than they are long, data at odd elements, matrices that are part of another."""
+    big = F.tokens(gen(3), 70, 1001, 1.0, "cuda").to(F.TYPES[dtype])
+    x = big[3:60, 7:500]
+    whole = poisoned(90, 900)
+    codes = whole.codes[16:16 + 57, 128:128 + 512]
+    m = D.fp8_matrix(codes, whole.scales[1:5, 16:16 + 60], 57, 493)
+    t = poisoned(493, 57)
+    D.dopt_fp8_cast(x, m, t, stream=stream())
+    c, e = F.encode(x, "row")
+    assert torch.equal(F.codes(m), c) and torch.equal(F.exponents(m), e)
+    same_codes(t, x.t(), "row")
+    around = whole.codes.view(torch.uint8).clone()
+    around[16:16 + 57, 128:128 + 512] = 0x55
+    assert bool((around == 0x55).all())
+    scales = whole.scales.view(torch.uint8).clone()
+    scales[1:5, 16:16 + 57] = 0x55
+    assert bool((scales == 0x55).all())
+
+
+@pytest.mark.parametrize("kind", ["row", "tile"])
+@pytest.mark.parametrize("wtype", ["f32", "bf16", "f16"])
+def test_cast_with_factors(wtype, kind):
+    x = F.tokens(gen(5), 200, 333, 1.0, "cuda").to(torch.bfloat16)
+    row = torch.rand(200, generator=gen(6), device="cuda") + 0.5
+    col = (torch.rand(333, generator=gen(7), device="cuda") + 0.5).to(F.TYPES[wtype])
+    want = (x.float() * row[:, None]) * col.float()
+    both = poisoned(200, 333, kind), poisoned(333, 200, kind)
+    D.dopt_fp8_cast(x, *both, row, col, stream())
+    same_codes(both[0], want, kind)
+    same_codes(both[1], want.t(), kind)
+    row[3], col[5] = math.inf, math.nan  # what pads the last blocks stays 0
+    want = (x.float() * row[:, None]) * col.float()
+    D.dopt_fp8_cast(x, *both, row, col, stream())
+    same_codes(both[0], want, kind)
+    same_codes(both[1], want.t(), kind)
+
+
+# ---- product --------------------------------------------------------------------------------------------------------
+
+def whole_numbers(g, rows, cols, kind, spread=2):
+    """A matrix of small whole numbers times powers of two by block, so that sums of products are exact in fp32."""
+    m = poisoned(rows, cols, kind)
+    v = torch.randint(-4, 5, (rows, cols), generator=g, device="cuda").float()
+    m.codes.view(torch.uint8).zero_()
+    m.codes.view(torch.uint8)[:, :cols] = v.to(torch.float8_e4m3fn).view(torch.uint8)
+    n = rows if kind == "row" else -(-rows // 128)
+    s = torch.randint(127 - spread, 128 + spread, (-(-cols // 128), n), generator=g, device="cuda")
+    m.scales.view(torch.uint8)[:, :n] = s.to(torch.uint8)
+    return m
+
+
+GEMMS = [(1, 1, 1), (1, 16, 128), (1, 77, 300), (5, 130, 1000), (16, 129, 256), (17, 300, 129), (33, 64, 4000), (64, 257, 640),
+         (65, 65, 65), (128, 128, 128), (129, 130, 257), (200, 1000, 384), (100, 100, 4096), (255, 256, 500), (300, 333, 1100),
+         (777, 1029, 640), (2049, 4097, 256), (4100, 3000, 130)]
+
+
+@pytest.mark.parametrize("kind", ["tile", "row"])
+@pytest.mark.parametrize("m,n,k", GEMMS)
+def test_gemm_exact(m, n, k, kind):
+    """Whole numbers: products and sums are exact (below 4096 * 16 * 16 in steps of 1 / 16), so every element is equal."""
+    g = gen(m * 31 + n * 7 + k)
+    a, b = whole_numbers(g, m, k, "row"), whole_numbers(g, n, k, kind)
+    want = F.values(a) @ F.values(b).t()
+    ws = torch.empty(D.dopt_fp8_gemm_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    out = torch.full((m + 1, n + 3), math.nan, device="cuda")
+    D.dopt_fp8_gemm(a, b, out[:m, :n], False, ws, stream())
+    assert torch.equal(out[:m, :n].double(), want)
+    assert torch.isnan(out[m:]).all() and torch.isnan(out[:, n:]).all()
+    D.dopt_fp8_gemm(a, b, out[:m, :n], True, ws, stream())
+    assert torch.equal(out[:m, :n].double(), 2 * want)
+    assert torch.isnan(out[m:]).all() and torch.isnan(out[:, n:]).all()
+    for t in ("bf16", "f16"):
+        low = torch.zeros(m, n, dtype=F.TYPES[t], device="cuda")
+        D.dopt_fp8_gemm(a, b, low, False, ws, stream())
+        assert torch.equal(low, want.float().to(F.TYPES[t]))
+        D.dopt_fp8_gemm(a, b, low, True, ws, stream())
+        assert torch.equal(low, (want.float().to(F.TYPES[t]).float() + want.float()).to(F.TYPES[t]))
+
+
+@pytest.mark.parametrize("kind", ["tile", "row"])
+@pytest.mark.parametrize("m,n,k", [(3, 200, 4096), (50, 90, 1111), (150, 200, 3000), (600, 700, 900), (3300, 4000, 512)])
+def test_gemm_random(m, n, k, kind):
+    """Each of the K sums of products is within half a step of fp32, or a whole one where it is cut, of partial
+    sums that are at most sum |a||b|: K * 2^-23 * sum |a||b| in all.  For 16-bit outputs, IN_EIGHT more."""
+    g = gen(m + n + k)
+    a = held(F.tokens(g, m, k, 1.0, "cuda"))
+    b = held(F.tokens(g, n, k, 0.02, "cuda"), kind)
+    x, y = F.values(a), F.values(b)
+    want, size = x @ y.t(), x.abs() @ y.abs().t()
+    ws = torch.empty(D.dopt_fp8_gemm_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    base = torch.randn(m, n, generator=g, device="cuda")
+    out = base.clone()
+    D.dopt_fp8_gemm(a, b, out, True, ws, stream())
+    bound = k * 2 * U * size + U * (base.double() + want).abs()
+    assert bool(((out.double() - (base.double() + want)).abs() <= bound).all())
+    for t in ("f32", "bf16", "f16"):
+        low = torch.empty(m, n, dtype=F.TYPES[t], device="cuda")
+        D.dopt_fp8_gemm(a, b, low, False, ws, stream())
+        bound = (k * 2 * U + (IN_EIGHT if t != "f32" else 0)) * size
+        bound = bound + F.HALF_STEP[t] * (want.abs() + bound) + F.TINY[t]
+        assert bool(((low.double() - want).abs() <= bound).all())
+        again = torch.empty_like(low)
+        D.dopt_fp8_gemm(a, b, again, False, ws, stream())
+        assert torch.equal(low, again)
+
+
+@pytest.mark.parametrize("m", [2, 100, 4000])
+def test_gemm_nan_stays_in_its_row_and_column(m):
+    n, k = 4000, 300
+    a, b = whole_numbers(gen(1), m, k, "row"), whole_numbers(gen(2), n, k, "row")
+    want = F.values(a) @ F.values(b).t()
+    x, y = m // 2, 1234
+    a.codes.view(torch.uint8)[x, 299] = 0x7f
+    b.codes.view(torch.uint8)[y, 0] = 0xff
+    out = torch.empty(m, n, device="cuda")
+    ws = torch.empty(D.dopt_fp8_gemm_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    D.dopt_fp8_gemm(a, b, out, False, ws, stream())
+    assert torch.isnan(out[x]).all() and torch.isnan(out[:, y]).all()
+    want[x], want[:, y] = math.nan, math.nan
+    assert torch.equal(torch.nan_to_num(out.double(), 0.5), torch.nan_to_num(want, 0.5))
+
+
+def test_gemm_no_depth():
+    a, b = fp8_alloc(5, 0), fp8_alloc(200, 0)
+    out = torch.ones(5, 200, device="cuda")
+    D.dopt_fp8_gemm(a, b, out, True, None, stream())
+    assert bool((out == 1).all())
+    D.dopt_fp8_gemm(a, b, out, False, None, stream())
+    assert bool((out == 0).all())
+    a, out = fp8_alloc(300, 0), torch.ones(300, 200, device="cuda", dtype=torch.float16)
+    D.dopt_fp8_gemm(a, b, out, False, None, stream())
+    assert bool((out == 0).all())
+
+
+def test_gemm_parts_of_matrices():
+    """Rows of a larger weight and of larger activations, and an output that is part of another."""
+    k = 260
+    a, b = whole_numbers(gen(3), 400, k, "row"), whole_numbers(gen(4), 700, k, "tile")
+    x = D.fp8_matrix(a.codes[100:310], a.scales[:, 100:312], 210, k)
+    w = D.fp8_matrix(b.codes[128:528], b.scales[:, 1:5], 400, k, "tile")
+    out = torch.zeros(300, 1001, device="cuda", dtype=torch.bfloat16)
+    ws = torch.empty(max(1, D.dopt_fp8_gemm_workspace_bytes(210, 400, k)), dtype=torch.uint8, device="cuda")
+    D.dopt_fp8_gemm(x, w, out[40:250, 333:733], False, ws, stream())
+    want = (F.values(a)[100:310] @ F.values(b)[128:528].t()).to(torch.bfloat16)
+    assert torch.equal(out[40:250, 333:733], want)
+    out[40:250, 333:733] = 0
+    assert bool((out == 0).all())
+
+
+def test_gemm_scales_of_all_sizes():
+    """Scales from the least to the largest: products that underflow, are in range and overflow as in fp32."""
+    a, b = fp8_alloc(16, 128), fp8_alloc(16, 128)
+    for m in (a, b):
+        m.codes.view(torch.uint8).zero_()
+        m.codes.view(torch.uint8)[:, 0] = 0x38  # 1.0
+    e = torch.tensor([1, 2, 20, 60, 63, 64, 65, 100, 126, 127, 128, 150, 190, 192, 200, 247], device="cuda")
+    a.scales.view(torch.uint8)[0, :16] = e.to(torch.uint8)
+    b.scales.view(torch.uint8)[0, :16] = e.to(torch.uint8)
+    out = torch.empty(16, 16, device="cuda")
+    D.dopt_fp8_gemm(a, b, out, False, None, stream())
+    want = (F.values(a) @ F.values(b).t()).float()  # one product each: exact, or out of range
+    normal = (want >= torch.finfo(torch.float32).smallest_normal) | (want == 0)
+    assert torch.equal(out[normal], want[normal])
+    assert bool(((out - want)[~normal].abs() <= torch.finfo(torch.float32).smallest_normal).all())
+
+
+# ---- norm -----------------------------------------------------------------------------------------------------------
+
+def norm_slack(cols):
+    """How far rstd may be off, relative: a sum of squares passes at most 8 * 8 + 8 additions in registers and
+    8 across threads (long rows: 8 + cols / 2048 and 8), then a division, eps, a root and a division."""
+    return (80 + cols / 2048) * U / 2 + 4 * U
+
+
+NORMS = [(1, 1), (1, 4096), (3, 127), (5, 512), (7, 513), (9, 768), (4, 1024), (6, 1025), (3, 2048), (17, 2049), (5, 4097),
+         (3, 8192), (2, 8200), (2, 16384), (3, 16390), (2, 40000)]
+
+
+@pytest.mark.parametrize("dtype,wtype", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols", NORMS)
+def test_norm(rows, cols, residual, dtype, wtype):
+    g, t, eps = gen(rows + cols), F.TYPES[dtype], 1e-5
+    x = F.tokens(g, rows, cols, 0.5, "cuda").to(t)
+    res = F.tokens(g, rows, cols, 1.0, "cuda").to(t) if residual else None
+    w = (torch.randn(cols, generator=g, device="cuda") * 0.1 + 1).to(F.TYPES[wtype])
+    want_h, want_r, want_y = F.rms_norm(x, res, w, eps, t)
+    h, y = torch.full((rows, cols), 7, dtype=t, device="cuda"), torch.empty(rows, cols, dtype=t, device="cuda")
+    rstd, q = torch.empty(rows, device="cuda"), poisoned(rows, cols)
+    D.dopt_rmsnorm(x, w, eps, residual=res, h=h, y=y, q=q, rstd=rstd, stream=stream())
+    assert torch.equal(h.double(), want_h)
+    slack = norm_slack(cols)
+    assert bool(((rstd.double() - want_r).abs() <= slack * want_r).all())
+    slack += 2 * U  # two products
+    near = slack * want_y.abs()
+    assert bool(((y.double() - want_y).abs() <= near + F.HALF_STEP[dtype] * (want_y.abs() + near) + F.TINY[dtype]).all())
+    # a code is the nearest to a y within `slack`: half a step of 2^-3, or of 2^-9 below 2^-6, in units of the scale
+    unit = torch.exp2(F.exponents(q).double()).repeat_interleave(128, 1)[:, :cols]
+    half = torch.maximum(2.0 ** -4 * (want_y.abs() + near), 2.0 ** -10 * unit)
+    assert bool(((F.values(q) - want_y).abs() <= near + half).all())
+    top = F.blocks_of(want_y, "row").abs().amax((1, 3)) / torch.exp2(F.exponents(q).double())
+    assert bool((top <= 448 * (1 + slack)).all()) and bool((top >= 224 * (1 - slack)).all())
+    assert F.padding_is_zero(q) and bool((q.scales.view(torch.uint8)[:, rows:] == 0x55).all())
+    # the cast of what was kept gives the same codes
+    again = poisoned(rows, cols)
+    D.dopt_fp8_cast(h, again, None, rstd, w, stream())
+    assert torch.equal(q.codes.view(torch.uint8), again.codes.view(torch.uint8))
+    assert torch.equal(q.scales.view(torch.uint8), again.scales.view(torch.uint8))
+    # in place, and with fewer outputs
+    for target in ("x", "residual"):
+        if target == "residual" and not residual:
+            continue
+        x2, res2, q2 = x.clone(), None if res is None else res.clone(), poisoned(rows, cols)
+        D.dopt_rmsnorm(x2, w, eps, residual=res2, h=x2 if target == "x" else res2, q=q2, stream=stream())
+        assert torch.equal(x2 if target == "x" else res2, h)
+        assert torch.equal(q.codes.view(torch.uint8), q2.codes.view(torch.uint8))
+    y2 = torch.empty_like(y)
+    D.dopt_rmsnorm(x, w, eps, residual=res, y=y2, stream=stream())
+    assert torch.equal(y, y2)
+
+
+def test_norm_special_rows():
+    """A row of zeros, one with an infinity, one with a NaN, one of very small values: none touches another."""
+    x = torch.randn(6, 700, generator=gen(1), device="cuda")
+    x[1], x[4] = 0, x[4] * 1e-30
+    x[2, 5], x[3, 699] = math.inf, math.nan
+    w = torch.ones(700, device="cuda")
+    y, q, rstd = torch.empty_like(x), poisoned(6, 700), torch.empty(6, device="cuda")
+    D.dopt_rmsnorm(x, w, 1e-6, y=y, q=q, rstd=rstd, stream=stream())
+    assert bool((y[1] == 0).all()) and bool((F.codes(q)[1] == 0).all())
+    assert rstd[2] == 0 and torch.isnan(y[2, 5]) and bool((y[2, 6:] == 0).all()) and torch.isnan(F.codes(q)[2, 5])
+    assert torch.isnan(y[3]).all() and torch.isnan(F.codes(q)[3]).all()
+    good = [0, 4, 5]
+    _, _, want = F.rms_norm(x[good], None, w, 1e-6, torch.float32)
+    assert bool(((y[good].double() - want).abs() <= (norm_slack(700) + 3 * U) * want.abs() + 2.0 ** -149).all())
+
+
+@pytest.mark.parametrize("dtype,dtype_dy,wtype", [("f32", "f32", "f32"), ("bf16", "bf16", "f32"), ("bf16", "f32", "bf16"),
+                                                  ("f16", "f16", "f16"), ("f16", "f32", "f32")])
+@pytest.mark.parametrize("rows,cols", NORMS + [(1500, 300), (2500, 1100)])
+def test_norm_grad(rows, cols, dtype, dtype_dy, wtype):
+    g, t = gen(rows + cols + 1), F.TYPES[dtype]
+    h = F.tokens(g, rows, cols, 0.7, "cuda").to(t)
+    dy = F.tokens(g, rows, cols, 0.1, "cuda").to(F.TYPES[dtype_dy])
+    dh = F.tokens(g, rows, cols, 0.1, "cuda").to(t)
+    w = (torch.randn(cols, generator=g, device="cuda") * 0.1 + 1).to(F.TYPES[wtype])
+    rstd = (h.double().square().mean(1) + 1e-5).rsqrt().float()
+    ws = torch.empty(D.dopt_rmsnorm_grad_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    depth = norm_slack(cols) * 2 + 8 * U
+    for res in (None, dh):
+        want, want_w = F.rms_norm_grad(dy, h, res, w, rstd)
+        gg, r = (dy.double() * w.double()).abs(), rstd.double()[:, None]
+        size = r * (gg + h.double().abs() * r * r * (gg * h.double().abs()).mean(1, keepdim=True))
+        size = size + (0 if res is None else res.double().abs())
+        dx, dw = torch.empty_like(h), torch.full((cols,), 3.0, device="cuda")
+        D.dopt_rmsnorm_grad(dy, h, w, rstd, dx, dw, dh=res, workspace=ws, stream=stream())
+        bound = depth * size
+        assert bool(((dx.double() - want).abs() <= bound + F.HALF_STEP[dtype] * (want.abs() + bound) + F.TINY[dtype]).all())
+        # each worker adds at most ceil(rows / 1024) rows, then up to 32 and 32 sums are joined
+        size_w = (dy.double() * h.double() * r).abs().sum(0)
+        bound_w = (rows / 1024 + 70) * U * size_w
+        assert bool(((dw.double() - want_w).abs() <= bound_w + U * want_w.abs()).all())
+        base = torch.randn(cols, generator=g, device="cuda")
+        acc = base.clone()
+        D.dopt_rmsnorm_grad(dy, h, w, rstd, dx, acc, dh=res, accumulate=True, workspace=ws, stream=stream())
+        assert torch.equal(acc, base + dw)
+        for low in (torch.bfloat16, torch.float16):
+            d16 = torch.ones(cols, dtype=low, device="cuda")
+            D.dopt_rmsnorm_grad(dy, h, w, rstd, dx, d16, dh=res, workspace=ws, stream=stream())
+            assert torch.equal(d16, dw.to(low))
+            D.dopt_rmsnorm_grad(dy, h, w, rstd, dx, d16, dh=res, accumulate=True, workspace=ws, stream=stream())
+            assert torch.equal(d16, (dw.to(low).float() + dw).to(low))
+        # in place: the grad of the residual's sum, or the norm's own
+        if res is not None:
+            into = res.clone()
+            D.dopt_rmsnorm_grad(dy, h, w, rstd, into, dw, dh=into, workspace=ws, stream=stream())
+            assert torch.equal(into, dx)
+        if dtype == dtype_dy:
+            into = dy.clone()
+            D.dopt_rmsnorm_grad(into, h, w, rstd, into, dw, dh=res, workspace=ws, stream=stream())
+            assert torch.equal(into, dx)
+
+
+def test_norm_grad_against_differences():
+    """The grad of sum(dy * y) by central differences of the definition, in 64 bits."""
+    rows, cols = 4, 40
+    g = gen(9)
+    x, dy = torch.randn(rows, cols, generator=g, device="cuda"), torch.randn(rows, cols, generator=g, device="cuda")
+    w = torch.randn(cols, generator=g, device="cuda") + 1
+    eps, y, rstd = 1e-3, torch.empty(rows, cols, device="cuda"), torch.empty(rows, device="cuda")
+    D.dopt_rmsnorm(x, w, eps, y=y, rstd=rstd, stream=stream())
+    dx, dw = torch.empty_like(x), torch.empty(cols, device="cuda")
+    ws = torch.empty(D.dopt_rmsnorm_grad_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    D.dopt_rmsnorm_grad(dy, x, w, rstd, dx, dw, workspace=ws, stream=stream())
+
+    def loss(x, w):
+        r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+        return (dy.double() * (x * r * w)).sum()
+
+    step = 1e-5  # third derivatives here are of order 10: the differences are off by 1e-9 or so, dx by its own rounding
+    for i in range(rows):
+        for j in range(0, cols, 7):
+            d = torch.zeros(rows, cols, dtype=torch.float64, device="cuda")
+            d[i, j] = step
+            slope = (loss(x.double() + d, w.double()) - loss(x.double() - d, w.double())) / (2 * step)
+            assert abs(slope.item() - dx[i, j].item()) < 1e-5
+    for j in range(cols):
+        d = torch.zeros(cols, dtype=torch.float64, device="cuda")
+        d[j] = step
+        slope = (loss(x.double(), w.double() + d) - loss(x.double(), w.double() - d)) / (2 * step)
+        assert abs(slope.item() - dw[j].item()) < 1e-5
+
+
+def test_norm_grad_no_rows():
+    dw = torch.ones(300, device="cuda")
+    none = torch.empty(0, 300, device="cuda")
+    args = (none, none, torch.ones(300, device="cuda"), torch.empty(0, device="cuda"), none)
+    D.dopt_rmsnorm_grad(*args, dw, accumulate=True, stream=stream())
+    assert bool((dw == 1).all())
+    D.dopt_rmsnorm_grad(*args, dw, stream=stream())
+    assert bool((dw == 0).all())
+
+
+def test_norm_strides():
+    big = F.tokens(gen(4), 40, 1333, 1.0, "cuda").to(torch.bfloat16)
+    x, res = big[3:30, 5:600], big[5:32, 701:1296]
+    w = torch.rand(595, generator=gen(5), device="cuda").to(torch.bfloat16)
+    out = torch.zeros(50, 1333, dtype=torch.bfloat16, device="cuda")
+    y, h, rstd = out[1:28, 11:606], out[2:29, 611:1206], torch.empty(27, device="cuda")
+    D.dopt_rmsnorm(x, w, 1e-6, residual=res, h=h, y=y, rstd=rstd, stream=stream())
+    c = [torch.empty(27, 595, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    D.dopt_rmsnorm(x.contiguous(), w, 1e-6, residual=res.contiguous(), h=c[0], y=c[1], stream=stream())
+    assert torch.equal(h, c[0]) and torch.equal(y, c[1])
+    ws = torch.empty(D.dopt_rmsnorm_grad_workspace_bytes(27, 595), dtype=torch.uint8, device="cuda")
+    dx, dw = torch.empty(27, 700, dtype=torch.bfloat16, device="cuda")[:, 1:596], torch.empty(595, device="cuda")
+    D.dopt_rmsnorm_grad(x, h, w, rstd, dx, dw, dh=y, workspace=ws, stream=stream())
+    dx2, dw2 = torch.empty(27, 595, dtype=torch.bfloat16, device="cuda"), torch.empty(595, device="cuda")
+    D.dopt_rmsnorm_grad(x.contiguous(), h.contiguous(), w, rstd, dx2, dw2, dh=y.contiguous(), workspace=ws, stream=stream())
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    y.zero_()
+    h.zero_()
+    assert bool((out == 0).all())
+
+
+# ---- together -------------------------------------------------------------------------------------------------------
+
+class Layer:
+    """A norm and a linear layer in 8 bits, whose params a list steps and whose grads go straight to its grads."""
+
+    def __init__(self, tokens, width, out, seed=0):
+        g = gen(seed)
+        self.t, self.k, self.n = tokens, width, out
+        self.params = [(torch.randn(out, width, generator=g, device="cuda") * 0.05).bfloat16(),
+                       torch.ones(width, device="cuda") + 0.1 * torch.randn(width, generator=g, device="cuda")]
+        self.grads = [torch.zeros(out, width, device="cuda"), torch.zeros(width, device="cuda")]
+        self.lst = D.dopt_list_build([D.TensorSpec(out * width, "bf16", "f32"), D.TensorSpec(width, "f32", "f32")], "f32")
+        self.arrays = ListArrays(self.lst)
+        self.tensors = D.list_tensors(self.lst, [p.view(-1) for p in self.params], [x.view(-1) for x in self.grads], self.arrays.state)
+        D.dopt_list_init(self.lst, self.tensors, D.scaler_cfg(), self.arrays.workspace, stream())
+        self.hp = D.hparams_array([(1e-3, 0.9, 0.999, 1e-8, 0.01)])
+        self.w, self.wt = fp8_alloc(out, width, "tile"), fp8_alloc(width, out, "tile")
+        self.q, self.qt = fp8_alloc(tokens, width), fp8_alloc(width, tokens)
+        self.dq, self.dqt = fp8_alloc(tokens, out), fp8_alloc(out, tokens)
+        e = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
+        self.h, self.rstd, self.y = e(tokens, width), e(tokens, dtype=torch.float32), e(tokens, out)
+        self.dn, self.dx = e(tokens, width, dtype=torch.float32), e(tokens, width)
+        need = max(D.dopt_fp8_gemm_workspace_bytes(tokens, out, width), D.dopt_fp8_gemm_workspace_bytes(tokens, width, out),
+                   D.dopt_fp8_gemm_workspace_bytes(out, width, tokens), D.dopt_rmsnorm_grad_workspace_bytes(tokens, width))
+        self.ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+        self.cast_weight(stream())
+
+    def cast_weight(self, s):
+        D.dopt_fp8_cast(self.params[0], self.w, self.wt, stream=s)
+
+    def forward(self, x, res, s):
+        D.dopt_rmsnorm(x, self.params[1], 1e-5, residual=res, h=self.h, q=self.q, rstd=self.rstd, stream=s)
+        D.dopt_fp8_gemm(self.q, self.w, self.y, False, self.ws, s)
+
+    def backward(self, dy, dh, s):
+        D.dopt_fp8_cast(dy, self.dq, self.dqt, stream=s)
+        D.dopt_fp8_gemm(self.dq, self.wt, self.dn, False, self.ws, s)
+        D.dopt_fp8_cast(self.h, None, self.qt, self.rstd, self.params[1], s)
+        D.dopt_fp8_gemm(self.dqt, self.qt, self.grads[0], True, self.ws, s)
+        D.dopt_rmsnorm_grad(self.dn, self.h, self.params[1], self.rstd, self.dx, self.grads[1], dh=dh, accumulate=True,
+                            workspace=self.ws, stream=s)
+
+    def step(self, s):
+        D.dopt_list_step(self.lst, self.tensors, self.hp, 1.0, self.arrays.workspace, s, want_stats=False)
+        self.cast_weight(s)
+
+    def state(self):
+        return [*self.params, *self.grads, self.y, self.dx, self.dn, self.w.codes.view(torch.uint8), self.arrays.state["exp_avg"]]
+
+
+def batch(layer, seed):
+    g = gen(seed)
+    t = lambda n, s: F.tokens(g, layer.t, n, s, "cuda").bfloat16()  # noqa: E731
+    return t(layer.k, 0.5), t(layer.k, 1.0), t(layer.n, 0.01), t(layer.k, 0.01)
+
+
+@pytest.mark.parametrize("tokens,width,out", [(300, 520, 391), (1, 128, 64), (2050, 768, 2304)])
+def test_layer(tokens, width, out):
+    """Two micro-batches through the layer, forward and backward, then a step and the cast of the stepped weight.
+    Grads against 64 bits from the 8-bit operands, so the operands' own rounding does not count."""
+    L = Layer(tokens, width, out)
+    want = [torch.zeros(out, width, dtype=torch.float64, device="cuda"), torch.zeros(width, dtype=torch.float64, device="cuda")]
+    size = [x.clone() for x in want]
+    for i in range(2):
+        x, res, dy, dh = batch(L, i)
+        L.forward(x, res, stream())
+        L.backward(dy, dh, stream())
+        q, w, dq = F.values(L.q), F.values(L.w), F.values(L.dq)
+        y = q @ w.t()
+        bound = (width * 2 * U + IN_EIGHT) * (q.abs() @ w.abs().t())
+        assert bool(((L.y.double() - y).abs() <= bound + 2.0 ** -8 * (y.abs() + bound)).all())
+        dn = dq @ F.values(L.wt).t()
+        assert bool(((L.dn.double() - dn).abs() <= out * 2 * U * (dq.abs() @ F.values(L.wt).abs().t()) + U * dn.abs()).all())
+        assert torch.equal(F.values(L.wt), F.values(L.w).t())
+        dqt, qt = F.values(L.dqt), F.values(L.qt)
+        want[0] += dqt @ qt.t()
+        size[0] += dqt.abs() @ qt.abs().t()
+        dx, dw = F.rms_norm_grad(L.dn, L.h, dh, L.params[1], L.rstd)
+        want[1] += dw
+        size[1] += (L.dn.double() * L.h.double() * L.rstd.double()[:, None]).abs().sum(0)
+        scale = dx.abs().amax(1, keepdim=True) + dh.double().abs()
+        assert bool(((L.dx.double() - dx).abs() <= 2.0 ** -8 * dx.abs() + 1e-4 * scale).all())
+    assert bool(((L.grads[0].double() - want[0]).abs() <= (tokens * 2 + 4) * U * size[0] + 2.0 ** -149).all())
+    assert bool(((L.grads[1].double() - want[1]).abs() <= (tokens / 1024 + 75) * U * size[1]).all())
+    before = L.params[0].clone()
+    L.step(stream())
+    assert not torch.equal(before, L.params[0])
+    same_codes_of = F.encode(L.params[0], "tile")[0]
+    assert torch.equal(F.codes(L.w), same_codes_of)
+
+
+def test_layer_nan_reaches_the_overflow_check():
+    L = Layer(130, 256, 100)
+    x, res, dy, dh = batch(L, 1)
+    x[7, 3] = math.inf
+    L.forward(x, res, stream())
+    L.backward(dy, dh, stream())
+    before = L.params[0].clone()
+    st = D.dopt_list_step(L.lst, L.tensors, L.hp, 1.0, L.arrays.workspace, stream())
+    assert st["found_inf"] == 1 and st["skipped"] == 1 and torch.equal(before, L.params[0])
+
+
+@pytest.mark.parametrize("tokens,width,out", [(300, 520, 391), (2050, 768, 640)])
+def test_layer_captured(tokens, width, out):
+    """A captured forward, backward and step, replayed several times between eager work, against an eager twin."""
+    eager, graphed = Layer(tokens, width, out), Layer(tokens, width, out)
+    x, res, dy, dh = (b.clone() for b in batch(eager, 0))
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        s = torch.cuda.current_stream()
+        graphed.forward(x, res, s)
+        graphed.backward(dy, dh, s)
+        graphed.step(s)
+    for i in range(4):
+        for old, new in zip((x, res, dy, dh), batch(eager, 10 + i)):
+            old.copy_(new)
+        graph.replay()
+        eager.forward(x, res, stream())
+        eager.backward(dy, dh, stream())
+        eager.step(stream())
+        torch.cuda.synchronize()
+        for a, b in zip(eager.state(), graphed.state()):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Two layers with buffers of their own on two streams give what each gives alone."""
+    layers = [Layer(700, 768, 513, i) for i in range(2)]
+    alone = [Layer(700, 768, 513, i) for i in range(2)]
+    data = [batch(layers[i], 50 + i) for i in range(2)]
+    for i, L in enumerate(alone):
+        for _ in range(3):
+            L.forward(data[i][0], data[i][1], stream())
+            L.backward(data[i][2], data[i][3], stream())
+            L.step(stream())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for i, L in enumerate(layers):
+            L.forward(data[i][0], data[i][1], streams[i])
+            L.backward(data[i][2], data[i][3], streams[i])
+            L.step(streams[i])
+    torch.cuda.synchronize()
+    for a, b in zip(layers, alone):
+        for x, y in zip(a.state(), b.state()):
+            assert torch.equal(x, y)
+
+
+def test_binding_refusals():
+    x = torch.zeros(4, 256, device="cuda")
+    q = fp8_alloc(4, 256)
+    with pytest.raises(D.DoptError, match="not a device tensor"):
+        D.dopt_fp8_cast(x.cpu(), q)
+    with pytest.raises(D.DoptError, match="dimensions"):
+        D.dopt_fp8_cast(x.view(-1), q)
+    with pytest.raises(D.DoptError, match="next to each other"):
+        D.dopt_fp8_cast(x.t(), fp8_alloc(256, 4))
+    with pytest.raises(D.DoptError, match="rows overlap"):
+        D.dopt_fp8_cast(x[:1].expand(4, 256), q)
+    with pytest.raises(D.DoptError, match="fp32, bf16 or fp16"):
+        D.dopt_fp8_cast(x.double(), q)
+    with pytest.raises(D.DoptError, match="together"):
+        D.dopt_fp8_cast(x, q, row_factor=torch.ones(4, device="cuda"))
+    with pytest.raises(D.DoptError, match="row_factor"):
+        D.dopt_fp8_cast(x, q, None, torch.ones(5, device="cuda"), torch.ones(256, device="cuda"))
+    with pytest.raises(D.DoptError, match="weight"):
+        D.dopt_rmsnorm(x, torch.ones(255, device="cuda"), 1e-5, q=q)
+    with pytest.raises(D.DoptError, match="codes"):
+        D.fp8_matrix(q.codes[:3], q.scales, 4, 256)
+    with pytest.raises(D.DoptError, match="scales"):
+        D.fp8_matrix(q.codes, q.scales[:, :3], 4, 256)
+    with pytest.raises(D.DoptError, match="overlaps"):
+        D.dopt_fp8_gemm(q, q, q.codes.view(torch.float32).view(4, 64)[:, :4])
