@@ -92,8 +92,8 @@ int dopt_fp8_layout(int64_t rows, int64_t cols, int32_t kind, dopt_fp8_sizes *ou
  * `transposed` its transpose (x->cols x x->rows); either may be NULL, and
  * both are of one kind.  With row_factor and col_factor (x->rows fp32 and
  * x->cols elements of col_dtype; both or neither), what is cast is
- * (x[r][c] * row_factor[r]) * col_factor[c], each product rounded to fp32:
- * with dopt_rmsnorm's rstd and weight, the norm's output from its kept input.
+ * x[r][c] * row_factor[r] * col_factor[c], rounded to fp32 once: with
+ * dopt_rmsnorm's rstd and weight, the norm's output from its kept input, bit for bit.
  */
 int dopt_fp8_cast(const dopt_dense *x, const float *row_factor, const void *col_factor, int32_t col_dtype,
                   const dopt_fp8_matrix *codes, const dopt_fp8_matrix *transposed, hipStream_t stream);
@@ -112,11 +112,12 @@ int dopt_fp8_gemm(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, const dopt
 /*
  * dopt_rmsnorm -- per row of x (and residual, NULL: none), of one type:
  *     h    = x + residual, rounded to their type
- *     rstd = 1 / sqrt(mean(h^2) + eps)
- *     y    = (h * rstd) * weight, each product rounded to fp32
+ *     rstd = 1 / sqrt(mean(h^2) + eps), rounded to fp32
+ *     y    = h * rstd * weight, rounded to fp32 once
  * h (NULL: not kept; may be x or residual itself), rstd (fp32, one per row;
  * NULL: not kept) and y: `y` in x's type, `q` in 8 bits (kind ROW), or both.
- * The weight is x->cols elements of weight_dtype.  Statistics in fp32.
+ * The weight is x->cols elements of weight_dtype.  Squares of 8 neighbours are
+ * added in fp32, their sums and the rest of rstd in 64 bits.
  */
 int dopt_rmsnorm(const dopt_dense *x, const dopt_dense *residual, const void *weight, int32_t weight_dtype, double eps,
                  const dopt_dense *h, const dopt_dense *y, const dopt_fp8_matrix *q, float *rstd, hipStream_t stream);

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Dict, List, NamedTuple, Optional, Sequence, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -943,42 +944,68 @@ def _dtype_id(dt, what) -> int:
     return i
 
 
-def _here(x, what, device: int):
-    """Refuses a tensor that is not on the device that the call is launched on."""
+def _misplaced(x, what):
     if not x.is_cuda:
         raise DoptError(DOPT_ERR_INVALID, f"{what}: not a device tensor")
-    if x.get_device() != device:
-        _elsewhere(what, x.get_device())
+    _elsewhere(what, x.get_device())
 
 
-def _dense(x, what, device: int) -> Optional[dopt_dense]:
-    """A 2-d tensor whose rows' elements lie next to each other."""
+# The calls below are made once per layer and token batch, so their arguments
+# are packed into bytes (a third of the time that a ctypes structure takes) and
+# the functions take them as addresses.
+_pack_dense = struct.Struct("PqqqiI").pack
+assert len(_pack_dense(0, 0, 0, 0, 0, 0)) == ctypes.sizeof(dopt_dense)
+
+
+def _by_address():
+    L = ctypes.CDLL(LIB_PATH)  # function objects of its own: _lib's take structures
+    I32, I64, VP, D = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double
+    L.dopt_fp8_cast.argtypes = [VP, VP, VP, I32, VP, VP, VP]
+    L.dopt_fp8_gemm.argtypes = [VP, VP, VP, I32, VP, I64, VP]
+    L.dopt_rmsnorm.argtypes = [VP, VP, VP, I32, D, VP, VP, VP, VP, VP]
+    L.dopt_rmsnorm_grad.argtypes = [VP, VP, VP, VP, I32, VP, VP, VP, I32, I32, VP, I64, VP]
+    return L.dopt_fp8_cast, L.dopt_fp8_gemm, L.dopt_rmsnorm, L.dopt_rmsnorm_grad
+
+
+_cast_call, _gemm_call, _rmsnorm_call, _rmsnorm_grad_call = _by_address()
+
+
+def _dense(x, what, device: int) -> Optional[bytes]:
+    """A 2-d tensor whose rows' elements lie next to each other, as a dopt_dense."""
     if x is None:
         return None
-    if x.dim() != 2:
-        raise DoptError(DOPT_ERR_INVALID, f"{what}: {x.dim()} dimensions, a matrix has 2")
-    rows, cols = x.shape
+    shape = x.shape
+    if len(shape) != 2:
+        raise DoptError(DOPT_ERR_INVALID, f"{what}: {len(shape)} dimensions, a matrix has 2")
+    rows, cols = shape
     ld, step = x.stride()
-    if cols > 1 and step != 1:
+    if rows <= 1:
+        ld = cols
+    if step != 1 and cols > 1:
         raise DoptError(DOPT_ERR_INVALID, f"{what}: the elements of a row do not lie next to each other")
-    if rows > 1 and ld < cols:
+    if ld < cols:
         raise DoptError(DOPT_ERR_INVALID, f"{what}: rows overlap")
-    _here(x, what, device)
-    return dopt_dense(x.data_ptr(), rows, cols, ld if rows > 1 else cols, _dtype_id(x.dtype, what), 0)
+    if x.get_device() != device:
+        _misplaced(x, what)
+    t = _dtype_ids.get(x.dtype)
+    return _pack_dense(x.data_ptr(), rows, cols, ld, _dtype_id(x.dtype, what) if t is None else t, 0)
 
 
 def _vector(x, what, n: int, device: int, dtype=None):
     """(address, DOPT_* type) of a contiguous vector of n elements."""
     if x is None:
         raise DoptError(DOPT_ERR_INVALID, f"{what}: missing")
-    i = _dtype_id(x.dtype, what)
+    i = _dtype_ids.get(x.dtype)
+    if i is None:
+        i = _dtype_id(x.dtype, what)
     if dtype is not None and i != dtype:
         raise DoptError(DOPT_ERR_INVALID, f"{what}: dtype {x.dtype}, {DTYPE_NAMES[dtype]} is needed")
     if x.numel() != n:
         raise DoptError(DOPT_ERR_INVALID, f"{what}: {x.numel()} elements, {n} are needed")
     if not x.is_contiguous():
         raise DoptError(DOPT_ERR_INVALID, f"{what}: not contiguous")
-    _here(x, what, device)
+    if x.get_device() != device:
+        _misplaced(x, what)
     return x.data_ptr(), i
 
 
@@ -988,15 +1015,25 @@ def _scratch(x, device: int):
         return None, 0
     if not x.is_contiguous():
         raise DoptError(DOPT_ERR_INVALID, "workspace: not contiguous")
-    _here(x, "workspace", device)
-    return x.data_ptr(), x.numel() * x.element_size()
+    if x.get_device() != device:
+        _misplaced(x, "workspace")
+    return x.data_ptr(), x.nbytes
+
+
+def _device() -> int:
+    """The current device, on which the calls are launched."""
+    global _device
+    import torch
+    torch.cuda.init()
+    _device = torch._C._cuda_getDevice  # from now on without torch.cuda's own checks
+    return _device()
 
 
 def _on(stream, device: int) -> Optional[int]:
     if stream is None or isinstance(stream, int):
         return stream
-    if stream.device.index != device:
-        _elsewhere("stream", stream.device.index)
+    if stream.device_index != device:
+        _elsewhere("stream", stream.device_index)
     return stream.cuda_stream
 
 
@@ -1006,9 +1043,9 @@ class Fp8Matrix:
     torch.float8_e8m0fnu or uint8), .rows, .cols and .kind ('row' | 'tile').
     Make it with fp8_matrix() or arena.fp8_alloc()."""
 
-    def __init__(self, codes, scales, rows: int, cols: int, kind: str, struct: dopt_fp8_matrix, device: int):
+    def __init__(self, codes, scales, rows: int, cols: int, kind: str, desc: dopt_fp8_matrix, device: int):
         self.codes, self.scales, self.rows, self.cols, self.kind = codes, scales, rows, cols, kind
-        self.struct, self.device = struct, device
+        self.packed, self.device = bytes(desc), device
 
 
 def fp8_matrix(codes, scales, rows: int, cols: int, kind: str = "row") -> Fp8Matrix:
@@ -1043,27 +1080,31 @@ def dopt_fp8_layout(rows: int, cols: int, kind: str = "row") -> Dict:
     return {name: getattr(o, name) for name, _ in o._fields_}
 
 
-def _fp8(x: Optional[Fp8Matrix], what, device: int) -> Optional[dopt_fp8_matrix]:
+def _fp8(x: Optional[Fp8Matrix], what, device: int) -> Optional[bytes]:
     if x is None:
         return None
     if x.device != device:
         _elsewhere(what, x.device)
-    return x.struct
+    return x.packed
 
 
 def dopt_fp8_cast(x, codes: Optional[Fp8Matrix] = None, transposed: Optional[Fp8Matrix] = None, row_factor=None,
                   col_factor=None, stream=None):
     """x (a matrix of fp32, bf16 or fp16) to 8 bits, its transpose, or both,
     with x[r][c] * row_factor[r] * col_factor[c] in x's place if factors are given."""
-    d = _current_device()
+    d = _device()
     xd = _dense(x, "x", d)
+    if xd is None:
+        raise DoptError(DOPT_ERR_INVALID, "x: missing")
     if (row_factor is None) != (col_factor is None):
         raise DoptError(DOPT_ERR_INVALID, "row and column factors come together")
     r, c, ct = None, None, DOPT_F32
     if row_factor is not None:
-        r, _ = _vector(row_factor, "row_factor", xd.rows, d, DOPT_F32)
-        c, ct = _vector(col_factor, "col_factor", xd.cols, d)
-    _check(_lib.dopt_fp8_cast(xd, r, c, ct, _fp8(codes, "codes", d), _fp8(transposed, "transposed", d), _on(stream, d)))
+        r, _ = _vector(row_factor, "row_factor", x.shape[0], d, DOPT_F32)
+        c, ct = _vector(col_factor, "col_factor", x.shape[1], d)
+    rc = _cast_call(xd, r, c, ct, _fp8(codes, "codes", d), _fp8(transposed, "transposed", d), _on(stream, d))
+    if rc:
+        _check(rc)
 
 
 def _bytes(n: int) -> int:
@@ -1078,22 +1119,28 @@ def dopt_fp8_gemm_workspace_bytes(m: int, n: int, k: int) -> int:
 
 def dopt_fp8_gemm(a: Fp8Matrix, b: Fp8Matrix, out, accumulate: bool = False, workspace=None, stream=None):
     """out (+)= a b^T; a of kind 'row', b of either, both with k as columns."""
-    d = _current_device()
+    d = _device()
     ws, nbytes = _scratch(workspace, d)
-    _check(_lib.dopt_fp8_gemm(_fp8(a, "a", d), _fp8(b, "b", d), _dense(out, "out", d), accumulate, ws, nbytes,
-                              _on(stream, d)))
+    rc = _gemm_call(_fp8(a, "a", d), _fp8(b, "b", d), _dense(out, "out", d), accumulate, ws, nbytes, _on(stream, d))
+    if rc:
+        _check(rc)
 
 
 def dopt_rmsnorm(x, weight, eps: float, residual=None, h=None, y=None, q: Optional[Fp8Matrix] = None, rstd=None,
                  stream=None):
     """The RMS norm of x + residual: y in x's type, q in 8 bits, or both; h (the
     sum, which may be x or residual itself) and rstd are what the backward pass takes."""
-    d = _current_device()
+    d = _device()
     xd = _dense(x, "x", d)
-    w, wt = _vector(weight, "weight", xd.cols, d)
-    r = None if rstd is None else _vector(rstd, "rstd", xd.rows, d, DOPT_F32)[0]
-    _check(_lib.dopt_rmsnorm(xd, _dense(residual, "residual", d), w, wt, eps, _dense(h, "h", d), _dense(y, "y", d),
-                             _fp8(q, "q", d), r, _on(stream, d)))
+    if xd is None:
+        raise DoptError(DOPT_ERR_INVALID, "x: missing")
+    rows, cols = x.shape
+    w, wt = _vector(weight, "weight", cols, d)
+    r = None if rstd is None else _vector(rstd, "rstd", rows, d, DOPT_F32)[0]
+    rc = _rmsnorm_call(xd, _dense(residual, "residual", d), w, wt, eps, _dense(h, "h", d), _dense(y, "y", d), _fp8(q, "q", d),
+                       r, _on(stream, d))
+    if rc:
+        _check(rc)
 
 
 def dopt_rmsnorm_grad_workspace_bytes(rows: int, cols: int) -> int:
@@ -1103,16 +1150,19 @@ def dopt_rmsnorm_grad_workspace_bytes(rows: int, cols: int) -> int:
 def dopt_rmsnorm_grad(dy, h, weight, rstd, dx, dweight, dh=None, accumulate: bool = False, workspace=None, stream=None):
     """The norm's backward pass: dx (the grad of x and of the residual, dh
     added; may be dh or dy itself) and dweight, added to with `accumulate`."""
-    d = _current_device()
+    d = _device()
     hd = _dense(h, "h", d)
     if hd is None:
         raise DoptError(DOPT_ERR_INVALID, "h: missing")
-    w, wt = _vector(weight, "weight", hd.cols, d)
-    g, gt = _vector(dweight, "dweight", hd.cols, d)
-    r, _ = _vector(rstd, "rstd", hd.rows, d, DOPT_F32)
+    rows, cols = h.shape
+    w, wt = _vector(weight, "weight", cols, d)
+    g, gt = _vector(dweight, "dweight", cols, d)
+    r, _ = _vector(rstd, "rstd", rows, d, DOPT_F32)
     ws, nbytes = _scratch(workspace, d)
-    _check(_lib.dopt_rmsnorm_grad(_dense(dy, "dy", d), hd, _dense(dh, "dh", d), w, wt, r, _dense(dx, "dx", d), g, gt,
-                                  accumulate, ws, nbytes, _on(stream, d)))
+    rc = _rmsnorm_grad_call(_dense(dy, "dy", d), hd, _dense(dh, "dh", d), w, wt, r, _dense(dx, "dx", d), g, gt, accumulate, ws,
+                            nbytes, _on(stream, d))
+    if rc:
+        _check(rc)
 
 
 # ---- device-memory placement helpers (include/dopt_vmm.h) ----

@@ -57,6 +57,10 @@ struct __attribute__((packed, aligned(2))) Bytes8 {
     u32x2 v;
 };
 
+struct __attribute__((packed, aligned(4))) Float4 {
+    f32x4 v;
+};
+
 // Number of 16-byte words that 8 elements take.
 template <int T>
 constexpr int kWords8 = T == DOPT_F32 ? 2 : 1;
@@ -156,6 +160,14 @@ __device__ __forceinline__ void load_vector8(const void *p, int32_t dtype, int64
     if (dtype == DOPT_F32) unpack8<DOPT_F32>(load8<DOPT_F32>(p, e, n), x);
     else if (dtype == DOPT_BF16) unpack8<DOPT_BF16>(load8<DOPT_BF16>(p, e, n), x);
     else unpack8<DOPT_F16>(load8<DOPT_F16>(p, e, n), x);
+}
+
+// x * r * w rounded once: what the first product loses goes into the second.
+// A code lies next to a border as often as its value is off, so with two
+// roundings twice as many codes would differ from the formula's.
+__device__ __forceinline__ float product3(float x, float r, float w) {
+    const float t = x * r;
+    return fmaf(t, w, fmaf(x, r, -t) * w);
 }
 
 // ---- device: the 8-bit format -----------------------------------------------------

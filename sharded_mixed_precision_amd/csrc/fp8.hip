@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
             const bool inside = r0 + i < A.rows;  // what pads the tile stays 0 beside factors that are not finite
             const float r = inside ? A.row[r0 + i] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] = inside && j < n_cols ? (x[i][j] * r) * c[j] : 0.0f;
+            for (int j = 0; j < 8; ++j) x[i][j] = inside && j < n_cols ? product3(x[i][j], r, c[j]) : 0.0f;
         }
     }
 

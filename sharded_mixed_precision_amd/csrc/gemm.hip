@@ -25,10 +25,6 @@ struct GemmArgs {
 
 // ---- output -----------------------------------------------------------------------
 
-struct __attribute__((packed, aligned(4))) Float4 {
-    f32x4 v;
-};
-
 template <int T>
 __device__ __forceinline__ void put4_as(void *out, int64_t e, int n, f32x4 x, bool add) {
     if constexpr (T == DOPT_F32) {

@@ -27,8 +27,8 @@ static Shape shape_of(int64_t cols) {
     return {256, kLoop};
 }
 
-template <int LANES>
-__device__ __forceinline__ float row_sum(float s, float *shared) {
+template <int LANES, class F>
+__device__ __forceinline__ F row_sum(F s, F *shared) {
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m);
     if constexpr (LANES > 64) {
@@ -36,9 +36,21 @@ __device__ __forceinline__ float row_sum(float s, float *shared) {
         __syncthreads();  // the sums of the row before have been read
         if (threadIdx.x % 64 == 0) shared[w] = s;
         __syncthreads();
-        s = (shared[0] + shared[1]) + (shared[2] + shared[3]);
+        s = shared[0];
+#pragma unroll
+        for (int i = 1; i < LANES / 64; ++i) s += shared[i];
     }
     return s;
+}
+
+// 1 / sqrt(sum / cols + eps) to half a step of fp32: a 32-bit estimate and one
+// Newton step, whose residual is taken in 64 bits.
+__device__ __forceinline__ float rstd_of(double sum, int cols, double eps) {
+    const double m = sum / cols + eps;
+    const float r = 1.0f / sqrtf(static_cast<float>(m));
+    if (!(r > 0.0f && r < INFINITY)) return r;
+    const double e = 1.0 - m * (static_cast<double>(r) * r);
+    return static_cast<float>(r + 0.5 * r * e);
 }
 
 // ---- forward ----------------------------------------------------------------------
@@ -50,7 +62,7 @@ struct NormArgs {
     float *rstd;
     int64_t x_ld, res_ld, h_ld, y_ld, codes_ld, scale_ld;
     int32_t rows, cols, wdtype, per_xcd;
-    float eps;
+    double eps;
 };
 
 template <int T>
@@ -74,7 +86,7 @@ __device__ __forceinline__ void write_y(const NormArgs &A, int64_t row, int64_t 
     float w[8], y[8];
     load_vector8(A.weight, A.wdtype, e, n, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = j < n ? (x[j] * rstd) * w[j] : 0.0f;
+    for (int j = 0; j < 8; ++j) y[j] = j < n ? product3(x[j], rstd, w[j]) : 0.0f;
     if (A.y) store8<T>(A.y, row * A.y_ld + e, n, pack8<T>(y));
     if (A.codes) {
         uint32_t top = 0;
@@ -95,13 +107,13 @@ __device__ __forceinline__ int count8(int64_t cols, int64_t e) {
 
 template <int T, int LANES, int NV>
 __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs A) {
-    __shared__ float s_sum[4];
+    __shared__ double s_sum[4];
     const int t = threadIdx.x % LANES;
     // an XCD takes neighbouring rows, so that its L2 joins their scales' bytes
     const int64_t group = static_cast<int64_t>(blockIdx.x % 8) * A.per_xcd + blockIdx.x / 8;
     const int64_t row = group * (kNormThreads / LANES) + threadIdx.x / LANES;
     if (row >= A.rows) return;  // LANES = 256: all threads; 64: whole waves, which do not synchronise
-    float s = 0.0f;
+    double s = 0.0;
     if constexpr (NV != kLoop) {
         float x[NV][8];
 #pragma unroll
@@ -110,10 +122,13 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs A) {
             load_h<T>(A, row, e, count8(A.cols, e), x[v]);
         }
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) {
+            float q = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(x[v][j], x[v][j], s);
-        const float rstd = 1.0f / sqrtf(row_sum<LANES>(s, s_sum) / static_cast<float>(A.cols) + A.eps);
+            for (int j = 0; j < 8; ++j) q = fmaf(x[v][j], x[v][j], q);
+            s += q;
+        }
+        const float rstd = rstd_of(row_sum<LANES>(s, s_sum), A.cols, A.eps);
         if (A.rstd && t == 0) A.rstd[row] = rstd;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -130,7 +145,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs A) {
             for (int j = 0; j < 8; ++j) q = fmaf(x[j], x[j], q);
             s += q;
         }
-        const float rstd = 1.0f / sqrtf(row_sum<LANES>(s, s_sum) / static_cast<float>(A.cols) + A.eps);
+        const float rstd = rstd_of(row_sum<LANES>(s, s_sum), A.cols, A.eps);
         if (A.rstd && t == 0) A.rstd[row] = rstd;
         NormArgs B = A;  // h is written: x may be h itself, and is not added to again
         if (A.h) {
@@ -174,18 +189,34 @@ struct NormGradArgs {
     int32_t rows, cols, wdtype, workers;
 };
 
-// Workers (waves or workgroups, by the row's shape) share the rows and hold
-// the weight's grad of theirs in registers; their sums are joined in a fixed order.
-static int64_t workers_of(int64_t rows, int64_t) { return std::min<int64_t>(rows, 1024); }
+// Workgroups share the rows, a row to a wave or to the whole workgroup, and
+// hold the weight's grad of theirs in registers; a workgroup leaves one row of
+// sums, which k_norm_weight joins in a fixed order.
+constexpr int kMaxWorkers = 512;
+
+// As shape_of, with wider workgroups in place of more vectors to a thread: a
+// vector takes 40 registers here.
+static Shape grad_shape_of(int64_t cols) {
+    if (cols <= 4096) return shape_of(cols);
+    if (cols <= 8192) return {512, 2};
+    if (cols <= 16384) return {1024, 2};
+    return {1024, kLoop};
+}
+
+static int64_t workers_of(int64_t rows, int64_t cols) {
+    const int64_t at_once = std::max(1, kNormThreads / grad_shape_of(cols).lanes);
+    return std::min<int64_t>((rows + at_once - 1) / at_once, kMaxWorkers);
+}
 
 template <int T, int TD, int LANES, int NV>
-__global__ __launch_bounds__(kNormThreads) void k_norm_grad(NormGradArgs A) {
-    __shared__ float s_sum[4];
-    const int t = threadIdx.x % LANES;
-    const int worker = blockIdx.x * (kNormThreads / LANES) + threadIdx.x / LANES;
-    if (worker >= A.workers) return;
+__global__ __launch_bounds__(LANES > kNormThreads ? LANES : kNormThreads) void k_norm_grad(NormGradArgs A) {
+    constexpr int kAtOnce = LANES < kNormThreads ? kNormThreads / LANES : 1;
+    __shared__ float s_sum[LANES / 64];
+    __shared__ float s_dw[LANES == 64 ? kAtOnce - 1 : 1][LANES == 64 ? LANES * NV * 8 : 1];
+    const int t = threadIdx.x % LANES, part_of = threadIdx.x / LANES;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kAtOnce + part_of, next = static_cast<int64_t>(A.workers) * kAtOnce;
     const float cols = static_cast<float>(A.cols);
-    float *part = A.part + static_cast<int64_t>(worker) * A.cols;
+    float *part = A.part + static_cast<int64_t>(blockIdx.x) * A.cols;
     if constexpr (NV != kLoop) {
         float w[NV][8], dw[NV][8];
 #pragma unroll
@@ -195,7 +226,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_grad(NormGradArgs A) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) dw[v][j] = 0.0f;
         }
-        for (int64_t row = worker; row < A.rows; row += A.workers) {
+        for (int64_t row = first; row < A.rows; row += next) {
             Raw8<TD> dy[NV];
             Raw8<T> h[NV], dh[NV];
 #pragma unroll
@@ -227,14 +258,29 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_grad(NormGradArgs A) {
                 store8<T>(A.dx, row * A.dx_ld + e, count8(A.cols, e), pack8<T>(x));
             }
         }
+        if constexpr (LANES == 64) {
+            if (part_of > 0) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s_dw[part_of - 1][(8 * v + j) * 64 + t] = dw[v][j];
+            }
+            __syncthreads();
+            if (part_of > 0) return;
+#pragma unroll
+            for (int i = 0; i < kAtOnce - 1; ++i)
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dw[v][j] += s_dw[i][(8 * v + j) * 64 + t];
+        }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int64_t e = 8 * (t + int64_t(LANES) * v);
             store8<DOPT_F32>(part, e, count8(A.cols, e), pack8<DOPT_F32>(dw[v]));
         }
     } else {
-        bool first = true;
-        for (int64_t row = worker; row < A.rows; row += A.workers, first = false) {
+        for (int64_t row = first; row < A.rows; row += next) {
             const float rstd = A.rstd[row];
             float s = 0.0f;
             for (int64_t e = 8 * t; e < A.cols; e += 8 * LANES) {
@@ -254,7 +300,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_grad(NormGradArgs A) {
                 unpack8<TD>(load8<TD>(A.dy, row * A.dy_ld + e, n), d);
                 unpack8<T>(load8<T>(A.h, row * A.h_ld + e, n), hx);
                 load_vector8(A.weight, A.wdtype, e, n, w);
-                unpack8<DOPT_F32>(load8<DOPT_F32>(part, e, first ? 0 : n), dw);
+                unpack8<DOPT_F32>(load8<DOPT_F32>(part, e, row == first ? 0 : n), dw);
                 unpack8<T>(load8<T>(A.dh ? A.dh : A.h, row * (A.dh ? A.dh_ld : A.h_ld) + e, A.dh ? n : 0), r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -269,45 +315,60 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_grad(NormGradArgs A) {
     }
 }
 
-// The workers' sums of 32 columns: 32 slices of the workers, 8 lanes of 4 columns each.
-__global__ __launch_bounds__(kNormThreads) void k_norm_weight(const float *part, int workers, int cols, void *out,
-                                                              int32_t dtype, int accumulate) {
-    __shared__ float s_part[32][33];
-    const int lane = threadIdx.x % 32, first = threadIdx.x / 32;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+// The workers' sums of 32 columns: 8 lanes of 4 columns each, 128 slices of
+// the workers, so that a thread has at most 4 loads, all under way at once.
+constexpr int kJoinThreads = 1024;
+
+__global__ __launch_bounds__(kJoinThreads) void k_norm_weight(const float *part, int workers, int cols, void *out,
+                                                               int32_t dtype, int accumulate) {
+    __shared__ f32x4 s_part[kJoinThreads / 64][8];
+    const int lane = threadIdx.x % 8, slice = threadIdx.x / 8;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 32 + 4 * lane;
+    const int n = c0 >= cols ? 0 : cols - c0 >= 4 ? 4 : static_cast<int>(cols - c0);
+    f32x4 s = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float s = 0.0f;
-        if (c < cols)
-            for (int w = first + 8 * i; w < workers; w += 32) s += part[static_cast<int64_t>(w) * cols + c];
-        s_part[first + 8 * i][lane] = s;
+    for (int i = 0; i < kMaxWorkers / 128; ++i) {
+        const int w = slice + 128 * i;
+        if (w >= workers || n == 0) continue;
+        const float *p = part + static_cast<int64_t>(w) * cols + c0;
+        if (n == 4) {
+            s += reinterpret_cast<const Float4 *>(p)->v;
+        } else {
+            for (int j = 0; j < n; ++j) s[j] += p[j];
+        }
     }
-    __syncthreads();
-    if (threadIdx.x >= 32 || c >= cols) return;
-    float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += s_part[i][lane];
+    for (int m = 8; m < 64; m <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] += __shfl_xor(s[j], m);
+    if (threadIdx.x % 64 < 8) s_part[threadIdx.x / 64][lane] = s;
+    __syncthreads();
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+    if (threadIdx.x >= 32 || c >= cols) return;
+    float s1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 64; ++i) s1 += s_part[i][threadIdx.x / 4][threadIdx.x % 4];
     if (dtype == DOPT_F32) {
         float *p = static_cast<float *>(out) + c;
-        *p = accumulate ? *p + s : s;
+        *p = accumulate ? *p + s1 : s1;
     } else {
         uint16_t *p = static_cast<uint16_t *>(out) + c;
-        if (dtype == DOPT_BF16) *p = static_cast<uint16_t>(from_float<DOPT_BF16>(accumulate ? to_float<DOPT_BF16>(*p) + s : s));
-        else *p = static_cast<uint16_t>(from_float<DOPT_F16>(accumulate ? to_float<DOPT_F16>(*p) + s : s));
+        if (dtype == DOPT_BF16) *p = static_cast<uint16_t>(from_float<DOPT_BF16>(accumulate ? to_float<DOPT_BF16>(*p) + s1 : s1));
+        else *p = static_cast<uint16_t>(from_float<DOPT_F16>(accumulate ? to_float<DOPT_F16>(*p) + s1 : s1));
     }
 }
 
 template <int T, int TD>
 static void launch_norm_grad(const NormGradArgs &A, hipStream_t stream) {
-    const Shape s = shape_of(A.cols);
-    const unsigned grid = static_cast<unsigned>((int64_t(A.workers) * s.lanes + kNormThreads - 1) / kNormThreads);
+    const Shape s = grad_shape_of(A.cols);
+    const unsigned grid = static_cast<unsigned>(A.workers);
     if (s.lanes == 64 && s.nv == 1) k_norm_grad<T, TD, 64, 1><<<grid, kNormThreads, 0, stream>>>(A);
     else if (s.lanes == 64) k_norm_grad<T, TD, 64, 2><<<grid, kNormThreads, 0, stream>>>(A);
-    else if (s.nv == 1) k_norm_grad<T, TD, 256, 1><<<grid, kNormThreads, 0, stream>>>(A);
-    else if (s.nv == 2) k_norm_grad<T, TD, 256, 2><<<grid, kNormThreads, 0, stream>>>(A);
-    else if (s.nv == 4) k_norm_grad<T, TD, 256, 4><<<grid, kNormThreads, 0, stream>>>(A);
-    else if (s.nv == 8) k_norm_grad<T, TD, 256, 8><<<grid, kNormThreads, 0, stream>>>(A);
-    else k_norm_grad<T, TD, 256, kLoop><<<grid, kNormThreads, 0, stream>>>(A);
+    else if (s.lanes == 256 && s.nv == 1) k_norm_grad<T, TD, 256, 1><<<grid, kNormThreads, 0, stream>>>(A);
+    else if (s.lanes == 256) k_norm_grad<T, TD, 256, 2><<<grid, 256, 0, stream>>>(A);
+    else if (s.lanes == 512) k_norm_grad<T, TD, 512, 2><<<grid, 512, 0, stream>>>(A);
+    else if (s.nv == 2) k_norm_grad<T, TD, 1024, 2><<<grid, 1024, 0, stream>>>(A);
+    else k_norm_grad<T, TD, 1024, kLoop><<<grid, 1024, 0, stream>>>(A);
 }
 
 // `x` is of the size and type of `like`.
@@ -385,7 +446,7 @@ extern "C" int dopt_rmsnorm(const dopt_dense *x, const dopt_dense *residual, con
     A.rstd = rstd;
     A.rows = static_cast<int32_t>(x->rows);
     A.cols = static_cast<int32_t>(x->cols);
-    A.eps = static_cast<float>(eps);
+    A.eps = eps;
     if (x->dtype == DOPT_F32) launch_norm<DOPT_F32>(A, stream);
     else if (x->dtype == DOPT_BF16) launch_norm<DOPT_BF16>(A, stream);
     else launch_norm<DOPT_F16>(A, stream);
@@ -454,7 +515,7 @@ extern "C" int dopt_rmsnorm_grad(const dopt_dense *dy, const dopt_dense *h, cons
         if (int rc = launched("dopt_rmsnorm_grad")) return rc;
     }
     if (workers == 0 && accumulate) return DOPT_OK;
-    k_norm_weight<<<static_cast<unsigned>((h->cols + 31) / 32), kNormThreads, 0, stream>>>(
+    k_norm_weight<<<static_cast<unsigned>((h->cols + 31) / 32), kJoinThreads, 0, stream>>>(
         static_cast<const float *>(workspace), static_cast<int>(workers), static_cast<int>(h->cols), dweight, dweight_dtype, accumulate);
     return launched("dopt_rmsnorm_grad");
 }
