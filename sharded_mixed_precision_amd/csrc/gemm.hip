@@ -65,6 +65,59 @@ __device__ __forceinline__ void put4(const GemmArgs &A, int row, int col, f32x4 
     else put4_as<DOPT_F16>(A.out, e, n, x, A.accumulate);
 }
 
+// A wave's results, FI x 16 rows and FJ x 16 columns from (m0, n0) on in groups of 64, as
+// the matrix instruction leaves them: register v of a lane is row 4 * (lane / 16) + v of
+// its 16 and column lane % 16, and instruction i and j of a group hold every fourth row and
+// column from i and j on.  Four neighbours of a row are stored at once.  The type is
+// told apart once: straight code for one type, 64 stores of it, is
+// what a tile fetches, and not the branches of all.
+template <int T, bool ADD, bool WHOLE, int FI, int FJ>
+__device__ __forceinline__ void store_as(const GemmArgs &A, int m0, int n0, const f32x4 (&acc)[FI][FJ]) {
+    const int lane = threadIdx.x % 64;
+    const int row0 = m0 + 16 * (lane / 16), col0 = n0 + 4 * (lane % 16);
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int h = 0; h < FJ / 4; ++h) {
+                const int row = row0 + i / 4 * 64 + 4 * v + i % 4, col = col0 + 64 * h;
+                const f32x4 x = {acc[i][4 * h][v], acc[i][4 * h + 1][v], acc[i][4 * h + 2][v], acc[i][4 * h + 3][v]};
+                const int64_t e = static_cast<int64_t>(row) * A.out_ld + col;
+                if constexpr (WHOLE) {
+                    put4_as<T>(A.out, e, 4, x, ADD);
+                } else if (row < A.m) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (col + c < A.n) {
+                            if constexpr (T == DOPT_F32) {
+                                float *p = static_cast<float *>(A.out) + e + c;
+                                *p = ADD ? *p + x[c] : x[c];
+                            } else {
+                                uint16_t *p = static_cast<uint16_t *>(A.out) + e + c;
+                                *p = static_cast<uint16_t>(from_float<T>(ADD ? to_float<T>(*p) + x[c] : x[c]));
+                            }
+                        }
+                }
+            }
+}
+
+template <int T, int FI, int FJ>
+__device__ __forceinline__ void store_typed(const GemmArgs &A, int m0, int n0, const f32x4 (&acc)[FI][FJ]) {
+    const bool whole = m0 + 16 * FI <= A.m && n0 + 16 * FJ <= A.n;
+    if (whole && !A.accumulate) store_as<T, false, true>(A, m0, n0, acc);
+    else if (whole) store_as<T, true, true>(A, m0, n0, acc);
+    else if (!A.accumulate) store_as<T, false, false>(A, m0, n0, acc);
+    else store_as<T, true, false>(A, m0, n0, acc);
+}
+
+template <bool EXACT, int FI, int FJ>
+__device__ __forceinline__ void store_tile(const GemmArgs &A, int m0, int n0, const f32x4 (&acc)[FI][FJ]) {
+    if constexpr (EXACT) store_typed<DOPT_F32>(A, m0, n0, acc);
+    else if (A.dtype == DOPT_BF16) store_typed<DOPT_BF16>(A, m0, n0, acc);
+    else store_typed<DOPT_F16>(A, m0, n0, acc);
+}
+
 // A split's sums; rows of part are padded to 4.
 __device__ __forceinline__ void put4_part(const GemmArgs &A, int split, int row, int col, f32x4 x) {
     if (row >= A.m || col >= A.n) return;
@@ -148,6 +201,31 @@ __device__ __forceinline__ void load_lds4(uint32_t to, uint32_t offset, const ui
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
 
+// Where workgroup blockIdx.x's tile lies.  Each XCD takes neighbouring tiles, in
+// bands of 8 tile rows, so that its L2 serves them all.
+__device__ __forceinline__ void place_tile(const GemmArgs &A, int rows, int cols, int &m0, int &n0) {
+    constexpr int kBand = 8;
+    const int total = A.tiles_m * A.tiles_n, q = total / 8, rem = total % 8;
+    const int x = blockIdx.x % 8, i = blockIdx.x / 8;
+    const int tile = x * q + min(x, rem) + i;
+    const int band = tile / (kBand * A.tiles_n), in_band = tile % (kBand * A.tiles_n);
+    const int height = min(kBand, A.tiles_m - band * kBand);
+    m0 = (band * kBand + in_band % height) * rows;
+    n0 = in_band / height * cols;
+}
+
+// A wave's load l brings 8 slots of a tile to shared memory: where in the operand,
+// which has `rows` rows from the tile's first, a lane's 16 bytes lie.  Rows past the
+// last are read as the last: their results are not stored.
+__device__ __forceinline__ uint32_t slot_offset(int l, int lane, int rows, int ld) {
+    const int slot = 8 * l + lane / 8, r = slot % 16;
+    const int row = min(slot / 64 * 64 + 4 * r + slot % 64 / 16, rows - 1);
+    return static_cast<uint32_t>(row) * static_cast<uint32_t>(ld) + 16u * ((lane % 8) ^ (r / 2));
+}
+
+// Waits for a wave's own loads to shared memory and reads of it, then for the other waves.
+__device__ __forceinline__ void settle() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // A workgroup forms BM x BN of the output with WM x WN waves, each a part of
 // (BM / WM) x (BN / WN).  Per step of 128 along k, both operands' rows come
 // to shared memory, the next step's while this one's are multiplied.
@@ -171,34 +249,19 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_gemm_tile(GemmArgs A) {
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wm = wave / WN, wn = wave % WN;
 
-    // each XCD takes neighbouring tiles, in bands of 8 tile rows, so that its L2 serves them all
-    int tile;
-    {
-        const int total = A.tiles_m * A.tiles_n, q = total / 8, rem = total % 8;
-        const int x = blockIdx.x % 8, i = blockIdx.x / 8;
-        tile = x * q + min(x, rem) + i;
-    }
-    constexpr int kBand = 8;
-    const int band = tile / (kBand * A.tiles_n), in_band = tile % (kBand * A.tiles_n);
-    const int height = min(kBand, A.tiles_m - band * kBand);
-    const int m0 = (band * kBand + in_band % height) * BM, n0 = in_band / height * BN;
+    int m0, n0;
+    place_tile(A, BM, BN, m0, n0);
 
     const int split = blockIdx.y;
     const int first = split * A.split_steps, steps = min(A.split_steps, A.steps - first);
 
-    // rows past the last are read as the last: their results are not stored
     const uint8_t *pa = A.a + static_cast<int64_t>(m0) * A.a_ld + static_cast<int64_t>(first) * kStep;
     const uint8_t *pb = A.b + static_cast<int64_t>(n0) * A.b_ld + static_cast<int64_t>(first) * kStep;
     uint32_t off_a[kLoadsA], off_b[kLoadsB];
-    const auto place = [&](int load, int rows, int ld) {  // where a lane's 16 bytes of a load lie in the operand
-        const int slot = 8 * load + lane / 8, r = slot % 16;
-        const int row = min(slot / 64 * 64 + 4 * r + slot % 64 / 16, rows - 1);
-        return static_cast<uint32_t>(row) * static_cast<uint32_t>(ld) + 16u * ((lane % 8) ^ (r / 2));
-    };
 #pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) off_a[i] = place(wave * kLoadsA + i, A.m - m0, A.a_ld);
+    for (int i = 0; i < kLoadsA; ++i) off_a[i] = slot_offset(wave * kLoadsA + i, lane, A.m - m0, A.a_ld);
 #pragma unroll
-    for (int i = 0; i < kLoadsB; ++i) off_b[i] = place(wave * kLoadsB + i, A.n - n0, A.b_ld);
+    for (int i = 0; i < kLoadsB; ++i) off_b[i] = slot_offset(wave * kLoadsB + i, lane, A.n - n0, A.b_ld);
     const uint8_t *psa = A.as + first * A.as_ld, *psb = A.bs + first * A.bs_ld;
     const uint32_t off_sa = min(m0 + 4 * lane, (A.m + 3) / 4 * 4 - 4);
     const uint32_t off_sb = min(n0 + 4 * lane, (A.n + 3) / 4 * 4 - 4);
@@ -217,7 +280,6 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_gemm_tile(GemmArgs A) {
         psa += A.as_ld;
         psb += A.bs_ld;
     };
-    const auto settle = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
     f32x4 acc[4 * GA][4 * GB];
 #pragma unroll
@@ -302,21 +364,302 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_gemm_tile(GemmArgs A) {
         settle();
     }
 
-    // result register v of a lane: row 4 * quarter + v of the instruction's 16, column lane % 16
+    const int row0 = m0 + wm * (BM / WM), col0 = n0 + wn * (BN / WN);
+    if (A.splits == 1) {
+        store_tile<EXACT>(A, row0, col0, acc);
+        return;
+    }
 #pragma unroll
-    for (int i = 0; i < 4 * GA; ++i) {
+    for (int i = 0; i < 4 * GA; ++i)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int row = m0 + wm * (BM / WM) + i / 4 * 64 + 4 * (4 * quarter + v) + i % 4;
+        for (int v = 0; v < 4; ++v)
 #pragma unroll
-            for (int h = 0; h < GB; ++h) {
-                const int col = n0 + wn * (BN / WN) + 64 * h + 4 * r;
-                const f32x4 x = {acc[i][4 * h][v], acc[i][4 * h + 1][v], acc[i][4 * h + 2][v], acc[i][4 * h + 3][v]};
-                if (A.splits > 1) put4_part(A, split, row, col, x);
-                else put4(A, row, col, x);
-            }
+            for (int h = 0; h < GB; ++h)
+                put4_part(A, split, row0 + i / 4 * 64 + 4 * (4 * quarter + v) + i % 4, col0 + 64 * h + 4 * r,
+                          f32x4{acc[i][4 * h][v], acc[i][4 * h + 1][v], acc[i][4 * h + 2][v], acc[i][4 * h + 3][v]});
+}
+
+// ---- large tiles --------------------------------------------------------------------
+
+constexpr int kBig = 256;                            // rows and columns of a tile
+constexpr int kBigOperand = kBig * kStep;            // bytes of an operand's rows in a step
+constexpr int kBigBuffer = 2 * kBigOperand + 512;    // both, and 256 bytes of scales for each
+
+// A wave's share of a step's loads: 32 / WAVES of 1 KB for each operand, numbered from 0,
+// the scales with the last.  Then it goes on to the next step, or after the last
+// step to that one again: the loops below have no branches, since the compiler
+// would gather all products behind the last of them.  Even waves bring the
+// same scales of a, odd ones of b (TILE: of a again).
+template <int WAVES, bool BROW>
+struct Loads {
+    static constexpr int kEach = 32 / WAVES, kAll = 2 * kEach;
+    uint32_t off_a[kEach], off_b[kEach], off_s, lds, to_s, to;
+    const uint8_t *pa, *pb, *ps;
+    int64_t s_ld;
+    int left;
+
+    __device__ __forceinline__ Loads(const GemmArgs &A, const uint8_t *mem, int m0, int n0, int lane, int wave) {
+        pa = A.a + static_cast<int64_t>(m0) * A.a_ld;
+        pb = A.b + static_cast<int64_t>(n0) * A.b_ld;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            off_a[i] = slot_offset(kEach * wave + i, lane, A.m - m0, A.a_ld);
+            off_b[i] = slot_offset(kEach * wave + i, lane, A.n - n0, A.b_ld);
+        }
+        const bool of_b = BROW && wave % 2;
+        ps = of_b ? A.bs : A.as;
+        s_ld = of_b ? A.bs_ld : A.as_ld;
+        off_s = of_b ? min(n0 + 4 * lane, (A.n + 3) / 4 * 4 - 4) : min(m0 + 4 * lane, (A.m + 3) / 4 * 4 - 4);
+        lds = __builtin_amdgcn_readfirstlane(lds_address(mem));
+        to = lds + 1024 * kEach * wave;
+        to_s = lds + 2 * kBigOperand + (of_b ? 256 : 0);
+        left = A.steps;
+    }
+
+    __device__ __forceinline__ void start(int buffer, int i) {
+        if (i < kEach) load_lds16(to + buffer + 1024 * i, off_a[i % kEach], pa);
+        else load_lds16(to + buffer + kBigOperand + 1024 * (i - kEach), off_b[i % kEach], pb);
+        if (i == kAll - 1) {
+            load_lds4(to_s + buffer, off_s, ps);
+            const bool more = --left > 0;
+            pa += more ? kStep : 0;
+            pb += more ? kStep : 0;
+            ps += more ? s_ld : 0;
         }
     }
+};
+
+// A TILE operand's scales of a wave's columns: lane l holds that of step 64 c + l, and
+// in `next` that of step 64 (c + 1) + l.
+struct TileScales {
+    const uint8_t *p;
+    int64_t ld;
+    int steps, now, next;
+
+    __device__ __forceinline__ int load(int k, int lane) const {
+        int x = p[static_cast<int64_t>(min(k + lane, steps - 1)) * ld];
+        asm volatile("" : "+v"(x));  // waited for here, with no other loads under way
+        return x;
+    }
+    __device__ __forceinline__ int of(int k, int chunk_end) const {
+        const int x = __builtin_amdgcn_readlane(now, k % 64), y = __builtin_amdgcn_readlane(next, 0);
+        return (k == chunk_end ? y : x) * 0x01010101;
+    }
+};
+
+// Keeps the instructions before and after apart, so that reads stay between the products.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// 256 x 256 of the output by 4 waves, one to a SIMD with all of its registers, each
+// 128 x 128.  As k_gemm_tile, but a step has two phases with its one barrier
+// between them, so that the matrix cores have work on both sides of it:
+//   phase 0 multiplies the first 64 rows of a, and reads the others;
+//   barrier all have read this step, whose buffer is free, and the next step's loads are done;
+//   phase 1 multiplies the other rows, starts the loads of the step after the next into the
+//           free buffer, and reads the next step's first 64 rows of a and all of b, each
+//           register once its last product is under way.
+template <bool BROW>
+__global__ __launch_bounds__(256, 1) void k_gemm_big(GemmArgs A) {
+    __shared__ __align__(16) uint8_t s_mem[2 * kBigBuffer];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = wave / 2, wn = wave % 2;
+    int m0, n0;
+    place_tile(A, kBig, kBig, m0, n0);
+    Loads<4, BROW> loads(A, s_mem, m0, n0, lane, wave);
+    TileScales ts{A.bs + min(n0 + wn * 128, A.n - 1) / DOPT_FP8_BLOCK, A.bs_ld, A.steps, 0, 0};
+
+    f32x4 acc[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    const int r = lane % 16, quarter = lane / 16;
+    const uint32_t low = r * kStep + 16 * (quarter ^ (r / 2)), high = r * kStep + 16 * ((quarter + 4) ^ (r / 2));
+    const uint8_t *ma = s_mem + wm * 128 * kStep, *mb = s_mem + kBigOperand + wn * 128 * kStep;
+    const uint8_t *ms = s_mem + 2 * kBigOperand + 4 * r;
+    const auto read = [&](i32x8 &x, const uint8_t *mem, int at) {  // the 16 rows from slot `at`
+        x = join(*reinterpret_cast<const i32x4 *>(mem + at * kStep + low), *reinterpret_cast<const i32x4 *>(mem + at * kStep + high));
+    };
+    const auto scales_a = [&](int buffer, int g) { return *reinterpret_cast<const int *>(ms + buffer + wm * 128 + 64 * g); };
+    const auto scales_b = [&](int buffer, int g, int k, int chunk_end) {
+        if (BROW) return *reinterpret_cast<const int *>(ms + buffer + 256 + wn * 128 + 64 * g);
+        return ts.of(k, chunk_end);
+    };
+
+    if (A.steps > 0) {
+        if (!BROW) ts.now = ts.load(0, lane);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) loads.start(0, i);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) loads.start(kBigBuffer, i);
+    }
+    settle();
+    i32x8 a[8], b[8];
+    int sa[2] = {scales_a(0, 0), scales_a(0, 1)}, sb[2] = {scales_b(0, 0, 0, 64), scales_b(0, 1, 0, 64)};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) read(b[j], mb, 16 * j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) read(a[i], ma, 16 * i);
+    __builtin_amdgcn_s_waitcnt(0);  // so that in the loop only the loop's own reads are waited for
+    for (int chunk_at = 0; chunk_at < A.steps; chunk_at += 64) {
+        const int chunk_end = min(chunk_at + 64, A.steps);
+        if (!BROW && chunk_at > 0) ts.now = ts.next;
+        if (!BROW) ts.next = ts.load(chunk_end, lane);
+        for (int k = chunk_at; k < chunk_end; ++k) {
+            const int cur = (k & 1) * kBigBuffer, nxt = kBigBuffer - cur;
+            each4([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                read(a[4 + i], ma + cur, 16 * (4 + i));
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    each4([&](auto J) {
+                        constexpr int j = decltype(J)::value;
+                        acc[i][4 * g + j] = mfma<i, j>(a[i], b[4 * g + j], acc[i][4 * g + j], sa[0], sb[g]);
+                    });
+                in_order();
+            });
+            settle();
+            in_order();
+            const int next_sa0 = scales_a(nxt, 0), next_sa1 = scales_a(nxt, 1);
+            const int next_sb0 = scales_b(nxt, 0, k + 1, chunk_end), next_sb1 = scales_b(nxt, 1, k + 1, chunk_end);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                each4([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    loads.start(cur, 2 * (4 * g + j));
+                    loads.start(cur, 2 * (4 * g + j) + 1);
+                    if (g == 0) read(a[j], ma + nxt, 16 * j);
+                    each4([&](auto I) {
+                        constexpr int i = decltype(I)::value;
+                        acc[4 + i][4 * g + j] = mfma<i, j>(a[4 + i], b[4 * g + j], acc[4 + i][4 * g + j], sa[1], sb[g]);
+                    });
+                    in_order();
+                    read(b[4 * g + j], mb + nxt, 16 * (4 * g + j));
+                    in_order();
+                });
+            sa[0] = next_sa0;
+            sa[1] = next_sa1;
+            sb[0] = next_sb0;
+            sb[1] = next_sb1;
+        }
+    }
+    settle();  // the loads past the last step land in this workgroup's shared memory, so it stays until they have
+    store_tile<false>(A, m0 + wm * 128, n0 + wn * 128, acc);
+}
+
+// The same tile with widened codes, by 8 waves of 128 x 64 each.  A step has 16
+// turns, one for each half of its k and 16 rows of a, of 8 products.  A turn
+// multiplies what the one before has widened, widens the next one's rows and reads those of
+// the one after that; the columns of b are widened anew for each half, each right after
+// its last product.  The barrier stands before the last turn, when all of the step has been
+// read: the next step's loads, started in the first 8 turns, have landed by then.
+template <bool BROW>
+__global__ __launch_bounds__(512, 2) void k_gemm_wide(GemmArgs A) {
+    __shared__ __align__(16) uint8_t s_mem[2 * kBigBuffer];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = wave / 4, wn = wave % 4;
+    int m0, n0;
+    place_tile(A, kBig, kBig, m0, n0);
+    Loads<8, BROW> loads(A, s_mem, m0, n0, lane, wave);
+    TileScales ts{A.bs + min(n0 + wn * 64, A.n - 1) / DOPT_FP8_BLOCK, A.bs_ld, A.steps, 0, 0};
+
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    const int r = lane % 16, quarter = lane / 16;
+    const uint32_t low = r * kStep + 16 * (quarter ^ (r / 2)), high = r * kStep + 16 * ((quarter + 4) ^ (r / 2));
+    const uint8_t *ma = s_mem + wm * 128 * kStep, *mb = s_mem + kBigOperand + wn * 64 * kStep;
+    const uint8_t *ms = s_mem + 2 * kBigOperand + 4 * r;
+    const auto chunk = [&](const uint8_t *mem, int at, uint32_t half) {  // of the 16 rows from slot `at`
+        return *reinterpret_cast<const i32x4 *>(mem + at * kStep + half);
+    };
+    const auto scales_a = [&](int buffer, int g) { return *reinterpret_cast<const int *>(ms + buffer + wm * 128 + 64 * g); };
+    const auto scales_b = [&](int buffer, int k, int chunk_end) {
+        if (BROW) return *reinterpret_cast<const int *>(ms + buffer + 256 + wn * 64);
+        return ts.of(k, chunk_end);
+    };
+
+    if (A.steps > 0) {
+        if (!BROW) ts.now = ts.load(0, lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) loads.start(0, i);
+    }
+    settle();
+    bf16x8 wb[4][2], wa[2];
+    i32x4 ra[2], rb[4];
+    const auto widen_b = [&](int scales, auto J) {
+        constexpr int j = decltype(J)::value;
+        const float scale = scale_of<j>(scales);
+        wb[j][0] = widen8(rb[j][0], rb[j][1], scale);
+        wb[j][1] = widen8(rb[j][2], rb[j][3], scale);
+    };
+    int sa[2] = {scales_a(0, 0), scales_a(0, 1)}, sb = scales_b(0, 0, 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rb[j] = chunk(mb, 16 * j, low);
+    ra[0] = chunk(ma, 0, low);
+    ra[1] = chunk(ma, 16, low);
+    each4([&](auto J) { widen_b(sb, J); });
+    wa[0] = widen8(ra[0][0], ra[0][1], scale_of<0>(sa[0]));
+    wa[1] = widen8(ra[0][2], ra[0][3], scale_of<0>(sa[0]));
+    __builtin_amdgcn_s_waitcnt(0);
+    for (int chunk_at = 0; chunk_at < A.steps; chunk_at += 64) {
+        const int chunk_end = min(chunk_at + 64, A.steps);
+        if (!BROW && chunk_at > 0) ts.now = ts.next;
+        if (!BROW) ts.next = ts.load(chunk_end, lane);
+        for (int k = chunk_at; k < chunk_end; ++k) {
+            const int cur = (k & 1) * kBigBuffer, nxt = kBigBuffer - cur;
+            const auto turn = [&](auto T) {
+                constexpr int t = decltype(T)::value, i = t % 8, n = (t + 1) % 8;
+                if constexpr (t < 8) loads.start(nxt, t);
+                if constexpr (t == 15) {
+                    settle();
+                    in_order();
+                    sa[0] = scales_a(nxt, 0);
+                    sb = scales_b(nxt, k + 1, chunk_end);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) rb[j] = chunk(mb + nxt, 16 * j, low);
+                    ra[0] = chunk(ma + nxt, 0, low);
+                    ra[1] = chunk(ma + nxt, 16, low);
+                    sa[1] = scales_a(nxt, 1);
+                } else if constexpr (t < 14) {
+                    ra[t % 2] = chunk(ma + cur, 16 * ((t + 2) % 8), t + 2 < 8 ? low : high);
+                }
+                if constexpr (t == 6) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) rb[j] = chunk(mb + cur, 16 * j, high);
+                }
+                bf16x8 x0, x1;
+                each4([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    acc[i][j] = mfma(wa[0], wb[j][0], acc[i][j]);
+                    if (t < 15 && j == 1) x0 = widen8(ra[(t + 1) % 2][0], ra[(t + 1) % 2][1], scale_of<n % 4>(sa[n / 4]));
+                    if (t < 15 && j == 3) x1 = widen8(ra[(t + 1) % 2][2], ra[(t + 1) % 2][3], scale_of<n % 4>(sa[n / 4]));
+                });
+                each4([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    acc[i][j] = mfma(wa[1], wb[j][1], acc[i][j]);
+                    if constexpr (i == 7) widen_b(sb, J);
+                });
+                if constexpr (t == 15) {
+                    x0 = widen8(ra[0][0], ra[0][1], scale_of<0>(sa[0]));
+                    x1 = widen8(ra[0][2], ra[0][3], scale_of<0>(sa[0]));
+                }
+                wa[0] = x0;
+                wa[1] = x1;
+                in_order();
+            };
+            each4([&](auto T) { turn(T); });
+            each4([&](auto T) { turn(std::integral_constant<int, 4 + decltype(T)::value>{}); });
+            each4([&](auto T) { turn(std::integral_constant<int, 8 + decltype(T)::value>{}); });
+            each4([&](auto T) { turn(std::integral_constant<int, 12 + decltype(T)::value>{}); });
+        }
+    }
+    settle();
+    store_tile<true>(A, m0 + wm * 128, n0 + wn * 64, acc);
 }
 
 // ---- few rows ---------------------------------------------------------------------
@@ -419,7 +762,8 @@ static void launch_gemm(const GemmArgs &A, const Plan &p, hipStream_t stream) {
         else if (p.rows == 32) k_gemm_few<2, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
         else k_gemm_few<4, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
     } else if (p.rows == 256) {
-        k_gemm_tile<256, 256, 2, 4, BROW, EXACT><<<grid, 512, 0, stream>>>(A);
+        if constexpr (EXACT) k_gemm_wide<BROW><<<grid, 512, 0, stream>>>(A);
+        else k_gemm_big<BROW><<<grid, 256, 0, stream>>>(A);
     } else {
         k_gemm_tile<128, 128, 2, 2, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
     }
