@@ -226,199 +226,50 @@ __device__ __forceinline__ uint32_t slot_offset(int l, int lane, int rows, int l
 // Waits for a wave's own loads to shared memory and reads of it, then for the other waves.
 __device__ __forceinline__ void settle() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// A workgroup forms BM x BN of the output with WM x WN waves, each a part of
-// (BM / WM) x (BN / WN).  Per step of 128 along k, both operands' rows come
-// to shared memory, the next step's while this one's are multiplied.
-//
-// In shared memory a group of 64 rows lies in the order 0, 4, 8, .. 60, 1, 5, ..:
-// slot 16 i + r holds row 4 r + i.  The matrix instruction that takes slots 16 i
-// to 16 i + 15 thereby finds its rows' scales in byte i of the dword of row
-// 4 r, one dword for four instructions, and a lane's four results along
-// a row of the output are neighbours, which are stored at once.  Within a slot's
-// 128 bytes the 16-byte chunk c lies at c ^ (r / 2), which spreads the
-// 16 rows that a quarter of a wave reads over all banks.
-template <int BM, int BN, int WM, int WN, bool BROW, bool EXACT>
-__global__ __launch_bounds__(WM *WN * 64, 2) void k_gemm_tile(GemmArgs A) {
-    constexpr int kWaves = WM * WN;
-    constexpr int GA = BM / WM / 64, GB = BN / WN / 64;
-    constexpr int kA = BM * kStep, kB = BN * kStep;
-    constexpr int kBuffer = kA + kB + 512;  // and 256 bytes of scales for each
-    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves;
-    __shared__ __align__(16) uint8_t s_mem[2 * kBuffer];
+// Keeps the instructions before and after apart, so that reads stay between the products.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
-    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wm = wave / WN, wn = wave % WN;
+// A step's part of a workgroup's shared memory: SIDE rows of either operand and 256
+// bytes for the scales of each.
+template <int SIDE>
+struct StepMem {
+    static constexpr int kB = SIDE * kStep, kScalesA = 2 * SIDE * kStep, kScalesB = kScalesA + 256, kBytes = kScalesA + 512;
+};
 
-    int m0, n0;
-    place_tile(A, BM, BN, m0, n0);
-
-    const int split = blockIdx.y;
-    const int first = split * A.split_steps, steps = min(A.split_steps, A.steps - first);
-
-    const uint8_t *pa = A.a + static_cast<int64_t>(m0) * A.a_ld + static_cast<int64_t>(first) * kStep;
-    const uint8_t *pb = A.b + static_cast<int64_t>(n0) * A.b_ld + static_cast<int64_t>(first) * kStep;
-    uint32_t off_a[kLoadsA], off_b[kLoadsB];
-#pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) off_a[i] = slot_offset(wave * kLoadsA + i, lane, A.m - m0, A.a_ld);
-#pragma unroll
-    for (int i = 0; i < kLoadsB; ++i) off_b[i] = slot_offset(wave * kLoadsB + i, lane, A.n - n0, A.b_ld);
-    const uint8_t *psa = A.as + first * A.as_ld, *psb = A.bs + first * A.bs_ld;
-    const uint32_t off_sa = min(m0 + 4 * lane, (A.m + 3) / 4 * 4 - 4);
-    const uint32_t off_sb = min(n0 + 4 * lane, (A.n + 3) / 4 * 4 - 4);
-    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(s_mem));
-
-    const auto fetch = [&](int buffer) {
-        const uint32_t to = lds + buffer * kBuffer;
-#pragma unroll
-        for (int i = 0; i < kLoadsA; ++i) load_lds16(to + 1024 * (wave * kLoadsA + i), off_a[i], pa);
-#pragma unroll
-        for (int i = 0; i < kLoadsB; ++i) load_lds16(to + kA + 1024 * (wave * kLoadsB + i), off_b[i], pb);
-        if (wave == 0) load_lds4(to + kA + kB, off_sa, psa);
-        if (BROW && wave == 1) load_lds4(to + kA + kB + 256, off_sb, psb);
-        pa += kStep;
-        pb += kStep;
-        psa += A.as_ld;
-        psb += A.bs_ld;
-    };
-
-    f32x4 acc[4 * GA][4 * GB];
-#pragma unroll
-    for (int i = 0; i < 4 * GA; ++i)
-#pragma unroll
-        for (int j = 0; j < 4 * GB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    const int r = lane % 16, quarter = lane / 16;
-    // a lane takes chunks quarter and quarter + 4 of its row
-    const uint32_t low = r * kStep + 16 * (quarter ^ (r / 2)), high = r * kStep + 16 * ((quarter + 4) ^ (r / 2));
-    // TILE: lane l holds the scale of the wave's columns at step 64 j + l
-    const int block = min(n0 + wn * (BN / WN), A.n - 1) / DOPT_FP8_BLOCK;
-    int tile_scales = 0;
-
-    if (steps > 0) fetch(0);
-    settle();
-    for (int k = 0; k < steps; ++k) {
-        if (!BROW && k % 64 == 0) {
-            tile_scales = A.bs[static_cast<int64_t>(first + min(k + lane, steps - 1)) * A.bs_ld + block];
-            asm volatile("" : "+v"(tile_scales));  // waited for here, before the step's loads are under way
-        }
-        if (k + 1 < steps) fetch((k + 1) & 1);
-        const uint8_t *mem = s_mem + (k & 1) * kBuffer;
-        const uint8_t *ma = mem + wm * (BM / WM) * kStep, *mb = mem + kA + wn * (BN / WN) * kStep;
-        const uint8_t *ms = mem + kA + kB;
-        int sa[GA], sb[GB];
-#pragma unroll
-        for (int g = 0; g < GA; ++g) sa[g] = *reinterpret_cast<const int *>(ms + wm * (BM / WM) + 64 * g + 4 * r);
-#pragma unroll
-        for (int g = 0; g < GB; ++g) {
-            if (BROW) sb[g] = *reinterpret_cast<const int *>(ms + 256 + wn * (BN / WN) + 64 * g + 4 * r);
-            else sb[g] = __builtin_amdgcn_readlane(tile_scales, k % 64) * 0x01010101;
-        }
-        if constexpr (EXACT) {
-            // half a step at a time, so that the widened codes fit the registers
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t at = half ? high : low;
-                bf16x8 b[4 * GB][2];
-                each4([&](auto J) {
-                    constexpr int j = decltype(J)::value;
-#pragma unroll
-                    for (int h = 0; h < GB; ++h) {
-                        const i32x4 w = *reinterpret_cast<const i32x4 *>(mb + 16 * (4 * h + j) * kStep + at);
-                        const float scale = scale_of<j>(sb[h]);
-                        b[4 * h + j][0] = widen8(w[0], w[1], scale);
-                        b[4 * h + j][1] = widen8(w[2], w[3], scale);
-                    }
-                });
-#pragma unroll
-                for (int g = 0; g < GA; ++g)
-                    each4([&](auto I) {
-                        constexpr int i = decltype(I)::value;
-                        const i32x4 w = *reinterpret_cast<const i32x4 *>(ma + 16 * (4 * g + i) * kStep + at);
-                        const float scale = scale_of<i>(sa[g]);
-                        const bf16x8 a0 = widen8(w[0], w[1], scale), a1 = widen8(w[2], w[3], scale);
-#pragma unroll
-                        for (int j = 0; j < 4 * GB; ++j) acc[4 * g + i][j] = mfma(a0, b[j][0], acc[4 * g + i][j]);
-#pragma unroll
-                        for (int j = 0; j < 4 * GB; ++j) acc[4 * g + i][j] = mfma(a1, b[j][1], acc[4 * g + i][j]);
-                    });
-            }
-        } else {
-            i32x8 b[4 * GB];
-#pragma unroll
-            for (int j = 0; j < 4 * GB; ++j)
-                b[j] = join(*reinterpret_cast<const i32x4 *>(mb + 16 * j * kStep + low), *reinterpret_cast<const i32x4 *>(mb + 16 * j * kStep + high));
-#pragma unroll
-            for (int g = 0; g < GA; ++g)
-                each4([&](auto I) {
-                    constexpr int i = decltype(I)::value;
-                    const uint8_t *p = ma + 16 * (4 * g + i) * kStep;
-                    const i32x8 a = join(*reinterpret_cast<const i32x4 *>(p + low), *reinterpret_cast<const i32x4 *>(p + high));
-#pragma unroll
-                    for (int h = 0; h < GB; ++h)
-                        each4([&](auto J) {
-                            constexpr int j = decltype(J)::value;
-                            acc[4 * g + i][4 * h + j] = mfma<i, j>(a, b[4 * h + j], acc[4 * g + i][4 * h + j], sa[g], sb[h]);
-                        });
-                });
-        }
-        settle();
-    }
-
-    const int row0 = m0 + wm * (BM / WM), col0 = n0 + wn * (BN / WN);
-    if (A.splits == 1) {
-        store_tile<EXACT>(A, row0, col0, acc);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * GA; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-#pragma unroll
-            for (int h = 0; h < GB; ++h)
-                put4_part(A, split, row0 + i / 4 * 64 + 4 * (4 * quarter + v) + i % 4, col0 + 64 * h + 4 * r,
-                          f32x4{acc[i][4 * h][v], acc[i][4 * h + 1][v], acc[i][4 * h + 2][v], acc[i][4 * h + 3][v]});
-}
-
-// ---- large tiles --------------------------------------------------------------------
-
-constexpr int kBig = 256;                            // rows and columns of a tile
-constexpr int kBigOperand = kBig * kStep;            // bytes of an operand's rows in a step
-constexpr int kBigBuffer = 2 * kBigOperand + 512;    // both, and 256 bytes of scales for each
-
-// A wave's share of a step's loads: 32 / WAVES of 1 KB for each operand, numbered from 0,
-// the scales with the last.  Then it goes on to the next step, or after the last
+// A wave's share of a step's loads: SIDE / 8 / WAVES of 1 KB for each operand, numbered from
+// 0, the scales with the last.  Then it goes on to the next step, or after the last
 // step to that one again: the loops below have no branches, since the compiler
 // would gather all products behind the last of them.  Even waves bring the
 // same scales of a, odd ones of b (TILE: of a again).
-template <int WAVES, bool BROW>
+template <int SIDE, int WAVES, bool BROW>
 struct Loads {
-    static constexpr int kEach = 32 / WAVES, kAll = 2 * kEach;
-    uint32_t off_a[kEach], off_b[kEach], off_s, lds, to_s, to;
+    static constexpr int kEach = SIDE / 8 / WAVES, kAll = 2 * kEach;
+    uint32_t off_a[kEach], off_b[kEach], off_s, to_s, to;
     const uint8_t *pa, *pb, *ps;
     int64_t s_ld;
     int left;
 
-    __device__ __forceinline__ Loads(const GemmArgs &A, const uint8_t *mem, int m0, int n0, int lane, int wave) {
-        pa = A.a + static_cast<int64_t>(m0) * A.a_ld;
-        pb = A.b + static_cast<int64_t>(n0) * A.b_ld;
+    __device__ __forceinline__ Loads(const GemmArgs &A, const uint8_t *mem, int m0, int n0, int first, int steps, int lane, int wave) {
+        pa = A.a + static_cast<int64_t>(m0) * A.a_ld + static_cast<int64_t>(first) * kStep;
+        pb = A.b + static_cast<int64_t>(n0) * A.b_ld + static_cast<int64_t>(first) * kStep;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             off_a[i] = slot_offset(kEach * wave + i, lane, A.m - m0, A.a_ld);
             off_b[i] = slot_offset(kEach * wave + i, lane, A.n - n0, A.b_ld);
         }
         const bool of_b = BROW && wave % 2;
-        ps = of_b ? A.bs : A.as;
         s_ld = of_b ? A.bs_ld : A.as_ld;
+        ps = (of_b ? A.bs : A.as) + first * s_ld;
         off_s = of_b ? min(n0 + 4 * lane, (A.n + 3) / 4 * 4 - 4) : min(m0 + 4 * lane, (A.m + 3) / 4 * 4 - 4);
-        lds = __builtin_amdgcn_readfirstlane(lds_address(mem));
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(mem));
         to = lds + 1024 * kEach * wave;
-        to_s = lds + 2 * kBigOperand + (of_b ? 256 : 0);
-        left = A.steps;
+        to_s = lds + (of_b ? StepMem<SIDE>::kScalesB : StepMem<SIDE>::kScalesA);
+        left = steps;
     }
 
     __device__ __forceinline__ void start(int buffer, int i) {
         if (i < kEach) load_lds16(to + buffer + 1024 * i, off_a[i % kEach], pa);
-        else load_lds16(to + buffer + kBigOperand + 1024 * (i - kEach), off_b[i % kEach], pb);
+        else load_lds16(to + buffer + StepMem<SIDE>::kB + 1024 * (i - kEach), off_b[i % kEach], pb);
         if (i == kAll - 1) {
             load_lds4(to_s + buffer, off_s, ps);
             const bool more = --left > 0;
@@ -447,8 +298,150 @@ struct TileScales {
     }
 };
 
-// Keeps the instructions before and after apart, so that reads stay between the products.
-__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+// 128 x 128 of the output by 4 waves of 64 x 64.  A step's operands come to shared memory
+// STAGES steps ahead and to registers one ahead, so a step's one barrier stands
+// between two steps' products.  In shared memory a group of 64 rows lies in the order 0, 4,
+// 8, .. 60, 1, 5, ..: slot 16 i + r holds row 4 r + i.  The matrix instruction that takes slots 16 i
+// to 16 i + 15 thereby finds its rows' scales in byte i of the dword of row
+// 4 r, one dword for four instructions, and a lane's four results along
+// a row of the output are neighbours, which are stored at once.  Within a slot's
+// 128 bytes the 16-byte chunk c lies at c ^ (r / 2), which spreads the
+// 16 rows that a quarter of a wave reads over all banks (no conflict is counted).
+constexpr int kSmall = 128;
+
+template <int STAGES, bool BROW, bool EXACT>
+__global__ __launch_bounds__(256, STAGES > 2 ? 1 : 2) void k_gemm_tile(GemmArgs A) {
+    using Mem = StepMem<kSmall>;
+    __shared__ __align__(16) uint8_t s_mem[STAGES * Mem::kBytes];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = wave / 2, wn = wave % 2;
+    int m0, n0;
+    place_tile(A, kSmall, kSmall, m0, n0);
+    const int split = blockIdx.y, first = split * A.split_steps, steps = min(A.split_steps, A.steps - first);
+    Loads<kSmall, 4, BROW> loads(A, s_mem, m0, n0, first, steps, lane, wave);
+    TileScales ts{A.bs + first * A.bs_ld + n0 / DOPT_FP8_BLOCK, A.bs_ld, steps, 0, 0};
+
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    const int r = lane % 16, quarter = lane / 16;
+    const uint32_t low = r * kStep + 16 * (quarter ^ (r / 2)), high = r * kStep + 16 * ((quarter + 4) ^ (r / 2));
+    const uint8_t *ma = s_mem + wm * 64 * kStep, *mb = s_mem + Mem::kB + wn * 64 * kStep, *ms = s_mem + 4 * r;
+    struct Step {
+        i32x8 a[4], b[4];
+        int sa, sb;
+    } x, y;
+    const auto read = [&](i32x8 &v, const uint8_t *mem, int at) {  // the 16 rows from slot `at`
+        v = join(*reinterpret_cast<const i32x4 *>(mem + at * kStep + low), *reinterpret_cast<const i32x4 *>(mem + at * kStep + high));
+    };
+    const auto read_scales = [&](Step &v, int buffer, int k, int chunk_end) {
+        v.sa = *reinterpret_cast<const int *>(ms + buffer + Mem::kScalesA + wm * 64);
+        if (BROW) v.sb = *reinterpret_cast<const int *>(ms + buffer + Mem::kScalesB + wn * 64);
+        else v.sb = ts.of(k, chunk_end);
+    };
+    // multiplies v; in between next(i) for i in 0 to 3
+    const auto multiply = [&](const Step &v, const auto &next) {
+        if constexpr (!EXACT) {
+            each4([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                next(i);
+                each4([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    acc[i][j] = mfma<i, j>(v.a[i], v.b[j], acc[i][j], v.sa, v.sb);
+                });
+                in_order();
+            });
+        } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int h = 4 * half;
+                bf16x8 b[4][2];
+                each4([&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    const float scale = scale_of<j>(v.sb);
+                    b[j][0] = widen8(v.b[j][h], v.b[j][h + 1], scale);
+                    b[j][1] = widen8(v.b[j][h + 2], v.b[j][h + 3], scale);
+                });
+                each4([&](auto I) {
+                    constexpr int i = decltype(I)::value;
+                    if (i % 2 == 0) next(2 * half + i / 2);
+                    const float scale = scale_of<i>(v.sa);
+                    const bf16x8 a0 = widen8(v.a[i][h], v.a[i][h + 1], scale), a1 = widen8(v.a[i][h + 2], v.a[i][h + 3], scale);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = mfma(a0, b[j][0], acc[i][j]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = mfma(a1, b[j][1], acc[i][j]);
+                });
+            }
+        }
+    };
+    int at = 0;  // the buffer of the step that is multiplied
+    const auto after = [](int buffer) { return buffer == (STAGES - 1) * Mem::kBytes ? 0 : buffer + Mem::kBytes; };
+    // multiplies v, a step that all waves have read when the barrier is passed, starts loads into its buffer and
+    // reads the step after it, k, which has landed when at most STAGES - 2 steps' loads of the wave are under way
+    const auto turn = [&](Step &v, Step &w, int k, int chunk_end) {
+        if constexpr (STAGES == 2) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (Loads<kSmall, 4, BROW>::kAll + 1)) : "memory");
+        in_order();
+        const int nxt = after(at);
+        read_scales(w, nxt, k, chunk_end);
+        multiply(v, [&](int i) {
+            read(w.b[i], mb + nxt, 16 * i);
+            read(w.a[i], ma + nxt, 16 * i);
+            loads.start(at, 2 * i);
+            loads.start(at, 2 * i + 1);
+        });
+        in_order();
+        at = nxt;
+    };
+
+    if (steps > 0) {
+        if (!BROW) ts.now = ts.load(0, lane);
+#pragma unroll
+        for (int g = 0; g < STAGES; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) loads.start(g * Mem::kBytes, i);
+        // the first step has landed when at most STAGES - 1 are under way
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((STAGES - 1) * (Loads<kSmall, 4, BROW>::kAll + 1)) : "memory");
+        read_scales(x, 0, 0, 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            read(x.b[i], mb, 16 * i);
+            read(x.a[i], ma, 16 * i);
+        }
+    }
+    for (int chunk_at = 0; chunk_at < steps; chunk_at += 64) {
+        const int chunk_end = min(chunk_at + 64, steps);
+        if (!BROW && chunk_at > 0) ts.now = ts.next;
+        if (!BROW && chunk_end < steps) ts.next = ts.load(chunk_end, lane);
+        int k = chunk_at;
+        for (; k + 1 < chunk_end; k += 2) {
+            turn(x, y, k + 1, chunk_end);
+            turn(y, x, k + 2, chunk_end);
+        }
+        if (k < chunk_end) turn(x, y, k + 1, chunk_end);  // the last step of an odd number
+    }
+    settle();  // the loads past the last step land in this workgroup's shared memory, so it stays until they have
+
+    const int row0 = m0 + wm * 64, col0 = n0 + wn * 64;
+    if (A.splits == 1) {
+        store_tile<EXACT>(A, row0, col0, acc);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            put4_part(A, split, row0 + 4 * (4 * quarter + v) + i, col0 + 4 * r, f32x4{acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]});
+}
+
+// ---- large tiles --------------------------------------------------------------------
+
+constexpr int kBig = 256;  // rows and columns of a tile
+constexpr int kBigOperand = StepMem<kBig>::kB, kBigBuffer = StepMem<kBig>::kBytes;
 
 // 256 x 256 of the output by 4 waves, one to a SIMD with all of its registers, each
 // 128 x 128.  As k_gemm_tile, but a step has two phases with its one barrier
@@ -465,7 +458,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_big(GemmArgs A) {
     const int wm = wave / 2, wn = wave % 2;
     int m0, n0;
     place_tile(A, kBig, kBig, m0, n0);
-    Loads<4, BROW> loads(A, s_mem, m0, n0, lane, wave);
+    Loads<kBig, 4, BROW> loads(A, s_mem, m0, n0, 0, A.steps, lane, wave);
     TileScales ts{A.bs + min(n0 + wn * 128, A.n - 1) / DOPT_FP8_BLOCK, A.bs_ld, A.steps, 0, 0};
 
     f32x4 acc[8][8];
@@ -561,7 +554,7 @@ __global__ __launch_bounds__(512, 2) void k_gemm_wide(GemmArgs A) {
     const int wm = wave / 4, wn = wave % 4;
     int m0, n0;
     place_tile(A, kBig, kBig, m0, n0);
-    Loads<8, BROW> loads(A, s_mem, m0, n0, lane, wave);
+    Loads<kBig, 8, BROW> loads(A, s_mem, m0, n0, 0, A.steps, lane, wave);
     TileScales ts{A.bs + min(n0 + wn * 64, A.n - 1) / DOPT_FP8_BLOCK, A.bs_ld, A.steps, 0, 0};
 
     f32x4 acc[8][4];
@@ -664,61 +657,61 @@ __global__ __launch_bounds__(512, 2) void k_gemm_wide(GemmArgs A) {
 
 // ---- few rows ---------------------------------------------------------------------
 
-constexpr int kFewWaves = 8;
+// Up to 16 rows of a: b is read once, and what bounds the call is how fast.  A
+// workgroup takes 16 columns of the output, its waves share the steps along k, and
+// their sums are joined through shared memory.  A wave has the operands of
+// kFewDepth steps under way before it multiplies the first.
+constexpr int kFewDepth = 4;
 
-// Up to 16 * MT rows of a: b is read once, and what bounds the call is how
-// fast.  A workgroup takes 16 columns of the output, its waves share the
-// steps along k, and their sums are joined through shared memory.
-template <int MT, bool BROW, bool EXACT>
-__global__ __launch_bounds__(kFewWaves * 64) void k_gemm_few(GemmArgs A) {
-    __shared__ __align__(16) float s_sum[kFewWaves][MT][256];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+template <int WAVES, bool BROW, bool EXACT>
+__global__ __launch_bounds__(WAVES * 64) void k_gemm_few(GemmArgs A) {
+    __shared__ __align__(16) float s_sum[WAVES][256];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int r = lane % 16, quarter = lane / 16;
     const int n0 = blockIdx.x * 16, split = blockIdx.y;
     const int first = split * A.split_steps, end = min(first + A.split_steps, A.steps);
-    const int col = min(n0 + r, A.n - 1);
+    const int row = min(r, A.m - 1), col = min(n0 + r, A.n - 1), scale_col = BROW ? col : n0 / DOPT_FP8_BLOCK;
+    const uint8_t *pa = A.a + static_cast<int64_t>(row) * A.a_ld + 16 * quarter;
     const uint8_t *pb = A.b + static_cast<int64_t>(col) * A.b_ld + 16 * quarter;
-    const uint8_t *pa[MT];
-    int row[MT];
+    f32x4 acc = {0, 0, 0, 0};
+    for (int k0 = first + wave; k0 < end; k0 += kFewDepth * WAVES) {
+        i32x4 b[kFewDepth][2], a[kFewDepth][2];
+        int sb[kFewDepth], sa[kFewDepth];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        row[i] = min(16 * i + r, A.m - 1);
-        pa[i] = A.a + static_cast<int64_t>(row[i]) * A.a_ld + 16 * quarter;
-    }
-    f32x4 acc[MT];
+        for (int u = 0; u < kFewDepth; ++u) {
+            const int64_t k = min(k0 + u * WAVES, end - 1);  // steps past the last are read as the last, and not multiplied
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-    const int scale_col = BROW ? col : col / DOPT_FP8_BLOCK;
-#pragma unroll 4
-    for (int k = first + wave; k < end; k += kFewWaves) {
-        const int64_t at = static_cast<int64_t>(k) * kStep;
-        const i32x8 b = join(*reinterpret_cast<const i32x4 *>(pb + at), *reinterpret_cast<const i32x4 *>(pb + at + 64));
-        const int sb = A.bs[k * A.bs_ld + scale_col];
+            for (int h = 0; h < 2; ++h) {
+                b[u][h] = *reinterpret_cast<const i32x4 *>(pb + k * kStep + 64 * h);
+                a[u][h] = *reinterpret_cast<const i32x4 *>(pa + k * kStep + 64 * h);
+            }
+            sa[u] = A.as[k * A.as_ld + row];
+            sb[u] = A.bs[k * A.bs_ld + scale_col];
+        }
+        in_order();
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const i32x8 a = join(*reinterpret_cast<const i32x4 *>(pa[i] + at), *reinterpret_cast<const i32x4 *>(pa[i] + at + 64));
-            const int sa = A.as[k * A.as_ld + row[i]];
+        for (int u = 0; u < kFewDepth; ++u) {
+            if (k0 + u * WAVES >= end) break;
             if constexpr (EXACT) {
+                const float fa = scale_of<0>(sa[u]), fb = scale_of<0>(sb[u]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    acc[i] = mfma(widen8(a[2 * j], a[2 * j + 1], scale_of<0>(sa)), widen8(b[2 * j], b[2 * j + 1], scale_of<0>(sb)), acc[i]);
+                    acc = mfma(widen8(a[u][j / 2][2 * (j % 2)], a[u][j / 2][2 * (j % 2) + 1], fa),
+                               widen8(b[u][j / 2][2 * (j % 2)], b[u][j / 2][2 * (j % 2) + 1], fb), acc);
             } else {
-                acc[i] = mfma<0, 0>(a, b, acc[i], sa, sb);
+                acc = mfma<0, 0>(join(a[u][0], a[u][1]), join(b[u][0], b[u][1]), acc, sa[u], sb[u]);
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) s_sum[wave][i][(4 * quarter + v) * 16 + r] = acc[i][v];
+    for (int v = 0; v < 4; ++v) s_sum[wave][(4 * quarter + v) * 16 + r] = acc[v];
     __syncthreads();
-    if (threadIdx.x >= MT * 64) return;
-    const int i = threadIdx.x / 64, e = threadIdx.x % 64 * 4;
+    if (wave > 0) return;
     f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) x += *reinterpret_cast<const f32x4 *>(&s_sum[w][i][e]);
-    if (A.splits > 1) put4_part(A, split, 16 * i + e / 16, n0 + e % 16, x);
-    else put4(A, 16 * i + e / 16, n0 + e % 16, x);
+    for (int w = 0; w < WAVES; ++w) x += *reinterpret_cast<const f32x4 *>(&s_sum[w][4 * lane]);
+    if (A.splits > 1) put4_part(A, split, lane / 4, n0 + 4 * (lane % 4), x);
+    else put4(A, lane / 4, n0 + 4 * (lane % 4), x);
 }
 
 // ---- which kernel -------------------------------------------------------------------
@@ -726,29 +719,51 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_gemm_few(GemmArgs A) {
 struct Plan {
     int rows, cols;  // of a tile
     bool few;
+    int stages;  // of k_gemm_tile
+    int waves;   // of k_gemm_few
     int splits, split_steps;
 };
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int64_t kCus = 256;
+
 static Plan plan_of(int64_t m, int64_t n, int64_t k) {
     Plan p{};
-    const int64_t steps = ceil_div(k, kStep);
-    p.few = m <= 64;
-    if (p.few) {
-        p.rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
-        p.cols = 16;
-    } else {
-        p.rows = p.cols = ceil_div(m, 256) * ceil_div(n, 256) >= 192 ? 256 : 128;
-    }
-    const int64_t tiles = ceil_div(m, p.rows) * ceil_div(n, p.cols);
+    const int64_t steps = std::max<int64_t>(ceil_div(k, kStep), 1);
+    p.few = m <= 16;
+    p.stages = 2;
     int64_t splits = 1;
-    if (p.rows != 256) {
-        const int64_t want = p.few ? 256 : 512, least = p.few ? kFewWaves : 4;
-        splits = std::max<int64_t>(1, std::min(want / std::max<int64_t>(tiles, 1), steps / least));
+    if (p.few) {
+        // One batch of kFewDepth steps to a wave, up to 8 waves: 4096 columns, 8 steps: 3.8 us with 2
+        // waves, 4.5 with 4, 6.1 with 8; 6000 columns, 16 steps: 6.6, 6.3, 8.9; 11008 columns, 32 steps: 12.4, 13.0, 12.2;
+        // 8192 columns, 32 steps: 10.9, 10.6, 9.8.  More steps than that are shared by several workgroups where
+        // the columns are few: 768 columns, 128 steps: 13.1 us, split in 4 8.7, in 8 12.3; 2048 columns, 64 steps: 9.2, in 2 9.3.
+        p.rows = p.cols = 16;
+        p.waves = steps <= 12 ? 2 : steps <= 24 ? 4 : 8;
+        if (ceil_div(n, p.cols) <= 64) splits = steps / (8 * kFewDepth);
+    } else {
+        const int64_t small = ceil_div(m, kSmall) * ceil_div(n, kSmall), big = ceil_div(m, kBig) * ceil_div(n, kBig);
+        if (small <= kCus) {
+            // A tile or less to a CU: what counts is how soon a step's loads are back, so three steps are under way,
+            // and with 8 steps or more to each the steps are shared by several workgroups.
+            // 128 x 4096 x 4096, bf16 out: 24.8 us with 2 stages, 16.8 with 3 or 4; split in 2, 4, 8: 16.0,
+            // 16.2, 19.3.  1024 x 4096 x 4096: 26.7, 19.4.  768 x 768 x 8192, fp32 out: 52.7 us, split in 4 23.6, in 8 29.5.
+            p.rows = p.cols = kSmall;
+            p.stages = 3;
+            splits = std::min(kCus / small, steps / 8);
+        } else {
+            // A round of big tiles takes about 7 us and 1.25 for each step, one of twice as many small ones
+            // 2.5 and 0.92 (measured at 256 to 1024 small tiles and 8 to 32 steps; fp32 outputs in the same proportion).
+            // Small and big, us: 2048 x 4096 x 4096 34, 46; 4096 x 4096 x 4096 64, 53; 3073 x 4096 x 4096 56, 47;
+            // 8192 x 2304 x 768 24, 29; 4096 x 14336 x 128 33, 38; fp32 out 67, 78; 123, 96; 108, 85; 36, 44; 53, 59.
+            const int64_t as_big = ceil_div(big, kCus) * (28 + 5 * steps), as_small = ceil_div(small, 2 * kCus) * (100 + 37 * steps);
+            p.rows = p.cols = as_big * 10 <= as_small ? kBig : kSmall;
+        }
     }
-    p.split_steps = static_cast<int>(ceil_div(std::max<int64_t>(steps, 1), splits));
-    p.splits = static_cast<int>(ceil_div(std::max<int64_t>(steps, 1), p.split_steps));
+    splits = std::max<int64_t>(splits, 1);
+    p.split_steps = static_cast<int>(ceil_div(steps, splits));
+    p.splits = static_cast<int>(ceil_div(steps, p.split_steps));
     return p;
 }
 
@@ -758,14 +773,15 @@ template <bool BROW, bool EXACT>
 static void launch_gemm(const GemmArgs &A, const Plan &p, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(A.tiles_m * A.tiles_n), static_cast<unsigned>(A.splits));
     if (p.few) {
-        if (p.rows == 16) k_gemm_few<1, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
-        else if (p.rows == 32) k_gemm_few<2, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
-        else k_gemm_few<4, BROW, EXACT><<<grid, kFewWaves * 64, 0, stream>>>(A);
-    } else if (p.rows == 256) {
+        if (p.waves == 2) k_gemm_few<2, BROW, EXACT><<<grid, 128, 0, stream>>>(A);
+        else if (p.waves == 4) k_gemm_few<4, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
+        else k_gemm_few<8, BROW, EXACT><<<grid, 512, 0, stream>>>(A);
+    } else if (p.rows == kBig) {
         if constexpr (EXACT) k_gemm_wide<BROW><<<grid, 512, 0, stream>>>(A);
         else k_gemm_big<BROW><<<grid, 256, 0, stream>>>(A);
     } else {
-        k_gemm_tile<128, 128, 2, 2, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
+        if (p.stages == 2) k_gemm_tile<2, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
+        else k_gemm_tile<3, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
     }
 }
 
