@@ -88,14 +88,25 @@ __device__ __forceinline__ uint32_t from_float(float x) {
     if constexpr (T == DOPT_F16) return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
 }
 
+// As Bytes16 for accesses that pass the caches by: a vector type of that alignment.
+using u32x4_any = __attribute__((ext_vector_type(4), aligned(2))) uint32_t;
+
+// A matrix of more bytes than the 8 L2 caches hold (4 MB each) is read around them where it is
+// read once: its lines are gone before anyone could ask again, and what the call
+// writes for the next one stays longer.
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+
 // Elements [0, n) of the 8 at p, n <= 8, the others zero.
-template <int T>
+template <int T, bool STREAM = false>
 __device__ __forceinline__ Raw8<T> load8(const void *base, int64_t e, int n) {
     Raw8<T> r;
     if (n >= 8) {
-        const Bytes16 *p = reinterpret_cast<const Bytes16 *>(static_cast<const char *>(base) + e * (T == DOPT_F32 ? 4 : 2));
+        const char *p = static_cast<const char *>(base) + e * (T == DOPT_F32 ? 4 : 2);
 #pragma unroll
-        for (int i = 0; i < kWords8<T>; ++i) r.w[i] = p[i].v;
+        for (int i = 0; i < kWords8<T>; ++i) {
+            if constexpr (STREAM) r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p) + i);
+            else r.w[i] = reinterpret_cast<const Bytes16 *>(p)[i].v;
+        }
         return r;
     }
 #pragma unroll
@@ -139,12 +150,15 @@ __device__ __forceinline__ Raw8<T> pack8(const float (&x)[8]) {
     return r;
 }
 
-template <int T>
+template <int T, bool STREAM = false>
 __device__ __forceinline__ void store8(void *base, int64_t e, int n, const Raw8<T> &r) {
     if (n >= 8) {
-        Bytes16 *p = reinterpret_cast<Bytes16 *>(static_cast<char *>(base) + e * (T == DOPT_F32 ? 4 : 2));
+        char *p = static_cast<char *>(base) + e * (T == DOPT_F32 ? 4 : 2);
 #pragma unroll
-        for (int i = 0; i < kWords8<T>; ++i) p[i].v = r.w[i];
+        for (int i = 0; i < kWords8<T>; ++i) {
+            if constexpr (STREAM) __builtin_nontemporal_store(r.w[i], reinterpret_cast<u32x4_any *>(p) + i);
+            else reinterpret_cast<Bytes16 *>(p)[i].v = r.w[i];
+        }
         return;
     }
 #pragma unroll
@@ -196,6 +210,12 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as
 template <bool HIGH>
 __device__ __forceinline__ uint32_t codes2(float a, float b, float inv, uint32_t old) {
     return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, static_cast<int>(old), HIGH));
+}
+
+template <bool STREAM>
+__device__ __forceinline__ void store_codes8(uint8_t *p, u32x2 q) {
+    if constexpr (STREAM) __builtin_nontemporal_store(q, reinterpret_cast<u32x2 *>(p));
+    else *reinterpret_cast<u32x2 *>(p) = q;
 }
 
 __device__ __forceinline__ u32x2 codes8(const float (&x)[8], float inv) {

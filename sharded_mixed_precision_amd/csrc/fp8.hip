@@ -112,27 +112,37 @@ constexpr int kCastThreads = 256;
 // its codes leave as 128 consecutive bytes.  Columns are joined over the
 // threads through shared memory, and the transposed codes pass through it, so
 // that they too leave as 128 consecutive bytes of a row.
-template <int T, bool TILE>
-__global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
-    __shared__ uint32_t s_top[4][DOPT_FP8_BLOCK];
-    __shared__ __align__(16) uint8_t s_codes[DOPT_FP8_BLOCK * DOPT_FP8_BLOCK];
+struct CastMem {
+    uint32_t top[4][DOPT_FP8_BLOCK];
+    alignas(16) uint8_t codes[DOPT_FP8_BLOCK * DOPT_FP8_BLOCK];
+};
+
+// STREAM: x is read around the caches, and weights' codes (TILE) are written
+// around them: they are asked for when the other layers' weights have been cast, while a grad's or an
+// activation's (ROW) are the next product's operands.  8192 x 4096 bf16, both ways, ROW: 30.8 us
+// with ordinary reads, 28.6 around the caches, 24.8 with the codes too, but then the product of
+// 4096 x 14336 behind it takes 10 us longer; 1024 x 4096: 8.2 and 8.5.  14336 x 4096, TILE: 47.8 and 43.6.
+template <int T, bool TILE, bool WHOLE, bool STREAM>
+__device__ __forceinline__ void cast_tile(const CastArgs &A, CastMem &mem, int row0, int col0) {
+    auto &s_top = mem.top;
+    auto &s_codes = mem.codes;
     const int t = threadIdx.x, cx = t % 16, ry = t / 16;
-    const int row0 = blockIdx.x / A.col_tiles * DOPT_FP8_BLOCK, col0 = blockIdx.x % A.col_tiles * DOPT_FP8_BLOCK;
     const int r0 = row0 + 8 * ry, c0 = col0 + 8 * cx;
-    const int n_cols = A.cols - c0 < 0 ? 0 : A.cols - c0 > 8 ? 8 : A.cols - c0;
+    const int n_cols = WHOLE || A.cols - c0 > 8 ? 8 : A.cols - c0 < 0 ? 0 : A.cols - c0;
+    const auto inside = [&](int i) { return WHOLE || r0 + i < A.rows; };
     float x[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        unpack8<T>(load8<T>(A.x, static_cast<int64_t>(r0 + i) * A.ld + c0, r0 + i < A.rows ? n_cols : 0), x[i]);
+        unpack8<T>(load8<T, STREAM>(A.x, static_cast<int64_t>(r0 + i) * A.ld + c0, WHOLE ? 8 : inside(i) ? n_cols : 0), x[i]);
     if (A.row) {
         float c[8];
         load_vector8(A.col, A.col_dtype, c0, n_cols, c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool inside = r0 + i < A.rows;  // what pads the tile stays 0 beside factors that are not finite
-            const float r = inside ? A.row[r0 + i] : 0.0f;
+            const float r = inside(i) ? A.row[r0 + i] : 0.0f;
+            // what pads the tile stays 0 beside factors that are not finite
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] = inside && j < n_cols ? product3(x[i][j], r, c[j]) : 0.0f;
+            for (int j = 0; j < 8; ++j) x[i][j] = inside(i) && j < n_cols ? product3(x[i][j], r, c[j]) : 0.0f;
         }
     }
 
@@ -149,9 +159,9 @@ __global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
         top = s_top[0][cx];
         byte = scale_byte(max16(top));
         if (t == 0) {
-            if (A.codes) A.scales[static_cast<int64_t>(col0 / DOPT_FP8_BLOCK) * A.scale_ld + row0 / DOPT_FP8_BLOCK] = static_cast<uint8_t>(byte);
-            if (A.t_codes)
-                A.t_scales[static_cast<int64_t>(row0 / DOPT_FP8_BLOCK) * A.t_scale_ld + col0 / DOPT_FP8_BLOCK] = static_cast<uint8_t>(byte);
+            const int64_t i = row0 / DOPT_FP8_BLOCK, j = col0 / DOPT_FP8_BLOCK;
+            if (A.codes) A.scales[j * A.scale_ld + i] = static_cast<uint8_t>(byte);
+            if (A.t_codes) A.t_scales[i * A.t_scale_ld + j] = static_cast<uint8_t>(byte);
         }
     }
 
@@ -168,12 +178,15 @@ __global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
                 bytes |= static_cast<uint64_t>(byte) << (8 * i);
             }
             q[i] = codes8(x[i], inverse_scale(byte));
-            if (A.codes && r0 + i < A.rows)
-                *reinterpret_cast<u32x2 *>(A.codes + static_cast<int64_t>(r0 + i) * A.codes_ld + c0) = q[i];
         }
-        if constexpr (!TILE)
-            if (cx < 8 && r0 + cx < A.rows)
-                A.scales[static_cast<int64_t>(col0 / DOPT_FP8_BLOCK) * A.scale_ld + r0 + cx] = static_cast<uint8_t>(bytes >> (8 * cx));
+        if (A.codes) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (inside(i)) store_codes8<STREAM && TILE>(A.codes + static_cast<int64_t>(r0 + i) * A.codes_ld + c0, q[i]);
+            if constexpr (!TILE)
+                if (cx < 8 && (WHOLE || r0 + cx < A.rows))
+                    A.scales[static_cast<int64_t>(col0 / DOPT_FP8_BLOCK) * A.scale_ld + r0 + cx] = static_cast<uint8_t>(bytes >> (8 * cx));
+        }
     }
     if (!A.t_codes) return;
 
@@ -189,6 +202,13 @@ __global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
             if (t % 64 < 16) s_top[t / 64][8 * cx + j] = top;
         }
         __syncthreads();
+        if (t < DOPT_FP8_BLOCK) {
+            byte = scale_byte(max(max(s_top[0][t], s_top[1][t]), max(s_top[2][t], s_top[3][t])));
+            if (WHOLE || col0 + t < A.cols)
+                A.t_scales[static_cast<int64_t>(row0 / DOPT_FP8_BLOCK) * A.t_scale_ld + col0 + t] = static_cast<uint8_t>(byte);
+            s_top[0][t] = byte;
+        }
+        __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -201,14 +221,10 @@ __global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
                 for (int i = 0; i < 4; ++i) w[h] |= ((q[4 * h + i][j / 4] >> (8 * (j % 4))) & 0xffu) << (8 * i);
             }
         } else {
-            const int c = 8 * cx + j;
-            byte = scale_byte(max(max(s_top[0][c], s_top[1][c]), max(s_top[2][c], s_top[3][c])));
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = x[i][j];
-            w = codes8(y, inverse_scale(byte));
-            if (ry == 0 && col0 + c < A.cols)
-                A.t_scales[static_cast<int64_t>(row0 / DOPT_FP8_BLOCK) * A.t_scale_ld + col0 + c] = static_cast<uint8_t>(byte);
+            w = codes8(y, inverse_scale(s_top[0][8 * cx + j]));
         }
         // 16 chunks of 8 bytes to a row; the XOR spreads the 16 lanes of one ry over all banks
         *reinterpret_cast<u32x2 *>(s_codes + (8 * cx + j) * DOPT_FP8_BLOCK + 8 * (ry ^ cx)) = w;
@@ -218,15 +234,27 @@ __global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
     for (int i = 0; i < 8; ++i) {
         const int c = ry + 16 * i;
         const u32x2 w = *reinterpret_cast<const u32x2 *>(s_codes + c * DOPT_FP8_BLOCK + 8 * (cx ^ (c / 8)));
-        if (col0 + c < A.cols)
-            *reinterpret_cast<u32x2 *>(A.t_codes + static_cast<int64_t>(col0 + c) * A.t_codes_ld + row0 + 8 * cx) = w;
+        if (WHOLE || col0 + c < A.cols)
+            store_codes8<STREAM && TILE>(A.t_codes + static_cast<int64_t>(col0 + c) * A.t_codes_ld + row0 + 8 * cx, w);
     }
+}
+
+// Tiles that are whole, which most are, take code without bounds.
+template <int T, bool TILE, bool STREAM>
+__global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
+    __shared__ CastMem mem;
+    const int row0 = blockIdx.x / A.col_tiles * DOPT_FP8_BLOCK, col0 = blockIdx.x % A.col_tiles * DOPT_FP8_BLOCK;
+    if (row0 + DOPT_FP8_BLOCK <= A.rows && col0 + DOPT_FP8_BLOCK <= A.cols) cast_tile<T, TILE, true, STREAM>(A, mem, row0, col0);
+    else cast_tile<T, TILE, false, STREAM>(A, mem, row0, col0);
 }
 
 template <int T>
 static void launch_cast(const CastArgs &A, bool tile, unsigned grid, hipStream_t stream) {
-    if (tile) k_cast<T, true><<<grid, kCastThreads, 0, stream>>>(A);
-    else k_cast<T, false><<<grid, kCastThreads, 0, stream>>>(A);
+    const bool around = int64_t(A.rows) * A.cols * (T == DOPT_F32 ? 4 : 2) > kStreamBytes;
+    if (tile && around) k_cast<T, true, true><<<grid, kCastThreads, 0, stream>>>(A);
+    else if (tile) k_cast<T, true, false><<<grid, kCastThreads, 0, stream>>>(A);
+    else if (around) k_cast<T, false, true><<<grid, kCastThreads, 0, stream>>>(A);
+    else k_cast<T, false, false><<<grid, kCastThreads, 0, stream>>>(A);
 }
 
 }  // namespace dopt
