@@ -101,7 +101,10 @@ int dopt_fp8_cast(const dopt_dense *x, const float *row_factor, const void *col_
 /*
  * dopt_fp8_gemm -- out[m][n] = sum over k of a[m][k] * b[n][k], plus
  * out[m][n] if `accumulate`.  a (kind ROW) is M x K, b (either kind) N x K, out
- * M x N; sums in fp32, one rounding to out's type.  The workspace holds
+ * M x N; sums in fp32, one rounding to out's type.  For 16-bit outputs the matrix
+ * cores add 8 neighbouring products along k with 14 bits below the largest of
+ * them, which a result shows as 3 to 5e-5 of the outputs' root mean square; for fp32
+ * outputs, such as weight grads, every product is added in fp32.  Scales may be bytes 1 to 254.  The workspace holds
  * dopt_fp8_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned; where that is
  * 0 it may be NULL.
  */

@@ -129,6 +129,17 @@ def test_cast_strides(dtype):
 
 
 @pytest.mark.parametrize("kind", ["row", "tile"])
+@pytest.mark.parametrize("rows,cols,dtype", [(4200, 4100, "bf16"), (2100, 4099, "f32"), (130, 131073, "f16")])
+def test_cast_large(rows, cols, dtype, kind):
+    """More bytes than the caches hold, which are read around them."""
+    x = F.tokens(gen(8), rows, cols, 0.3, "cuda").to(F.TYPES[dtype])
+    both = poisoned(rows, cols, kind), poisoned(cols, rows, kind)
+    D.dopt_fp8_cast(x, *both, stream=stream())
+    same_codes(both[0], x, kind)
+    same_codes(both[1], x.t(), kind)
+
+
+@pytest.mark.parametrize("kind", ["row", "tile"])
 @pytest.mark.parametrize("wtype", ["f32", "bf16", "f16"])
 def test_cast_with_factors(wtype, kind):
     x = F.tokens(gen(5), 200, 333, 1.0, "cuda").to(torch.bfloat16)
@@ -162,16 +173,20 @@ def whole_numbers(g, rows, cols, kind, spread=2):
 
 GEMMS = [(1, 1, 1), (1, 16, 128), (1, 77, 300), (5, 130, 1000), (16, 129, 256), (17, 300, 129), (33, 64, 4000), (64, 257, 640),
          (65, 65, 65), (128, 128, 128), (129, 130, 257), (200, 1000, 384), (100, 100, 4096), (255, 256, 500), (300, 333, 1100),
-         (777, 1029, 640), (2049, 4097, 256), (4100, 3000, 130)]
+         (777, 1029, 640), (2049, 4097, 256), (4100, 3000, 130),
+         # each kernel with more than 64 steps of 128, and where the steps are shared by workgroups
+         (7, 100, 2000), (9, 1100, 8300), (2, 300, 8300), (100, 200, 2100), (1300, 2500, 8400), (2000, 4000, 8300),
+         (4100, 3000, 1100), (2100, 4200, 8300)]
 
 
 @pytest.mark.parametrize("kind", ["tile", "row"])
 @pytest.mark.parametrize("m,n,k", GEMMS)
 def test_gemm_exact(m, n, k, kind):
-    """Whole numbers: products and sums are exact (below 4096 * 16 * 16 in steps of 1 / 16), so every element is equal."""
+    """Whole numbers: sums of |products| are below 2^20 in steps of 1 / 16, so sums are exact and every element is equal."""
     g = gen(m * 31 + n * 7 + k)
     a, b = whole_numbers(g, m, k, "row"), whole_numbers(g, n, k, kind)
     want = F.values(a) @ F.values(b).t()
+    assert float((F.values(a).abs()[:64] @ F.values(b).abs().t()).max()) < 2.0 ** 20
     ws = torch.empty(D.dopt_fp8_gemm_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
     out = torch.full((m + 1, n + 3), math.nan, device="cuda")
     D.dopt_fp8_gemm(a, b, out[:m, :n], False, ws, stream())
@@ -291,11 +306,13 @@ def mean_slack(cols):
 
 NORMS = [(1, 1), (1, 4096), (3, 127), (5, 512), (7, 513), (9, 768), (4, 1024), (6, 1025), (3, 2048), (17, 2049), (5, 4097),
          (3, 8192), (2, 8200), (2, 16384), (3, 16390), (2, 40000)]
+# more bytes than the caches hold, which are read around them
+LARGE_NORMS = [(36000, 500), (18000, 1000), (9000, 2047), (4200, 4100), (2100, 8192), (1100, 16300), (450, 40000)]
 
 
 @pytest.mark.parametrize("dtype,wtype", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f16", "f16")])
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("rows,cols", NORMS)
+@pytest.mark.parametrize("rows,cols", NORMS + LARGE_NORMS)
 def test_norm(rows, cols, residual, dtype, wtype):
     g, t, eps = gen(rows + cols), F.TYPES[dtype], 1e-5
     x = F.tokens(g, rows, cols, 0.5, "cuda").to(t)
@@ -334,6 +351,42 @@ def test_norm(rows, cols, residual, dtype, wtype):
     y2 = torch.empty_like(y)
     D.dopt_rmsnorm(x, w, eps, residual=res, y=y2, stream=stream())
     assert torch.equal(y, y2)
+
+
+def test_offsets_past_32_bits():
+    """Operands of more than 2^31 bytes and 2^31 elements: rows at both ends and in the middle."""
+    rows, cols = 530000, 4200
+    x = torch.randn(rows, cols, generator=gen(1), device="cuda", dtype=torch.bfloat16)
+    q = fp8_alloc(rows, cols)
+    D.dopt_fp8_cast(x, q, stream=stream())
+    at = torch.tensor([0, 1, 255999, 256000, 511111, rows - 2, rows - 1], device="cuda")
+    c, e = F.encode(x[at], "row")
+    assert torch.equal(q.codes[:, :cols][at].double(), c)
+    assert torch.equal(q.scales.view(torch.uint8)[:, at].long().t() - 127, e)
+    w = whole_numbers(gen(2), 16, cols, "row")
+    want = (c * torch.exp2(e.double()).repeat_interleave(128, 1)[:, :cols]) @ F.values(w).t()
+    bound = cols * 2 * U * ((c * torch.exp2(e.double()).repeat_interleave(128, 1)[:, :cols]).abs() @ F.values(w).abs().t())
+    out = torch.empty(16, rows, device="cuda")  # the long operand as b, then as a
+    D.dopt_fp8_gemm(w, q, out, False, None, stream())
+    assert bool(((out[:, at].t().double() - want).abs() <= bound + U * want.abs()).all())
+    out = torch.empty(rows, 16, device="cuda")
+    ws = torch.empty(max(1, D.dopt_fp8_gemm_workspace_bytes(rows, 16, cols)), dtype=torch.uint8, device="cuda")
+    D.dopt_fp8_gemm(q, w, out, False, ws, stream())
+    assert bool(((out[at].double() - want).abs() <= bound + U * want.abs()).all())
+    del out, q
+    h, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda")
+    one = torch.ones(cols, device="cuda")
+    D.dopt_rmsnorm(x, one, 1e-5, residual=x, h=h, y=y, rstd=rstd, stream=stream())
+    want_h, want_r, want_y = F.rms_norm(x[at], x[at], one, 1e-5, torch.bfloat16)
+    assert torch.equal(h[at].double(), want_h)
+    assert bool(((rstd[at].double() - want_r).abs() <= norm_slack(cols) * want_r).all())
+    assert bool(((y[at].double() - want_y).abs() <= (2.0 ** -8 + norm_slack(cols) + 2 * U) * want_y.abs()).all())
+    dx, dw = y, torch.empty(cols, device="cuda")
+    ws = torch.empty(D.dopt_rmsnorm_grad_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    D.dopt_rmsnorm_grad(x, h, one, rstd, dx, dw, workspace=ws, stream=stream())
+    want_dx, _ = F.rms_norm_grad(x[at], h[at], None, one, rstd[at])
+    size = (rstd[at].double()[:, None] * x[at].double().abs() * 2).amax(1, keepdim=True)
+    assert bool(((dx[at].double() - want_dx).abs() <= 2.0 ** -8 * want_dx.abs() + (mean_slack(cols) + 8 * U + 2.0 ** -16) * size).all())
 
 
 def test_norm_special_rows():
