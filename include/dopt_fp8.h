@@ -24,7 +24,7 @@
  *     code  = e4m3(x * 2^-e), nearest, ties to even; NaN for NaN and infinities
  * (OCP e4m3: 1 sign, 4 exponent, 3 mantissa bits; largest 448).  The scaling
  * is exact, so an element is within 2^-4 of its value, or within 2^-10 * scale
- * if that is more.  A power of two costs no precision over A / 448 except to
+ * if that is more (in fp32 from 2^128 * (1 - 2^-5) on it rounds to 2^128, which is infinite).  A power of two costs no precision over A / 448 except to
  * elements 2^-14 of the largest and smaller, of which it may cut one bit, and
  * the matrix cores apply it without an instruction of its own.
  *
@@ -58,8 +58,9 @@ enum { DOPT_FP8_ROW = 0, DOPT_FP8_TILE = 1 };
 
 /* Elements along a row, and for TILE rows, of a block. */
 #define DOPT_FP8_BLOCK 128
-/* Columns of a matrix of either kind are at most this many; rows at most 2^31 - 1. */
+/* A matrix in the 8-bit format has at most this many columns, and one of either kind this many rows. */
 #define DOPT_FP8_MAX_COLS (1 << 22)
+#define DOPT_FP8_MAX_ROWS (1 << 30)
 
 /* A matrix in the 8-bit format (device addresses). */
 typedef struct dopt_fp8_matrix {
@@ -104,7 +105,8 @@ int dopt_fp8_cast(const dopt_dense *x, const float *row_factor, const void *col_
  * M x N; sums in fp32, one rounding to out's type.  For 16-bit outputs the matrix
  * cores add 8 neighbouring products along k with 14 bits below the largest of
  * them, which a result shows as 3 to 5e-5 of the outputs' root mean square; for fp32
- * outputs, such as weight grads, every product is added in fp32.  Scales may be bytes 1 to 254.  The workspace holds
+ * outputs, such as weight grads, every product is added in fp32.  Scales may be bytes 1 to
+ * 254; there elements below 2^-126 may count as 0.  The workspace holds
  * dopt_fp8_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned; where that is
  * 0 it may be NULL.
  */

@@ -12,7 +12,7 @@ int check_dense(const char *name, const dopt_dense *x) {
     const std::string n(name);
     if (!x) return fail(DOPT_ERR_INVALID, n + ": null");
     if (!is_dtype(x->dtype)) return fail(DOPT_ERR_INVALID, n + ": bad dtype");
-    if (x->rows < 0 || x->cols < 0 || x->rows > INT32_MAX || x->cols > INT32_MAX)
+    if (x->rows < 0 || x->cols < 0 || x->rows > DOPT_FP8_MAX_ROWS || x->cols > DOPT_FP8_MAX_ROWS)
         return fail(DOPT_ERR_INVALID, n + ": bad size");
     if (x->rows == 0 || x->cols == 0) return DOPT_OK;
     if (x->ld < x->cols || x->ld >= (1 << 23)) return fail(DOPT_ERR_INVALID, n + ": bad distance between rows");
@@ -26,7 +26,7 @@ int check_fp8(const char *name, const dopt_fp8_matrix *x) {
     const std::string n(name);
     if (!x) return fail(DOPT_ERR_INVALID, n + ": null");
     if (x->kind != DOPT_FP8_ROW && x->kind != DOPT_FP8_TILE) return fail(DOPT_ERR_INVALID, n + ": bad kind");
-    if (x->rows < 0 || x->cols < 0 || x->rows > INT32_MAX || x->cols > DOPT_FP8_MAX_COLS)
+    if (x->rows < 0 || x->cols < 0 || x->rows > DOPT_FP8_MAX_ROWS || x->cols > DOPT_FP8_MAX_COLS)
         return fail(DOPT_ERR_INVALID, n + ": bad size");
     if (x->rows == 0 || x->cols == 0) return DOPT_OK;
     const int64_t padded = (x->cols + DOPT_FP8_BLOCK - 1) / DOPT_FP8_BLOCK * DOPT_FP8_BLOCK;
@@ -264,7 +264,7 @@ using namespace dopt;
 extern "C" int dopt_fp8_layout(int64_t rows, int64_t cols, int32_t kind, dopt_fp8_sizes *out) {
     if (!out) return fail(DOPT_ERR_INVALID, "null output");
     if (kind != DOPT_FP8_ROW && kind != DOPT_FP8_TILE) return fail(DOPT_ERR_INVALID, "bad kind");
-    if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > DOPT_FP8_MAX_COLS) return fail(DOPT_ERR_INVALID, "bad size");
+    if (rows < 0 || cols < 0 || rows > DOPT_FP8_MAX_ROWS || cols > DOPT_FP8_MAX_COLS) return fail(DOPT_ERR_INVALID, "bad size");
     const int64_t groups = (cols + DOPT_FP8_BLOCK - 1) / DOPT_FP8_BLOCK;
     out->ld = groups * DOPT_FP8_BLOCK;
     out->scale_ld = kind == DOPT_FP8_ROW ? (rows + 15) / 16 * 16 : (rows + DOPT_FP8_BLOCK - 1) / DOPT_FP8_BLOCK;

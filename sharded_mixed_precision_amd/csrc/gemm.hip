@@ -65,50 +65,87 @@ __device__ __forceinline__ void put4(const GemmArgs &A, int row, int col, f32x4 
     else put4_as<DOPT_F16>(A.out, e, n, x, A.accumulate);
 }
 
-// A wave's results, FI x 16 rows and FJ x 16 columns from (m0, n0) on in groups of 64, as
-// the matrix instruction leaves them: register v of a lane is row 4 * (lane / 16) + v of
-// its 16 and column lane % 16, and instruction i and j of a group hold every fourth row and
-// column from i and j on.  Four neighbours of a row are stored at once.  The type is
-// told apart once: straight code for one type, 64 stores of it, is
-// what a tile fetches, and not the branches of all.
-template <int T, bool ADD, bool WHOLE, int FI, int FJ>
+// A wave's results, FI x FJ instructions of 16 x 16 from (m0, n0) on: in groups of 4, of
+// which instruction i and j hold every fourth row and column from i and j on. Register
+// v of a lane is row 4 * (lane / 16) + v of its 16, and column lane % 16. Four neighbours of a
+// row are stored at once. Where they are added to out, 16 reads are under way at a time. The type
+// and the bounds are told apart once for a tile: what it fetches is straight code for its own.
+enum { kWholeTile, kWholeColumns, kRagged };
+
+template <int T, bool ADD, int BOUNDS, int FI, int FJ>
 __device__ __forceinline__ void store_as(const GemmArgs &A, int m0, int n0, const f32x4 (&acc)[FI][FJ]) {
+    constexpr int ES = T == DOPT_F32 ? 4 : 2, H = FJ / 4, I = FI < 4 / H ? FI : 4 / H;
     const int lane = threadIdx.x % 64;
     const int row0 = m0 + 16 * (lane / 16), col0 = n0 + 4 * (lane % 16);
+    const uint32_t of_lane = static_cast<uint32_t>(16 * (lane / 16)) * static_cast<uint32_t>(A.out_ld * ES) + 4u * ES * (lane % 16);
+    char *out = static_cast<char *>(A.out) + (static_cast<int64_t>(m0) * A.out_ld + n0) * ES;
+    using Four = std::conditional_t<T == DOPT_F32, Float4, Bytes8>;
+    const auto delta = [](int i, int v) { return i / 4 * 64 + 4 * v + i % 4; };
+    const auto place = [&](int i, int v, int h) { return out + delta(i, v) * A.out_ld * ES + 64 * h * ES + of_lane; };
 #pragma unroll
-    for (int i = 0; i < FI; ++i)
+    for (int i0 = 0; i0 < FI; i0 += I) {
+        Four old[I][4][H];
+        if constexpr (ADD && BOUNDS != kRagged) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
+            for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int h = 0; h < FJ / 4; ++h) {
-                const int row = row0 + i / 4 * 64 + 4 * v + i % 4, col = col0 + 64 * h;
-                const f32x4 x = {acc[i][4 * h][v], acc[i][4 * h + 1][v], acc[i][4 * h + 2][v], acc[i][4 * h + 3][v]};
-                const int64_t e = static_cast<int64_t>(row) * A.out_ld + col;
-                if constexpr (WHOLE) {
-                    put4_as<T>(A.out, e, 4, x, ADD);
-                } else if (row < A.m) {
+                for (int v = 0; v < 4; ++v)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (col + c < A.n) {
-                            if constexpr (T == DOPT_F32) {
-                                float *p = static_cast<float *>(A.out) + e + c;
-                                *p = ADD ? *p + x[c] : x[c];
-                            } else {
-                                uint16_t *p = static_cast<uint16_t *>(A.out) + e + c;
-                                *p = static_cast<uint16_t>(from_float<T>(ADD ? to_float<T>(*p) + x[c] : x[c]));
+                    for (int h = 0; h < H; ++h)
+                        if (BOUNDS == kWholeTile || row0 + delta(i0 + i, v) < A.m) old[i][v][h] = *reinterpret_cast<const Four *>(place(i0 + i, v, h));
+        }
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    if (BOUNDS != kWholeTile && row0 + delta(i0 + i, v) >= A.m) continue;
+                    const auto &c = acc[i0 + i];
+                    f32x4 x = {c[4 * h][v], c[4 * h + 1][v], c[4 * h + 2][v], c[4 * h + 3][v]};
+                    char *p = place(i0 + i, v, h);
+                    if constexpr (BOUNDS == kRagged) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (col0 + 64 * h + e < A.n) {
+                                if constexpr (T == DOPT_F32) {
+                                    float *f = reinterpret_cast<float *>(p) + e;
+                                    *f = ADD ? *f + x[e] : x[e];
+                                } else {
+                                    uint16_t *f = reinterpret_cast<uint16_t *>(p) + e;
+                                    *f = static_cast<uint16_t>(from_float<T>(ADD ? to_float<T>(*f) + x[e] : x[e]));
+                                }
                             }
+                    } else if constexpr (T == DOPT_F32) {
+                        if (ADD) x += old[i][v][h].v;
+                        reinterpret_cast<Float4 *>(p)->v = x;
+                    } else {
+                        u32x2 r;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if constexpr (ADD) {
+                                x[2 * e] += to_float<T>(old[i][v][h].v[e] & 0xffffu);
+                                x[2 * e + 1] += to_float<T>(old[i][v][h].v[e] >> 16);
+                            }
+                            r[e] = from_float<T>(x[2 * e]) | from_float<T>(x[2 * e + 1]) << 16;
                         }
+                        reinterpret_cast<Bytes8 *>(p)->v = r;
+                    }
                 }
-            }
+    }
+}
+
+template <int T, bool ADD, int FI, int FJ>
+__device__ __forceinline__ void store_bounded(const GemmArgs &A, int m0, int n0, const f32x4 (&acc)[FI][FJ]) {
+    if (n0 + 16 * FJ > A.n) store_as<T, ADD, kRagged>(A, m0, n0, acc);
+    else if (m0 + 16 * FI > A.m) store_as<T, ADD, kWholeColumns>(A, m0, n0, acc);
+    else store_as<T, ADD, kWholeTile>(A, m0, n0, acc);
 }
 
 template <int T, int FI, int FJ>
 __device__ __forceinline__ void store_typed(const GemmArgs &A, int m0, int n0, const f32x4 (&acc)[FI][FJ]) {
-    const bool whole = m0 + 16 * FI <= A.m && n0 + 16 * FJ <= A.n;
-    if (whole && !A.accumulate) store_as<T, false, true>(A, m0, n0, acc);
-    else if (whole) store_as<T, true, true>(A, m0, n0, acc);
-    else if (!A.accumulate) store_as<T, false, false>(A, m0, n0, acc);
-    else store_as<T, true, false>(A, m0, n0, acc);
+    if (A.accumulate) store_bounded<T, true>(A, m0, n0, acc);
+    else store_bounded<T, false>(A, m0, n0, acc);
 }
 
 template <bool EXACT, int FI, int FJ>
@@ -786,7 +823,7 @@ static void launch_gemm(const GemmArgs &A, const Plan &p, hipStream_t stream) {
 }
 
 static bool size_ok(int64_t m, int64_t n, int64_t k) {
-    return m >= 0 && n >= 0 && k >= 0 && m <= INT32_MAX - 256 && n < (1 << 23) && k <= DOPT_FP8_MAX_COLS;
+    return m >= 0 && n >= 0 && k >= 0 && m <= DOPT_FP8_MAX_ROWS && n < (1 << 23) && k <= DOPT_FP8_MAX_COLS;
 }
 
 }  // namespace dopt

@@ -462,7 +462,7 @@ extern "C" int dopt_rmsnorm(const dopt_dense *x, const dopt_dense *residual, con
 }
 
 extern "C" int64_t dopt_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols) {
-    if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > DOPT_FP8_MAX_COLS) return fail(DOPT_ERR_INVALID, "bad size");
+    if (rows < 0 || cols < 0 || rows > DOPT_FP8_MAX_ROWS || cols > DOPT_FP8_MAX_COLS) return fail(DOPT_ERR_INVALID, "bad size");
     return workers_of(rows, cols) * cols * 4;
 }
 

@@ -36,7 +36,7 @@ def test_layout(rows, cols, kind, want):
 
 
 def test_layout_refusals():
-    for args in ((-1, 1, 0), (1, -1, 0), (1, (1 << 22) + 1, 0), (1 << 31, 1, 0), (1, 1, 2)):
+    for args in ((-1, 1, 0), (1, -1, 0), (1, (1 << 22) + 1, 0), ((1 << 30) + 1, 1, 0), (1, 1, 2)):
         refused(D.lib().dopt_fp8_layout(*args, ctypes.byref(D.dopt_fp8_sizes())), "bad")
     refused(D.lib().dopt_fp8_layout(1, 1, 0, None), "null output")
     with pytest.raises(D.DoptError):
@@ -75,6 +75,9 @@ def test_cast_refusals():
     refused(call(dense(10, 300, at=None), None, None, 0, q, None, None), "null device pointer")
     refused(call(dense(10, 300, at=AT + 1), None, None, 0, q, None, None), "aligned")
     refused(call(dense(-1, 300), None, None, 0, q, None, None), "bad size")
+    refused(call(dense((1 << 30) + 1, 1), None, None, 0, q, None, None), "bad size")
+    refused(call(dense((1 << 22) + 1, 1), None, None, 0, None, D.dopt_fp8_matrix(AT + (1 << 36), AT + (1 << 38), 1, (1 << 22) + 1, 1 << 23, 16, 0, 0),
+                 None), "bad size")
     refused(call(x, None, None, 0, fp8(11, 300), None, None), "not of x's size")
     refused(call(x, None, None, 0, None, q, None), "transpose")
     refused(call(x, None, None, 0, q, fp8(300, 10, "tile"), None), "kind")
