@@ -107,7 +107,8 @@ __device__ __forceinline__ void store_as(const GemmArgs &A, int m0, int n0, cons
                 for (int v = 0; v < 4; ++v)
 #pragma unroll
                     for (int h = 0; h < H; ++h)
-                        if (BOUNDS == kWholeTile || row0 + delta(i0 + i, v) < A.m) old[i][v][h] = *reinterpret_cast<const Four *>(place(i0 + i, v, h));
+                        if (BOUNDS == kWholeTile || row0 + delta(i0 + i, v) < A.m)
+                            old[i][v][h] = *reinterpret_cast<const Four *>(place(i0 + i, v, h));
         }
 #pragma unroll
         for (int i = 0; i < I; ++i)
@@ -206,8 +207,10 @@ __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs A) {
 // A lane holds 32 codes of row (lane % 16) of either operand; which of a step's 128
 // does not matter as long as both take the same.
 __device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
@@ -488,7 +491,8 @@ __global__ __launch_bounds__(256, STAGES > 2 ? 1 : 2) void k_gemm_tile(GemmArgs 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            put4_part(A, split, row0 + 4 * (4 * quarter + v) + i, col0 + 4 * r, f32x4{acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]});
+            put4_part(A, split, row0 + 4 * (4 * quarter + v) + i, col0 + 4 * r,
+                      f32x4{acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]});
 }
 
 // ---- large tiles --------------------------------------------------------------------

@@ -230,20 +230,21 @@ def test_gemm_random(m, n, k, kind):
         assert torch.equal(low, again)
 
 
-@pytest.mark.parametrize("m", [2, 100, 4000])
-def test_gemm_nan_stays_in_its_row_and_column(m):
-    n, k = 4000, 300
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(2, 4000, 300), (100, 4000, 300), (4000, 4000, 300), (4100, 3000, 1100)])
+def test_gemm_nan_stays_in_its_row_and_column(m, n, k, dtype):
     a, b = whole_numbers(gen(1), m, k, "row"), whole_numbers(gen(2), n, k, "row")
     want = F.values(a) @ F.values(b).t()
     x, y = m // 2, 1234
-    a.codes.view(torch.uint8)[x, 299] = 0x7f
+    a.codes.view(torch.uint8)[x, k - 1] = 0x7f
     b.codes.view(torch.uint8)[y, 0] = 0xff
-    out = torch.empty(m, n, device="cuda")
+    out = torch.empty(m, n, device="cuda", dtype=F.TYPES[dtype])
     ws = torch.empty(D.dopt_fp8_gemm_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
     D.dopt_fp8_gemm(a, b, out, False, ws, stream())
     assert torch.isnan(out[x]).all() and torch.isnan(out[:, y]).all()
     want[x], want[:, y] = math.nan, math.nan
-    assert torch.equal(torch.nan_to_num(out.double(), 0.5), torch.nan_to_num(want, 0.5))
+    want = want.float().to(out.dtype)  # sums are exact in fp32
+    assert torch.equal(torch.nan_to_num(out, 0.5), torch.nan_to_num(want, 0.5))
 
 
 def test_gemm_no_depth():
