@@ -97,18 +97,19 @@ __device__ __forceinline__ void store_as(const GemmArgs &A, int m0, int n0, cons
     using Four = std::conditional_t<T == DOPT_F32, Float4, Bytes8>;
     const auto delta = [](int i, int v) { return i / 4 * 64 + 4 * v + i % 4; };
     const auto place = [&](int i, int v, int h) { return out + delta(i, v) * A.out_ld * ES + 64 * h * ES + of_lane; };
+    const auto row_in = [&](int i, int v) { return BOUNDS == kWholeTile || row0 + delta(i, v) < A.m; };
+    const auto all_in = [&](int h) { return BOUNDS != kRagged || col0 + 64 * h + 4 <= A.n; };
 #pragma unroll
     for (int i0 = 0; i0 < FI; i0 += I) {
         Four old[I][4][H];
-        if constexpr (ADD && BOUNDS != kRagged) {
+        if constexpr (ADD) {
 #pragma unroll
             for (int i = 0; i < I; ++i)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
 #pragma unroll
                     for (int h = 0; h < H; ++h)
-                        if (BOUNDS == kWholeTile || row0 + delta(i0 + i, v) < A.m)
-                            old[i][v][h] = *reinterpret_cast<const Four *>(place(i0 + i, v, h));
+                        if (row_in(i0 + i, v) && all_in(h)) old[i][v][h] = *reinterpret_cast<const Four *>(place(i0 + i, v, h));
         }
 #pragma unroll
         for (int i = 0; i < I; ++i)
@@ -116,13 +117,13 @@ __device__ __forceinline__ void store_as(const GemmArgs &A, int m0, int n0, cons
             for (int v = 0; v < 4; ++v)
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    if (BOUNDS != kWholeTile && row0 + delta(i0 + i, v) >= A.m) continue;
+                    if (!row_in(i0 + i, v)) continue;
                     const auto &c = acc[i0 + i];
                     f32x4 x = {c[4 * h][v], c[4 * h + 1][v], c[4 * h + 2][v], c[4 * h + 3][v]};
                     char *p = place(i0 + i, v, h);
-                    if constexpr (BOUNDS == kRagged) {
+                    if (!all_in(h)) {  // the last one to three columns, by one lane
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 3; ++e)
                             if (col0 + 64 * h + e < A.n) {
                                 if constexpr (T == DOPT_F32) {
                                     float *f = reinterpret_cast<float *>(p) + e;
@@ -248,7 +249,8 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 }
 
 // 16 (or 4) bytes per lane from base + offset to shared memory at `to` + 16 (4) * lane, past
-// the registers.  The compiler does not know of the load: the kernel waits for it.
+// the registers.  The compiler does not know of the load: the kernel waits for it.  `base` comes
+// from scalar arithmetic; written by a vector instruction it would need 5 cycles before the load.
 __device__ __forceinline__ void load_lds16(uint32_t to, uint32_t offset, const uint8_t *base) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
