@@ -9,7 +9,7 @@
 //   1 x 14336 x 4096        12.5 us, 4.7 TB/s     k_gemm_few
 //   1024 x 2304 x 768        7.4 us               k_gemm_tile, 3 stages
 //   1024 x 4096 x 4096      19.0 us, 1.8 PFLOP/s  k_gemm_tile, 3 stages
-//   8192 x 14336 x 4096      370 us, 2.6 PFLOP/s  k_gemm_big
+//   8192 x 14336 x 4096  366 to 388 us, 2.5 to 2.6 PFLOP/s  k_gemm_big
 //   8192 x 4096 x 14336      341 us, 2.8 PFLOP/s  k_gemm_big
 //   777 x 50257 x 768, fp32 out    93 us          k_gemm_tile, 2 stages: 40 us of them are the stores
 //   4096 x 4096 x 8192, fp32 +=   202 us, 1.36 PFLOP/s  k_gemm_wide
@@ -510,7 +510,7 @@ constexpr int kBigOperand = StepMem<kBig>::kB, kBigBuffer = StepMem<kBig>::kByte
 //   phase 1 multiplies the other rows, starts the loads of the step after the next into the
 //           free buffer, and reads the next step's first 64 rows of a and all of b, each
 //           register once its last product is under way.
-// 8192 x 14336 x 4096: 366 to 377 us; the matrix cores are busy 60% of the cycles.  With 8 waves of 128 x 64 and
+// 8192 x 14336 x 4096: 366 to 388 us; the matrix cores are busy 60% of the cycles.  With 8 waves of 128 x 64 and
 // the same order of work 397 to 415 us (more reads of shared memory, and both waves of a SIMD
 // wait at the same time), with reads and products of a step between two barriers 408; by instructions of 32 x 32 390 to
 // 401; with all 16 loads at the start of phase 1 401 to 412, since they fill the path to the
