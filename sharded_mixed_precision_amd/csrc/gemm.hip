@@ -16,7 +16,7 @@
 //   8192 x 4096 x 14336, fp32 out 614 us, 1.57 PFLOP/s  k_gemm_wide
 #include <algorithm>
 #include <string>
-#include <utility>
+#include <type_traits>
 
 #include "fp8.h"
 
