@@ -2,18 +2,16 @@
 // a[m][k] b[n][k].
 //
 // Four kernels, by plan_of: up to 16 rows of a (k_gemm_few), bound by the one reading of b; 128 x 128
-// tiles (k_gemm_tile), bound by latency where tiles are few; 256 x 256 tiles (k_gemm_big for codes,
-// k_gemm_wide for widened ones), bound by the matrix cores and, with them, by power: the clock
-// falls from 2.4 to 2.05 GHz.  Measured on MI355X, where a library's large e4m3 product without scales of blocks
-// reaches 2.5 to 3.0 and a bf16 one 1.39 PFLOP/s, and a copy 5.1 TB/s:
-//   1 x 14336 x 4096        12.5 us, 4.7 TB/s     k_gemm_few
-//   1024 x 2304 x 768        7.4 us               k_gemm_tile, 3 stages
-//   1024 x 4096 x 4096      19.0 us, 1.8 PFLOP/s  k_gemm_tile, 3 stages
-//   8192 x 14336 x 4096  366 to 388 us, 2.5 to 2.6 PFLOP/s  k_gemm_big
-//   8192 x 4096 x 14336      341 us, 2.8 PFLOP/s  k_gemm_big
-//   777 x 50257 x 768, fp32 out    93 us          k_gemm_tile, 2 stages: 40 us of them are the stores
-//   4096 x 4096 x 8192, fp32 +=   202 us, 1.36 PFLOP/s  k_gemm_wide
-//   8192 x 4096 x 14336, fp32 out 614 us, 1.57 PFLOP/s  k_gemm_wide
+// tiles (k_gemm_tile), bound by latency where tiles are few; 256 x 256 tiles (k_gemm_wide for sums in
+// fp32, k_gemm_big for coarse ones).  Median times on MI355X, where a copy reaches 5.1 TB/s, in brackets those of
+// dopt_fp8_gemm_coarse:
+//   1 x 14336 x 4096        14.6 us, 4.0 TB/s              k_gemm_few
+//   1024 x 2304 x 768       10.1 us (7.6)                  k_gemm_tile, 3 stages
+//   1024 x 4096 x 4096      35 us (20.5)                   k_gemm_tile, 3 stages
+//   8192 x 14336 x 4096     640 us, 1.50 PFLOP/s (374, 2.57)   k_gemm_wide (k_gemm_big)
+//   8192 x 4096 x 14336     614 us, 1.57 PFLOP/s (347, 2.77)   k_gemm_wide (k_gemm_big)
+//   777 x 50257 x 768, fp32 out    93 us                   k_gemm_tile, 2 stages: 40 us of them are the stores
+//   4096 x 4096 x 8192, fp32 +=   202 us, 1.36 PFLOP/s     k_gemm_wide
 #include <algorithm>
 #include <string>
 #include <type_traits>
@@ -167,7 +165,7 @@ __device__ __forceinline__ void store_typed(const GemmArgs &A, int m0, int n0, c
 
 template <bool EXACT, int FI, int FJ>
 __device__ __forceinline__ void store_tile(const GemmArgs &A, int m0, int n0, const f32x4 (&acc)[FI][FJ]) {
-    if constexpr (EXACT) store_typed<DOPT_F32>(A, m0, n0, acc);
+    if (EXACT && A.dtype == DOPT_F32) store_typed<DOPT_F32>(A, m0, n0, acc);
     else if (A.dtype == DOPT_BF16) store_typed<DOPT_BF16>(A, m0, n0, acc);
     else store_typed<DOPT_F16>(A, m0, n0, acc);
 }
@@ -191,19 +189,21 @@ __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs A) {
 
 // ---- one step's products ------------------------------------------------------------
 
-// Two ways to multiply, chosen by the output's type.
+// Two ways to multiply, chosen by the caller.
 //
-// 16-bit outputs: the matrix instruction that takes e4m3 codes and applies the
+// dopt_fp8_gemm (EXACT): the codes become bf16 with their scale applied (exact: 4
+// bits of mantissa, and the scale is a power of two) in registers, and the bf16
+// instruction multiplies, whose products and sums are fp32's (1e-7 of the result),
+// at half the codes' rate.
+//
+// dopt_fp8_gemm_coarse: the matrix instruction that takes e4m3 codes and applies the
 // scales itself.  It adds 8 neighbouring products of k with 14 bits below the
 // largest of them, and such sums to one another and to the accumulator in
 // fp32 (measured: a product 2^-14 of the largest in its 8 is lost, one 2^-23 of it in
 // another 8 is kept).  On random operands a result is thereby off by 3 to 5e-5 of
-// the output's root mean square, a fifth of fp16's own rounding and a fortieth of bf16's.
-//
-// fp32 outputs, which would keep that error: the codes become bf16 with their
-// scale applied (exact: 4 bits of mantissa, and the scale is a power of two)
-// in registers, and the bf16 instruction multiplies, whose products and sums are
-// fp32's (1e-7 of the result), at half the codes' rate.
+// the output's root mean square, which moves one of 50 bf16 and one of 10 fp16 outputs by a
+// step; where large products cancel, all that is left of the small ones next to them may be lost.  No other
+// instruction takes e4m3 and adds more precisely: the one without scales, at half the rate, cuts the same.
 //
 // A lane holds 32 codes of row (lane % 16) of either operand; which of a step's 128
 // does not matter as long as both take the same.
@@ -727,12 +727,13 @@ __global__ __launch_bounds__(512, 2) void k_gemm_wide(GemmArgs A) {
 // Up to 16 rows of a: b is read once, and what bounds the call is how fast.  A
 // workgroup takes 16 columns of the output, its waves share the steps along k, and
 // their sums are joined through shared memory.  A wave has the operands of
-// kFewDepth steps under way before it multiplies the first.  1 x 14336 x 4096: 12.5 us, 15.7 without
+// kFewDepth steps under way before it multiplies the first.  It adds in fp32 whoever calls: with
+// the codes' own instruction 1 x 14336 x 4096 took 13.8 us for 14.6, 1 x 4096 x 14336 15.2 for 15.4.  1 x 14336 x 4096: 12.5 us, 15.7 without
 // that; 27 with 8 steps, whose waves are too few; 15.3 with b read around the caches.  17 to 64 rows so, with
 // a read anew by every workgroup, took 28 us (32 rows) and 43 (64) where k_gemm_tile takes 17.
 constexpr int kFewDepth = 4;
 
-template <int WAVES, bool BROW, bool EXACT>
+template <int WAVES, bool BROW>
 __global__ __launch_bounds__(WAVES * 64) void k_gemm_few(GemmArgs A) {
     __shared__ __align__(16) float s_sum[WAVES][256];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -761,15 +762,11 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_few(GemmArgs A) {
 #pragma unroll
         for (int u = 0; u < kFewDepth; ++u) {
             if (k0 + u * WAVES >= end) break;
-            if constexpr (EXACT) {
-                const float fa = scale_of<0>(sa[u]), fb = scale_of<0>(sb[u]);
+            const float fa = scale_of<0>(sa[u]), fb = scale_of<0>(sb[u]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc = mfma(widen8(a[u][j / 2][2 * (j % 2)], a[u][j / 2][2 * (j % 2) + 1], fa),
-                               widen8(b[u][j / 2][2 * (j % 2)], b[u][j / 2][2 * (j % 2) + 1], fb), acc);
-            } else {
-                acc = mfma<0, 0>(join(a[u][0], a[u][1]), join(b[u][0], b[u][1]), acc, sa[u], sb[u]);
-            }
+            for (int j = 0; j < 4; ++j)
+                acc = mfma(widen8(a[u][j / 2][2 * (j % 2)], a[u][j / 2][2 * (j % 2) + 1], fa),
+                           widen8(b[u][j / 2][2 * (j % 2)], b[u][j / 2][2 * (j % 2) + 1], fb), acc);
         }
     }
 #pragma unroll
@@ -816,7 +813,7 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k) {
         if (small <= kCus) {
             // A tile or less to a CU: what counts is how soon a step's loads are back, so three steps are under way,
             // and with 8 steps or more to each the steps are shared by several workgroups.
-            // 128 x 4096 x 4096, bf16 out: 24.8 us with 2 stages, 16.8 with 3 or 4; split in 2, 4, 8: 16.0,
+            // 128 x 4096 x 4096, coarse sums: 24.8 us with 2 stages, 16.8 with 3 or 4; split in 2, 4, 8: 16.0,
             // 16.2, 19.3.  1024 x 4096 x 4096: 26.7, 19.4.  768 x 768 x 8192, fp32 out: 52.7 us, split in 4 23.6, in 8 29.5.
             p.rows = p.cols = kSmall;
             p.stages = 3;
@@ -824,7 +821,7 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k) {
         } else {
             // A round of big tiles takes about 7 us and 1.25 for each step, one of twice as many small ones
             // 2.5 and 0.92 (measured at 256 to 1024 small tiles and 8 to 32 steps; fp32 outputs in the same proportion).
-            // Small and big, us: 2048 x 4096 x 4096 34, 46; 4096 x 4096 x 4096 64, 53; 3073 x 4096 x 4096 56, 47;
+            // Small and big, us, with coarse sums: 2048 x 4096 x 4096 34, 46; 4096 x 4096 x 4096 64, 53; 3073 x 4096 x 4096 56, 47;
             // 8192 x 2304 x 768 24, 29; 4096 x 14336 x 128 33, 38; fp32 out 67, 78; 123, 96; 108, 85; 36, 44; 53, 59.
             const int64_t as_big = ceil_div(big, kCus) * (28 + 5 * steps), as_small = ceil_div(small, 2 * kCus) * (100 + 37 * steps);
             p.rows = p.cols = as_big * 10 <= as_small ? kBig : kSmall;
@@ -842,9 +839,9 @@ template <bool BROW, bool EXACT>
 static void launch_gemm(const GemmArgs &A, const Plan &p, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(A.tiles_m * A.tiles_n), static_cast<unsigned>(A.splits));
     if (p.few) {
-        if (p.waves == 2) k_gemm_few<2, BROW, EXACT><<<grid, 128, 0, stream>>>(A);
-        else if (p.waves == 4) k_gemm_few<4, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
-        else k_gemm_few<8, BROW, EXACT><<<grid, 512, 0, stream>>>(A);
+        if (p.waves == 2) k_gemm_few<2, BROW><<<grid, 128, 0, stream>>>(A);
+        else if (p.waves == 4) k_gemm_few<4, BROW><<<grid, 256, 0, stream>>>(A);
+        else k_gemm_few<8, BROW><<<grid, 512, 0, stream>>>(A);
     } else if (p.rows == kBig) {
         if constexpr (EXACT) k_gemm_wide<BROW><<<grid, 512, 0, stream>>>(A);
         else k_gemm_big<BROW><<<grid, 256, 0, stream>>>(A);
@@ -869,13 +866,14 @@ extern "C" int64_t dopt_fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k
     return p.splits > 1 ? int64_t(p.splits) * m * part_ld_of(n) * 4 : 0;
 }
 
-extern "C" int dopt_fp8_gemm(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, const dopt_dense *out, int32_t accumulate,
-                             void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+static int gemm(bool exact, const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, const dopt_dense *out, int32_t accumulate,
+                void *workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (int rc = check_fp8("a", a)) return rc;
     if (int rc = check_fp8("b", b)) return rc;
     if (int rc = check_dense("out", out)) return rc;
     if (a->kind != DOPT_FP8_ROW) return fail(DOPT_ERR_INVALID, "a: not of kind ROW");
     if (a->cols != b->cols) return fail(DOPT_ERR_INVALID, "a and b differ in columns");
+    if (!exact && out->dtype == DOPT_F32) return fail(DOPT_ERR_INVALID, "out: fp32, which coarse sums are not for");
     if (out->rows != a->rows || out->cols != b->rows) return fail(DOPT_ERR_INVALID, "out: not of a's rows x b's rows");
     const int64_t m = a->rows, n = b->rows, k = a->cols;
     if (!size_ok(m, n, k)) return fail(DOPT_ERR_INVALID, "too large");
@@ -912,7 +910,7 @@ extern "C" int dopt_fp8_gemm(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b,
     A.split_steps = p.split_steps;
     A.dtype = out->dtype;
     A.accumulate = accumulate != 0;
-    const bool row = b->kind == DOPT_FP8_ROW, exact = out->dtype == DOPT_F32;
+    const bool row = b->kind == DOPT_FP8_ROW;
     if (row && exact) launch_gemm<true, true>(A, p, stream);
     else if (row) launch_gemm<true, false>(A, p, stream);
     else if (exact) launch_gemm<false, true>(A, p, stream);
@@ -924,4 +922,14 @@ extern "C" int dopt_fp8_gemm(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b,
         return launched("dopt_fp8_gemm");
     }
     return DOPT_OK;
+}
+
+extern "C" int dopt_fp8_gemm(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, const dopt_dense *out, int32_t accumulate,
+                             void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+    return gemm(true, a, b, out, accumulate, workspace, workspace_bytes, stream);
+}
+
+extern "C" int dopt_fp8_gemm_coarse(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, const dopt_dense *out, int32_t accumulate,
+                                    void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+    return gemm(false, a, b, out, accumulate, workspace, workspace_bytes, stream);
 }

@@ -209,3 +209,16 @@ def test_binding_refuses_host_tensors_and_bad_matrices():
         D.fp8_matrix(torch.zeros(2, 128), u8(1, 16), 2, 100)
     with pytest.raises(D.DoptError, match="not a device tensor"):
         D.fp8_matrix(u8(2, 128), u8(1, 16), 2, 100)
+
+
+def test_gemm_coarse_refusals():
+    """As dopt_fp8_gemm's, and fp32 outputs."""
+    call = D.lib().dopt_fp8_gemm_coarse
+    a, b, o = fp8(100, 300), fp8(50, 300, "tile", at=AT + (1 << 37)), dense(100, 50)
+    refused(call(a, b, dense(100, 50, D.DOPT_F32), 0, None, 0, None), "coarse")
+    refused(call(None, b, o, 0, None, 0, None), "a: null")
+    refused(call(a, fp8(50, 301), o, 0, None, 0, None), "differ in columns")
+    refused(call(a, b, dense(100, 50, at=a.codes), 0, None, 0, None), "overlaps a")
+    big = fp8(100, 1 << 20), fp8(50, 1 << 20, at=AT + (1 << 37))
+    refused(call(*big, o, 0, None, 0, None), "workspace")
+    assert call(fp8(0, 300, codes=None, scales=None), b, dense(0, 50, at=None), 0, None, 0, None) == 0

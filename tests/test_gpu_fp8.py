@@ -689,3 +689,64 @@ def test_binding_refusals():
         D.fp8_matrix(q.codes, q.scales[:, :3], 4, 256)
     with pytest.raises(D.DoptError, match="overlaps"):
         D.dopt_fp8_gemm(q, q, q.codes.view(torch.float32).view(4, 64)[:, :4])
+
+
+def cancelling(g, m, n, k):
+    """Operands whose products, in each 8 neighbours along k, are 2^16, -2^16 and 6 multiples of 2^-4 up to 9 / 16, in any
+    order.  A sum in fp32 is exact in any order: 128 of them are below 2^20 + 128 in steps of 2^-4, and what
+    remains of each 128 below 128.  One with 20 bits or fewer below the largest of its 8 loses most of it."""
+    a, b = fp8_alloc(m, k), fp8_alloc(n, k)
+    small = lambda rows: torch.randint(1, 4, (rows, k), generator=g, device="cuda").float() / 4  # noqa: E731
+    x, y = small(m) * (1 - 2 * torch.randint(0, 2, (m, k), generator=g, device="cuda").float()), small(n)
+    at = torch.rand(k // 8, 8, generator=g, device="cuda").argsort(1) + 8 * torch.arange(k // 8, device="cuda")[:, None]
+    x[:, at[:, 0]], x[:, at[:, 1]] = 256.0, -256.0
+    y[:, at[:, :2].flatten()] = 256.0
+    for q, v in ((a, x), (b, y)):
+        q.codes.view(torch.uint8).zero_()
+        q.codes.view(torch.uint8)[:, :k] = v.to(torch.float8_e4m3fn).view(torch.uint8)
+        q.scales.view(torch.uint8).fill_(127)
+    return a, b
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 4096), (16, 200, 520), (50, 96, 1112), (150, 200, 4000), (600, 700, 904), (1300, 2500, 640),
+                                   (3300, 4000, 512), (4100, 3000, 1096)])
+def test_gemm_sums_in_fp32(m, n, k, dtype):
+    """Large products that cancel leave the small ones next to them as they are, whatever the output's type."""
+    a, b = cancelling(gen(m + n + k), m, n, k)
+    want = F.values(a) @ F.values(b).t()
+    assert float(want.abs().max()) < 2.0 ** 12 and float(want.square().mean()) > 1  # exact in fp32, and not all near 0
+    ws = torch.empty(D.dopt_fp8_gemm_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    out = torch.full((m, n), math.nan, dtype=F.TYPES[dtype], device="cuda")
+    D.dopt_fp8_gemm(a, b, out, False, ws, stream())
+    assert torch.equal(out, want.float().to(out.dtype))
+
+
+@pytest.mark.parametrize("kind", ["tile", "row"])
+@pytest.mark.parametrize("m,n,k", [(3, 200, 4096), (50, 90, 1111), (150, 200, 3000), (600, 700, 900), (1300, 2500, 8400), (3300, 4000, 512),
+                                   (4100, 3000, 1100), (2100, 4200, 8300)])
+def test_gemm_coarse(m, n, k, kind):
+    """The matrix cores' own sums: exact on whole numbers with few bits, within IN_EIGHT of the sum of |a||b| on others."""
+    g = gen(m + n + k)
+    a, b = whole_numbers(g, m, k, "row", 1), whole_numbers(g, n, k, kind, 1)  # products of 5 bits, times 1 or 1 / 2, 1 / 4
+    ws = torch.empty(D.dopt_fp8_gemm_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    want = (F.values(a) @ F.values(b).t()).float()
+    for t in (torch.bfloat16, torch.float16):
+        out = torch.full((m + 1, n + 3), math.nan, dtype=t, device="cuda")
+        D.dopt_fp8_gemm_coarse(a, b, out[:m, :n], False, ws, stream())
+        assert torch.equal(out[:m, :n], want.to(t))
+        D.dopt_fp8_gemm_coarse(a, b, out[:m, :n], True, ws, stream())
+        assert torch.equal(out[:m, :n], (want.to(t).float() + want).to(t))
+        assert torch.isnan(out[m:]).all() and torch.isnan(out[:, n:]).all()
+    a = held(F.tokens(g, m, k, 1.0, "cuda"))
+    b = held(F.tokens(g, n, k, 0.02, "cuda"), kind)
+    x, y = F.values(a), F.values(b)
+    want, size = x @ y.t(), x.abs() @ y.abs().t()
+    for t in ("bf16", "f16"):
+        low, again = torch.empty(m, n, dtype=F.TYPES[t], device="cuda"), torch.empty(m, n, dtype=F.TYPES[t], device="cuda")
+        D.dopt_fp8_gemm_coarse(a, b, low, False, ws, stream())
+        bound = (k * 2 * U + IN_EIGHT) * size
+        bound = bound + F.HALF_STEP[t] * (want.abs() + bound) + F.TINY[t]
+        assert bool(((low.double() - want).abs() <= bound).all())
+        D.dopt_fp8_gemm_coarse(a, b, again, False, ws, stream())
+        assert torch.equal(low, again)
