@@ -93,7 +93,7 @@ int dopt_fp8_layout(int64_t rows, int64_t cols, int32_t kind, dopt_fp8_sizes *ou
  * `transposed` its transpose (x->cols x x->rows); either may be NULL, and
  * both are of one kind.  With row_factor and col_factor (x->rows fp32 and
  * x->cols elements of col_dtype; both or neither), what is cast is
- * x[r][c] * row_factor[r] * col_factor[c], rounded to fp32 once: with
+ * x[r][c] * row_factor[r] * col_factor[c], in 64 bits and rounded to fp32 once: with
  * dopt_rmsnorm's rstd and weight, the norm's output from its kept input, bit for bit.
  */
 int dopt_fp8_cast(const dopt_dense *x, const float *row_factor, const void *col_factor, int32_t col_dtype,

@@ -176,12 +176,14 @@ __device__ __forceinline__ void load_vector8(const void *p, int32_t dtype, int64
     else unpack8<DOPT_F16>(load8<DOPT_F16>(p, e, n), x);
 }
 
-// x * r * w rounded once: what the first product loses goes into the second.
-// A code lies next to a border as often as its value is off, so with two
-// roundings twice as many codes would differ from the formula's.
+// x * r * w in 64 bits, where x * r is exact and in range, rounded to fp32 at the
+// end.  In 32 bits x * r may be infinite or lose bits where the whole would not, and a second rounding
+// makes twice as many codes differ from the formula's, since a code lies next to a border as often
+// as its value is off.  8192 x 8192 bf16 norm with a residual: 92.5 us; in 32 bits with what
+// the first product loses added to the second, 90.6; so, and again in 64 bits where
+// a product of the 8 left the range, 95.2.
 __device__ __forceinline__ float product3(float x, float r, float w) {
-    const float t = x * r;
-    return fmaf(t, w, fmaf(x, r, -t) * w);
+    return static_cast<float>(static_cast<double>(x) * r * w);
 }
 
 // ---- device: the 8-bit format -----------------------------------------------------

@@ -750,3 +750,41 @@ def test_gemm_coarse(m, n, k, kind):
         assert bool(((low.double() - want).abs() <= bound).all())
         D.dopt_fp8_gemm_coarse(a, b, again, False, ws, stream())
         assert torch.equal(low, again)
+
+
+@pytest.mark.parametrize("kind", ["row", "tile"])
+@pytest.mark.parametrize("dtype,wtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16"), ("f16", "f16")])
+def test_cast_with_factors_of_all_sizes(dtype, wtype, kind):
+    """x * row_factor is far out of fp32's range, below and above, where the whole product is in it; and the other way round."""
+    g = gen(11)
+
+    def wide(t, *shape):
+        low, high = (-24, 15) if t == "f16" else (-140, 127)
+        e = torch.randint(low, high + 1, shape, generator=g, device="cuda").float()
+        sign = 1 - 2 * torch.randint(0, 2, shape, generator=g, device="cuda").float()
+        return (torch.ldexp(torch.rand(shape, generator=g, device="cuda", dtype=torch.float64) + 1, e).float() * sign).to(F.TYPES[t])
+
+    x, row, col = wide(dtype, 260, 390), wide("f32", 260), wide(wtype, 390)
+    if dtype == wtype == "f32":
+        x[0, 0], row[0], col[0] = 1e30, 1e20, 1e-30
+        x[0, 1], col[1] = 1e-38, 1e38
+        x[129, 1], row[129] = 1e-30, 1e-20
+    want = (x.double() * row[:, None].double() * col.double()).float()  # 24 + 24 + 24 bits, off by 2^-53 before its rounding to fp32
+    both = poisoned(260, 390, kind), poisoned(390, 260, kind)
+    D.dopt_fp8_cast(x, *both, row, col, stream())
+    same_codes(both[0], want, kind)
+    same_codes(both[1], want.t(), kind)
+
+
+def test_norm_weights_of_all_sizes():
+    """Infinite, NaN, very large and very small weights: y is h * rstd * weight wherever that is, a zero times infinity a NaN."""
+    x = torch.randn(5, 700, generator=gen(1), device="cuda")
+    x[2, :9], x[3] = 0, x[3] * 1e-25
+    w = torch.ones(700, device="cuda")
+    w[:8] = torch.tensor([math.inf, -math.inf, math.nan, 3e38, -1e-38, 1e-45, 0.0, -0.0])
+    w[8:12] = torch.tensor([1e30, 1e25, -1e20, 2e-20])
+    y, rstd = torch.empty_like(x), torch.empty(5, device="cuda")
+    D.dopt_rmsnorm(x, w, 1e-6, y=y, rstd=rstd, stream=stream())
+    assert torch.equal(torch.isnan(y), torch.isnan(x.double() * rstd.double()[:, None] * w.double()))
+    want = (x.double() * rstd.double()[:, None] * w.double()).float()
+    assert torch.equal(torch.nan_to_num(y, 0.5, 2.0, 3.0), torch.nan_to_num(want, 0.5, 2.0, 3.0))
