@@ -126,8 +126,9 @@ int dopt_fp8_gemm_coarse(const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, con
  *     y    = h * rstd * weight, rounded to fp32 once
  * h (NULL: not kept; may be x or residual itself), rstd (fp32, one per row;
  * NULL: not kept) and y: `y` in x's type, `q` in 8 bits (kind ROW), or both.
- * The weight is x->cols elements of weight_dtype.  Squares of 8 neighbours are
- * added in fp32, their sums and the rest of rstd in 64 bits.
+ * The weight is x->cols elements of weight_dtype.  Squares, their sum and
+ * rstd are in 64 bits, so a row of any finite numbers has its rstd; it is infinite
+ * where mean(h^2) + eps is below 2^-256.
  */
 int dopt_rmsnorm(const dopt_dense *x, const dopt_dense *residual, const void *weight, int32_t weight_dtype, double eps,
                  const dopt_dense *h, const dopt_dense *y, const dopt_fp8_matrix *q, float *rstd, hipStream_t stream);

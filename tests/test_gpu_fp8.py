@@ -788,3 +788,28 @@ def test_norm_weights_of_all_sizes():
     assert torch.equal(torch.isnan(y), torch.isnan(x.double() * rstd.double()[:, None] * w.double()))
     want = (x.double() * rstd.double()[:, None] * w.double()).float()
     assert torch.equal(torch.nan_to_num(y, 0.5, 2.0, 3.0), torch.nan_to_num(want, 0.5, 2.0, 3.0))
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [7, 500, 1000, 2047, 4096, 8000, 16001, 20000])
+def test_norm_rows_of_all_sizes(cols, dtype, eps):
+    """Rows whose squares, or whose mean square, are far above or below fp32's range: rstd as the formula's in 64 bits, rounded
+    to fp32, and y from it; infinite where it is above fp32's range, and 0 only for rows with an infinity."""
+    t = F.TYPES[dtype]
+    sizes = [1.0, 1e18, 2e19, 1e20, 1e30, 1e37, 1e-18, 1e-22, 1e-23, 1e-30, 1e-37, 1e-43, 1.0, 1e-30, 1.0]
+    x = torch.rand(len(sizes), cols, generator=gen(cols), device="cuda", dtype=torch.float64) + 0.5
+    x = (x * torch.tensor(sizes, device="cuda", dtype=torch.float64)[:, None]).to(t)
+    x[12, cols // 2], x[13, cols - 1] = 1e25, 1.0  # one large among others
+    x[14] = torch.finfo(t).max
+    w = torch.rand(cols, generator=gen(2), device="cuda") + 0.5
+    y, q, rstd = torch.empty_like(x), poisoned(len(sizes), cols), torch.empty(len(sizes), device="cuda")
+    D.dopt_rmsnorm(x, w, eps, y=y, q=q, rstd=rstd, stream=stream())
+    want = 1.0 / torch.sqrt(x.double().square().mean(1) + eps)
+    held_as = want.float()  # infinite from 2^128 on
+    assert torch.equal(torch.isinf(rstd), torch.isinf(held_as))
+    finite = ~torch.isinf(held_as)
+    assert bool(((rstd.double() - want).abs() <= norm_slack(cols) * want + 2.0 ** -150)[finite].all())
+    value = (x.double() * rstd.double()[:, None] * w.double()).float()
+    assert torch.equal(torch.nan_to_num(y, 0.5), torch.nan_to_num(value.to(t), 0.5))
+    same_codes(q, value, "row")
