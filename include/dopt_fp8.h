@@ -135,9 +135,9 @@ int dopt_rmsnorm(const dopt_dense *x, const dopt_dense *residual, const void *we
 
 /*
  * dopt_rmsnorm_grad -- the backward pass, from the grad dy of y (h's type or
- * fp32) and what the forward pass kept.  Per row, with g = dy * weight:
- *     dx = dh + rstd * (g - h * (rstd^2 * mean(g * h)))
- *     dweight[c] = sum over rows of dy[r][c] * (h[r][c] * rstd[r]), plus dweight[c] if `accumulate`
+ * fp32) and what the forward pass kept.  Per row, with g = dy * weight and n = h * rstd:
+ *     dx = dh + rstd * (g - n * mean(g * n))
+ *     dweight[c] = sum over rows of dy[r][c] * n[r][c], plus dweight[c] if `accumulate`
  * dh (NULL: 0) is the grad that reaches h past the norm, in h's type; dx, in
  * h's type, is the grad of x and of the residual, and may be dh or dy itself.  dweight is
  * h->cols elements of dweight_dtype, sums in fp32.  The workspace holds

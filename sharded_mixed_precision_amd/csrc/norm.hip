@@ -202,6 +202,9 @@ struct NormGradArgs {
     int32_t rows, cols, wdtype, workers;
 };
 
+// With n = h * rstd, which is at most sqrt(cols), dx = dh + rstd * (g - n * mean(g * n)): neither rstd^2
+// nor g * h is formed, which may be out of range where dx is not.
+//
 // Workgroups share the rows, a row to a wave or to the whole workgroup, and
 // hold the weight's grad of theirs in registers; a workgroup leaves one row of
 // sums, which k_norm_weight joins in a fixed order.  512 of them, of at least 2 rows each: 2048 x 4096
@@ -258,17 +261,17 @@ __global__ __launch_bounds__(LANES > kNormThreads ? LANES : kNormThreads) void k
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(element<TD>(dy[v], j) * w[v][j], element<T>(h[v], j), s);
-            const float c = rstd * rstd * (row_sum<LANES>(s, s_sum) / cols);
+                for (int j = 0; j < 8; ++j) s = fmaf(element<TD>(dy[v], j) * w[v][j], element<T>(h[v], j) * rstd, s);
+            const float c = row_sum<LANES>(s, s_sum) / cols;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int64_t e = 8 * (t + int64_t(LANES) * v);
                 float x[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float d = element<TD>(dy[v], j), hj = element<T>(h[v], j);
-                    dw[v][j] = fmaf(d, hj * rstd, dw[v][j]);
-                    x[j] = rstd * (d * w[v][j] - hj * c);
+                    const float d = element<TD>(dy[v], j), n = element<T>(h[v], j) * rstd;
+                    dw[v][j] = fmaf(d, n, dw[v][j]);
+                    x[j] = rstd * (d * w[v][j] - n * c);
                     if (A.dh) x[j] += element<T>(dh[v], j);
                 }
                 store8<T>(A.dx, row * A.dx_ld + e, count8(A.cols, e), pack8<T>(x));
@@ -306,10 +309,10 @@ __global__ __launch_bounds__(LANES > kNormThreads ? LANES : kNormThreads) void k
                 unpack8<T>(load8<T>(A.h, row * A.h_ld + e, n), hx);
                 load_vector8(A.weight, A.wdtype, e, n, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q = fmaf(d[j] * w[j], hx[j], q);
+                for (int j = 0; j < 8; ++j) q = fmaf(d[j] * w[j], hx[j] * rstd, q);
                 s += q;
             }
-            const float c = rstd * rstd * (row_sum<LANES>(s, s_sum) / cols);
+            const float c = row_sum<LANES>(s, s_sum) / cols;
             for (int64_t e = 8 * t; e < A.cols; e += 8 * LANES) {
                 const int n = count8(A.cols, e);
                 float d[8], hx[8], w[8], x[8], dw[8], r[8];
@@ -320,8 +323,9 @@ __global__ __launch_bounds__(LANES > kNormThreads ? LANES : kNormThreads) void k
                 unpack8<T>(load8<T>(A.dh ? A.dh : A.h, row * (A.dh ? A.dh_ld : A.h_ld) + e, A.dh ? n : 0), r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    dw[j] = fmaf(d[j], hx[j] * rstd, dw[j]);
-                    x[j] = rstd * (d[j] * w[j] - hx[j] * c);
+                    const float nj = hx[j] * rstd;
+                    dw[j] = fmaf(d[j], nj, dw[j]);
+                    x[j] = rstd * (d[j] * w[j] - nj * c);
                     if (A.dh) x[j] += r[j];
                 }
                 store8<T>(A.dx, row * A.dx_ld + e, n, pack8<T>(x));

@@ -813,3 +813,29 @@ def test_norm_rows_of_all_sizes(cols, dtype, eps):
     value = (x.double() * rstd.double()[:, None] * w.double()).float()
     assert torch.equal(torch.nan_to_num(y, 0.5), torch.nan_to_num(value.to(t), 0.5))
     same_codes(q, value, "row")
+
+
+@pytest.mark.parametrize("dtype,dtype_dy", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("cols", [7, 500, 1000, 2047, 4096, 8000, 16001, 20000])
+def test_norm_grad_rows_of_all_sizes(cols, dtype, dtype_dy):
+    """Rows whose rstd squared, or whose products with the grad, are out of fp32's range; in the weight's grad rows
+    of all sizes count alike."""
+    t = F.TYPES[dtype]
+    sizes = [1.0, 1e10, 1e19, 1e25, 1e30, 1e37, 1e-10, 1e-19, 1e-22, 1e-30, 1e-37]
+    rows, g = len(sizes), gen(cols)
+    h = torch.rand(rows, cols, generator=g, device="cuda", dtype=torch.float64) + 0.5
+    h = (h * torch.tensor(sizes, device="cuda", dtype=torch.float64)[:, None]).to(t)
+    dy = F.tokens(g, rows, cols, 0.1, "cuda").to(F.TYPES[dtype_dy])
+    dy[5] *= 1e5  # products with h above fp32's range
+    w = torch.rand(cols, generator=g, device="cuda") + 0.5
+    rstd = h.double().square().mean(1).rsqrt().float()
+    dx, dw = torch.empty_like(h), torch.empty(cols, device="cuda")
+    ws = torch.empty(D.dopt_rmsnorm_grad_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    D.dopt_rmsnorm_grad(dy, h, w, rstd, dx, dw, workspace=ws, stream=stream())
+    want, want_w = F.rms_norm_grad(dy, h, None, w, rstd)
+    gg, r = (dy.double() * w.double()).abs(), rstd.double()[:, None]
+    size = r * (gg + (h.double().abs() * r) * (gg * (h.double().abs() * r)).mean(1, keepdim=True))
+    bound = (mean_slack(cols) + 8 * U) * size
+    assert bool(((dx.double() - want).abs() <= bound + F.HALF_STEP[dtype] * (want.abs() + bound) + F.TINY[dtype]).all())
+    size_w = (dy.double() * h.double() * r).abs().sum(0)
+    assert bool(((dw.double() - want_w).abs() <= (rows / 1024 + 70) * U * size_w + U * want_w.abs()).all())
