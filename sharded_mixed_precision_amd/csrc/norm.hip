@@ -120,11 +120,15 @@ __device__ __forceinline__ int count8(int64_t cols, int64_t e) {
     return n <= 0 ? 0 : n >= 8 ? 8 : static_cast<int>(n);
 }
 
+// Workgroups in a row of the grid: a launch has less than 2^32 threads along x, and up to
+// 2^30 rows take 2^36 to 2^38.
+constexpr int64_t kNormGridX = int64_t(1) << 23;
+
 template <int T, int LANES, int NV, bool STREAM>
 __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs A) {
     __shared__ double s_sum[4];
     const int t = threadIdx.x % LANES;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kNormThreads / LANES) + threadIdx.x / LANES;
+    const int64_t row = (blockIdx.y * kNormGridX + blockIdx.x) * (kNormThreads / LANES) + threadIdx.x / LANES;
     if (row >= A.rows) return;  // LANES = 256: all threads; 64: whole waves, which do not synchronise
     double s = 0.0;
     if constexpr (NV != kLoop) {
@@ -175,7 +179,8 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs A) {
 template <int T, bool STREAM>
 static void launch_norm_as(const NormArgs &A, hipStream_t stream) {
     const Shape s = shape_of(A.cols);
-    const unsigned grid = static_cast<unsigned>((int64_t(A.rows) * s.lanes + kNormThreads - 1) / kNormThreads);
+    const int64_t blocks = (int64_t(A.rows) * s.lanes + kNormThreads - 1) / kNormThreads;
+    const dim3 grid(static_cast<unsigned>(std::min(blocks, kNormGridX)), static_cast<unsigned>((blocks + kNormGridX - 1) / kNormGridX));
     if (s.lanes == 64 && s.nv == 1) k_norm<T, 64, 1, STREAM><<<grid, kNormThreads, 0, stream>>>(A);
     else if (s.lanes == 64) k_norm<T, 64, 2, STREAM><<<grid, kNormThreads, 0, stream>>>(A);
     else if (s.nv == 1) k_norm<T, 256, 1, STREAM><<<grid, kNormThreads, 0, stream>>>(A);

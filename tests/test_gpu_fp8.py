@@ -839,3 +839,18 @@ def test_norm_grad_rows_of_all_sizes(cols, dtype, dtype_dy):
     assert bool(((dx.double() - want).abs() <= bound + F.HALF_STEP[dtype] * (want.abs() + bound) + F.TINY[dtype]).all())
     size_w = (dy.double() * h.double() * r).abs().sum(0)
     assert bool(((dw.double() - want_w).abs() <= (rows / 1024 + 70) * U * size_w + U * want_w.abs()).all())
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 26) + 5, 8), ((1 << 24) + 3, 1025)])
+def test_norm_many_rows(rows, cols):
+    """More rows than one launch has threads for along a dimension."""
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(1))
+    w = torch.rand(cols, generator=gen(2), device="cuda") + 0.5
+    y, rstd = torch.zeros_like(x), torch.zeros(rows, device="cuda")
+    D.dopt_rmsnorm(x, w, 1e-5, y=y, rstd=rstd, stream=stream())
+    assert bool((rstd > 0).all())
+    edge = 1 << (26 if cols == 8 else 24)
+    at = torch.cat([torch.arange(0, rows, rows // 5000, device="cuda"), torch.arange(edge - 9, rows, device="cuda"), torch.arange(edge // 2 - 9, edge // 2 + 9, device="cuda")])
+    _, want, _ = F.rms_norm(x[at], None, w, 1e-5, torch.bfloat16)
+    assert bool(((rstd[at].double() - want).abs() <= norm_slack(cols) * want).all())
+    assert torch.equal(y[at], (x[at].double() * rstd[at].double()[:, None] * w.double()).float().bfloat16())
