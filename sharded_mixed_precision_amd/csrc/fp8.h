@@ -40,6 +40,9 @@ Span scales_span(const char *name, const dopt_fp8_matrix *x);
 int check_apart(const Span *out, int n_out, const Span *in, int n_in);
 int launched(const char *what);
 
+// A launch has less than this many threads along a dimension of its grid.
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
+
 // ---- device: elements -------------------------------------------------------------
 
 using i32x4 = __attribute__((ext_vector_type(4))) int;

@@ -323,7 +323,7 @@ extern "C" int dopt_fp8_cast(const dopt_dense *x, const float *row_factor, const
     }
     A.col_tiles = static_cast<int32_t>((x->cols + DOPT_FP8_BLOCK - 1) / DOPT_FP8_BLOCK);
     const int64_t tiles = (x->rows + DOPT_FP8_BLOCK - 1) / DOPT_FP8_BLOCK * A.col_tiles;
-    if (tiles > INT32_MAX) return fail(DOPT_ERR_INVALID, "x: too large");
+    if (tiles * kCastThreads >= kMaxThreads) return fail(DOPT_ERR_INVALID, "x: too large");
     const bool tile = (codes ? codes : transposed)->kind == DOPT_FP8_TILE;
     const unsigned grid = static_cast<unsigned>(tiles);
     if (x->dtype == DOPT_F32) launch_cast<DOPT_F32>(A, tile, grid, stream);

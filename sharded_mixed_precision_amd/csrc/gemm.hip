@@ -835,19 +835,23 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k) {
 
 static int64_t part_ld_of(int64_t n) { return (n + 3) / 4 * 4; }
 
+// Threads of a workgroup.
+static unsigned threads_of(const Plan &p, bool exact) { return p.few ? 64 * p.waves : p.rows == kBig && exact ? 512 : 256; }
+
 template <bool BROW, bool EXACT>
 static void launch_gemm(const GemmArgs &A, const Plan &p, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(A.tiles_m * A.tiles_n), static_cast<unsigned>(A.splits));
+    const unsigned threads = threads_of(p, EXACT);
     if (p.few) {
-        if (p.waves == 2) k_gemm_few<2, BROW><<<grid, 128, 0, stream>>>(A);
-        else if (p.waves == 4) k_gemm_few<4, BROW><<<grid, 256, 0, stream>>>(A);
-        else k_gemm_few<8, BROW><<<grid, 512, 0, stream>>>(A);
+        if (p.waves == 2) k_gemm_few<2, BROW><<<grid, threads, 0, stream>>>(A);
+        else if (p.waves == 4) k_gemm_few<4, BROW><<<grid, threads, 0, stream>>>(A);
+        else k_gemm_few<8, BROW><<<grid, threads, 0, stream>>>(A);
     } else if (p.rows == kBig) {
-        if constexpr (EXACT) k_gemm_wide<BROW><<<grid, 512, 0, stream>>>(A);
-        else k_gemm_big<BROW><<<grid, 256, 0, stream>>>(A);
+        if constexpr (EXACT) k_gemm_wide<BROW><<<grid, threads, 0, stream>>>(A);
+        else k_gemm_big<BROW><<<grid, threads, 0, stream>>>(A);
     } else {
-        if (p.stages == 2) k_gemm_tile<2, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
-        else k_gemm_tile<3, BROW, EXACT><<<grid, 256, 0, stream>>>(A);
+        if (p.stages == 2) k_gemm_tile<2, BROW, EXACT><<<grid, threads, 0, stream>>>(A);
+        else k_gemm_tile<3, BROW, EXACT><<<grid, threads, 0, stream>>>(A);
     }
 }
 
@@ -887,7 +891,7 @@ static int gemm(bool exact, const dopt_fp8_matrix *a, const dopt_fp8_matrix *b, 
 
     const Plan p = plan_of(m, n, k);
     const int64_t tiles_m = ceil_div(m, p.rows), tiles_n = ceil_div(n, p.cols);
-    if (tiles_m * tiles_n > INT32_MAX) return fail(DOPT_ERR_INVALID, "too large");
+    if (tiles_m * tiles_n * threads_of(p, exact) >= kMaxThreads) return fail(DOPT_ERR_INVALID, "out: too large");
     GemmArgs A{};
     A.a = static_cast<const uint8_t *>(a->codes);
     A.b = static_cast<const uint8_t *>(b->codes);

@@ -222,3 +222,13 @@ def test_gemm_coarse_refusals():
     big = fp8(100, 1 << 20), fp8(50, 1 << 20, at=AT + (1 << 37))
     refused(call(*big, o, 0, None, 0, None), "workspace")
     assert call(fp8(0, 300, codes=None, scales=None), b, dense(0, 50, at=None), 0, None, 0, None) == 0
+
+
+def test_grids_past_the_limit_of_a_launch():
+    """Sizes whose tiles take 2^32 threads or more along one dimension are refused before any launch."""
+    L, m = D.lib(), 1 << 30
+    refused(L.dopt_fp8_cast(dense(m, 256), None, None, 0, fp8(m, 256, at=AT + (1 << 41), scales=AT + (1 << 43)), None, None), "too large")  # 2^24 tiles
+    a, b = fp8(m, 128, at=AT + (1 << 42), scales=AT + (1 << 43)), fp8(257, 128, at=AT + (1 << 44))
+    assert D.dopt_fp8_gemm_workspace_bytes(m, 257, 128) == 0
+    refused(L.dopt_fp8_gemm(a, b, dense(m, 257), 0, None, 0, None), "too large")  # 2^22 x 2 tiles of 512 threads, or 2^23 x 3 of 256
+    refused(L.dopt_fp8_gemm_coarse(a, fp8(1025, 128, at=AT + (1 << 44)), dense(m, 1025), 0, None, 0, None), "too large")
