@@ -103,7 +103,7 @@ int dopt_fp8_cast(const dopt_dense *x, const float *row_factor, const void *col_
  * dopt_fp8_gemm -- out[m][n] = sum over k of a[m][k] * b[n][k], plus
  * out[m][n] if `accumulate`.  a (kind ROW) is M x K, b (either kind) N x K, out
  * M x N; products and sums in fp32, one rounding to out's type.  Scales may be bytes 1 to
- * 254; there elements below 2^-126 may count as 0.  The workspace holds
+ * 254; elements below 2^-126 may count as 0, those of 2^128 and more as infinite.  The workspace holds
  * dopt_fp8_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned; where that is
  * 0 it may be NULL.
  *

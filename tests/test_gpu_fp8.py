@@ -854,3 +854,36 @@ def test_norm_many_rows(rows, cols):
     _, want, _ = F.rms_norm(x[at], None, w, 1e-5, torch.bfloat16)
     assert bool(((rstd[at].double() - want).abs() <= norm_slack(cols) * want).all())
     assert torch.equal(y[at], (x[at].double() * rstd[at].double()[:, None] * w.double()).float().bfloat16())
+
+
+@pytest.mark.parametrize("call", ["dopt_fp8_gemm", "dopt_fp8_gemm_coarse"])
+@pytest.mark.parametrize("kind", ["row", "tile"])
+@pytest.mark.parametrize("m,n", [(16, 400), (200, 300), (1300, 2500), (3300, 4000)])
+def test_gemm_scales_of_all_sizes_in_every_kernel(m, n, kind, call):
+    """Scale bytes 1 to 254 on either side, one element to a row: a product of numbers in fp32's normal range is exact, or out of
+    range as in fp32 (below its normal numbers it may be cut)."""
+    g = gen(m)
+    a, b = fp8_alloc(m, 256), fp8_alloc(n, 256, kind)
+    some = torch.tensor([1.0, -1.75, 448.0, 2.0 ** -6, 2.0 ** -9, 0.0], device="cuda")
+    for q, rows in ((a, m), (b, n)):
+        q.codes.view(torch.uint8).zero_()
+        q.codes.view(torch.uint8)[:, 200] = some[torch.randint(0, 6, (rows,), generator=g, device="cuda")].to(torch.float8_e4m3fn).view(torch.uint8)
+        s = q.scales.view(torch.uint8)
+        s.copy_(torch.randint(1, 255, s.shape, generator=g, device="cuda"))
+        s[1, :8] = torch.tensor([1, 254, 247, 248, 127, 2, 253, 64], device="cuda")[:s.shape[1]]
+    x, y = F.values(a), F.values(b)
+    want = x @ y.t()  # one product each
+    least, most = 2.0 ** -126, 2.0 ** 128
+
+    def ordinary(v):
+        v = v[:, 200].abs()
+        return (v == 0) | ((v >= least) & (v < most))
+
+    ok = ordinary(x)[:, None] & ordinary(y)[None, :]
+    for t in (("f32", "bf16", "f16") if call == "dopt_fp8_gemm" else ("bf16", "f16")):
+        out = torch.full((m, n), 7.0, dtype=F.TYPES[t], device="cuda")
+        getattr(D, call)(a, b, out, False, torch.empty(max(1, D.dopt_fp8_gemm_workspace_bytes(m, n, 256)), dtype=torch.uint8, device="cuda"), stream())
+        as_t = want.float().to(out.dtype)
+        normal = (want.abs() >= least) | (want == 0)
+        assert torch.equal(out[ok & normal], as_t[ok & normal])
+        assert bool(((out.double() - want)[ok & ~normal].abs() <= least + F.TINY[t]).all())
