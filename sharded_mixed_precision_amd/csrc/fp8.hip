@@ -72,7 +72,7 @@ Span scales_span(const char *name, const dopt_fp8_matrix *x) {
 
 int check_apart(const Span *out, int n_out, const Span *in, int n_in) {
     const auto meet = [](const Span &a, const Span &b) {
-        if (a.lo >= b.hi || b.lo >= a.hi) return false;
+        if (a.lo == a.hi || b.lo == b.hi || a.lo >= b.hi || b.lo >= a.hi) return false;
         if (a.pitch == 0 || a.pitch != b.pitch) return true;
         const uint64_t pitch = static_cast<uint64_t>(a.pitch);
         const uint64_t at = b.lo >= a.lo ? (b.lo - a.lo) % pitch : (pitch - (a.lo - b.lo) % pitch) % pitch;

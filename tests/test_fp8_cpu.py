@@ -232,3 +232,12 @@ def test_grids_past_the_limit_of_a_launch():
     assert D.dopt_fp8_gemm_workspace_bytes(m, 257, 128) == 0
     refused(L.dopt_fp8_gemm(a, b, dense(m, 257), 0, None, 0, None), "too large")  # 2^22 x 2 tiles of 512 threads, or 2^23 x 3 of 256
     refused(L.dopt_fp8_gemm_coarse(a, fp8(1025, 128, at=AT + (1 << 44)), dense(m, 1025), 0, None, 0, None), "too large")
+
+
+def test_nothing_overlaps_nothing():
+    """A workspace of which no byte is needed may lie anywhere: the call gets past the check to the next refusal."""
+    m = 1 << 30
+    a, b = fp8(m, 128, at=AT + (1 << 42), scales=AT + (1 << 43)), fp8(257, 128, at=AT + (1 << 44))
+    assert D.dopt_fp8_gemm_workspace_bytes(m, 257, 128) == 0
+    for ws in (AT + (1 << 30), AT + (1 << 42) + (1 << 30)):
+        refused(D.lib().dopt_fp8_gemm(a, b, dense(m, 257), 0, ws, 1 << 20, None), "out: too large")
