@@ -727,10 +727,11 @@ __global__ __launch_bounds__(512, 2) void k_gemm_wide(GemmArgs A) {
 // Up to 16 rows of a: b is read once, and what bounds the call is how fast.  A
 // workgroup takes 16 columns of the output, its waves share the steps along k, and
 // their sums are joined through shared memory.  A wave has the operands of
-// kFewDepth steps under way before it multiplies the first.  It adds in fp32 whoever calls: with
-// the codes' own instruction 1 x 14336 x 4096 took 13.8 us for 14.6, 1 x 4096 x 14336 15.2 for 15.4.  1 x 14336 x 4096: 12.5 us, 15.7 without
-// that; 27 with 8 steps, whose waves are too few; 15.3 with b read around the caches.  17 to 64 rows so, with
-// a read anew by every workgroup, took 28 us (32 rows) and 43 (64) where k_gemm_tile takes 17.
+// kFewDepth steps under way before it multiplies the first.  It adds in fp32 whoever calls: 1 x 14336 x 4096
+// takes 14.5 us so and 13.8 with the codes' own instruction, 1 x 4096 x 14336 15.4 and 15.2.  With that instruction
+// 1 x 14336 x 4096 took 3 us more without steps under way, 14 more with 8 of them, whose waves are too few, and 3 more with b read
+// around the caches; 17 to 64 rows so, with a read anew by every workgroup, 28 us (32 rows) and 43 (64) where
+// k_gemm_tile takes 17.
 constexpr int kFewDepth = 4;
 
 template <int WAVES, bool BROW>
@@ -801,10 +802,10 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k) {
     p.stages = 2;
     int64_t splits = 1;
     if (p.few) {
-        // One batch of kFewDepth steps to a wave, up to 8 waves: 4096 columns, 8 steps: 3.8 us with 2
-        // waves, 4.5 with 4, 6.1 with 8; 6000 columns, 16 steps: 6.6, 6.3, 8.9; 11008 columns, 32 steps: 12.4, 13.0, 12.2;
-        // 8192 columns, 32 steps: 10.9, 10.6, 9.8.  More steps than that are shared by several workgroups where
-        // the columns are few: 768 columns, 128 steps: 13.1 us, split in 4 8.7, in 8 12.3; 2048 columns, 64 steps: 9.2, in 2 9.3.
+        // One batch of kFewDepth steps to a wave, up to 8 waves: 4096 columns, 8 steps: 4.4 us with 2
+        // waves, 4.6 with 4, 5.7 with 8; 6000 columns, 16 steps: 6.8, 6.4, 8.5; 11008 columns, 32 steps: 12.6, 13.2, 11.7;
+        // 8192 columns, 32 steps: 11.0, 10.8, 9.5.  More steps than that are shared by several workgroups where
+        // the columns are few: 768 columns, 128 steps: 13.0 us, split in 4 9.5, in 8 12.1; 2048 columns, 64 steps: 8.6, in 2 9.3.
         p.rows = p.cols = 16;
         p.waves = steps <= 12 ? 2 : steps <= 24 ? 4 : 8;
         if (ceil_div(n, p.cols) <= 64) splits = steps / (8 * kFewDepth);
@@ -813,16 +814,18 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k) {
         if (small <= kCus) {
             // A tile or less to a CU: what counts is how soon a step's loads are back, so three steps are under way,
             // and with 8 steps or more to each the steps are shared by several workgroups.
-            // 128 x 4096 x 4096, coarse sums: 24.8 us with 2 stages, 16.8 with 3 or 4; split in 2, 4, 8: 16.0,
-            // 16.2, 19.3.  1024 x 4096 x 4096: 26.7, 19.4.  768 x 768 x 8192, fp32 out: 52.7 us, split in 4 23.6, in 8 29.5.
+            // 1024 x 4096 x 4096: 42 us with 2 stages, 33 with 3 (coarse 26.6, 21.7).  128 x 4096 x 4096: 40 with 2 stages, 29.7
+            // with 3; split in 2, 4, 8: 22.4, 19.2, 20.8 (coarse 24.6, 16.4; 15.7, 15.7, 18.8).  768 x 768 x 8192 added to fp32, split in 1, 2, 4,
+            // 7, 8 (the rule's 7): 53, 33.6, 23.4, 21.7, 28.4; 768 x 2304 x 8192 unsplit, in 2, 3, 4, 7 (the rule's 2): 53.5, 39.1, 47.4, 43.6, 54.1.
             p.rows = p.cols = kSmall;
             p.stages = 3;
             splits = std::min(kCus / small, steps / 8);
         } else {
-            // A round of big tiles takes about 7 us and 1.25 for each step, one of twice as many small ones
-            // 2.5 and 0.92 (measured at 256 to 1024 small tiles and 8 to 32 steps; fp32 outputs in the same proportion).
-            // Small and big, us, with coarse sums: 2048 x 4096 x 4096 34, 46; 4096 x 4096 x 4096 64, 53; 3073 x 4096 x 4096 56, 47;
-            // 8192 x 2304 x 768 24, 29; 4096 x 14336 x 128 33, 38; fp32 out 67, 78; 123, 96; 108, 85; 36, 44; 53, 59.
+            // With coarse sums a round of big tiles takes about 7 us and 1.25 for each step, one of twice as many small
+            // ones 2.5 and 0.92 (measured at 256 to 1024 small tiles and 8 to 32 steps); sums in fp32 take longer in about the same proportion.
+            // Small and big, us: 2048 x 4096 x 4096 60, 81; 3073 x 4096 x 4096 101, 83; 4096 x 4096 x 4096 114, 95;
+            // 8192 x 2304 x 768 34, 41; 4096 x 14336 x 128 36, 38; coarse 34, 48; 57, 48; 62, 56; 25, 32; 32, 41; fp32 out 59, 80; 105, 85; 116, 102;
+            // 37, 45; 54, 61.
             const int64_t as_big = ceil_div(big, kCus) * (28 + 5 * steps), as_small = ceil_div(small, 2 * kCus) * (100 + 37 * steps);
             p.rows = p.cols = as_big * 10 <= as_small ? kBig : kSmall;
         }
