@@ -887,3 +887,35 @@ def test_gemm_scales_of_all_sizes_in_every_kernel(m, n, kind, call):
         normal = (want.abs() >= least) | (want == 0)
         assert torch.equal(out[ok & normal], as_t[ok & normal])
         assert bool(((out.double() - want)[ok & ~normal].abs() <= least + F.TINY[t]).all())
+
+
+@pytest.mark.parametrize("call", ["dopt_fp8_gemm", "dopt_fp8_gemm_coarse"])
+@pytest.mark.parametrize("m,n,k", [(5, 333, 300), (301, 335, 1100), (1301, 2503, 640), (4101, 3001, 1100)])
+def test_gemm_16_bit_outputs_at_odd_widths_and_strides(m, n, k, call):
+    """The output is part of a larger matrix of odd width, from an odd element on; stored and added to, captured and replayed."""
+    g = gen(m + n)
+    a, b = whole_numbers(g, m, k, "row", 1), whole_numbers(g, n, k, "tile", 1)
+    want = (F.values(a) @ F.values(b).t()).float()
+    ws = torch.empty(max(1, D.dopt_fp8_gemm_workspace_bytes(m, n, k)), dtype=torch.uint8, device="cuda")
+    go = getattr(D, call)
+    for t in (torch.bfloat16, torch.float16):
+        whole = torch.full((m + 2, n + 8 - n % 2), math.nan, dtype=t, device="cuda")
+        out = whole[1:m + 1, 3:n + 3]
+        go(a, b, out, False, ws, stream())
+        assert torch.equal(out, want.to(t))
+        go(a, b, out, True, ws, stream())
+        twice = (want.to(t).float() + want).to(t)
+        assert torch.equal(out, twice)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            go(a, b, out, False, ws, torch.cuda.current_stream())
+            go(a, b, out, True, ws, torch.cuda.current_stream())
+        for _ in range(3):
+            out.fill_(3.0)
+            ws.fill_(0xff)
+            graph.replay()
+            assert torch.equal(out, twice)
+            torch.cuda.synchronize()
+        out.fill_(math.nan)
+        assert torch.isnan(whole).all()
