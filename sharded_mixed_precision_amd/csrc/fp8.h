@@ -94,10 +94,12 @@ __device__ __forceinline__ uint32_t from_float(float x) {
 // As Bytes16 for accesses that pass the caches by: a vector type of that alignment.
 using u32x4_any = __attribute__((ext_vector_type(4), aligned(2))) uint32_t;
 
-// A matrix of more bytes than the 8 L2 caches hold (4 MB each) is read around them where it is
-// read once: its lines are gone before anyone could ask again, and what the call
-// writes for the next one stays longer.
+// A matrix of 16-bit elements of more bytes than the 8 L2 caches hold (4 MB each) is read around them where it
+// is read once: its lines are gone before anyone could ask again, and what the call
+// writes for the next one stays longer.  Of fp32 elements a lane reads 32 bytes in two loads, and around the caches a line
+// may be fetched for each: there only the cast does so, from 96 MB on.
 constexpr int64_t kStreamBytes = int64_t(32) << 20;
+constexpr int64_t kStreamBytesF32 = int64_t(96) << 20;
 
 // Elements [0, n) of the 8 at p, n <= 8, the others zero.
 template <int T, bool STREAM = false>

@@ -122,7 +122,9 @@ struct CastMem {
 // around them: they are asked for when the other layers' weights have been cast, while a grad's or an
 // activation's (ROW) are the next product's operands.  8192 x 4096 bf16, both ways, ROW: 30.8 us
 // with ordinary reads, 28.6 around the caches, 24.8 with the codes too, but then the product of
-// 4096 x 14336 behind it takes 10 us longer; 1024 x 4096: 8.2 and 8.5.  14336 x 4096, TILE: 47.8 and 43.6.
+// 4096 x 14336 behind it takes 10 us longer; 1024 x 4096: 8.2 and 8.5.  14336 x 4096, TILE: 47.8 and 43.6.  fp32, codes only, ROW
+// and TILE: 4096 x 4096 15.0 and 14.9 us with ordinary reads, 19.6 and 17.7 around; 6000 x 4096 26.5 and 26.4, 26.6 and 25.2; 14336 x 4096
+// 56.1 and 56.2, 55.3 and 52.8.
 template <int T, bool TILE, bool WHOLE, bool STREAM>
 __device__ __forceinline__ void cast_tile(const CastArgs &A, CastMem &mem, int row0, int col0) {
     auto &s_top = mem.top;
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(kCastThreads) void k_cast(CastArgs A) {
 
 template <int T>
 static void launch_cast(const CastArgs &A, bool tile, unsigned grid, hipStream_t stream) {
-    const bool around = int64_t(A.rows) * A.cols * (T == DOPT_F32 ? 4 : 2) > kStreamBytes;
+    const bool around = T == DOPT_F32 ? int64_t(A.rows) * A.cols * 4 > kStreamBytesF32 : int64_t(A.rows) * A.cols * 2 > kStreamBytes;
     if (tile && around) k_cast<T, true, true><<<grid, kCastThreads, 0, stream>>>(A);
     else if (tile) k_cast<T, true, false><<<grid, kCastThreads, 0, stream>>>(A);
     else if (around) k_cast<T, false, true><<<grid, kCastThreads, 0, stream>>>(A);

@@ -919,3 +919,13 @@ def test_gemm_16_bit_outputs_at_odd_widths_and_strides(m, n, k, call):
             torch.cuda.synchronize()
         out.fill_(math.nan)
         assert torch.isnan(whole).all()
+
+
+@pytest.mark.parametrize("kind", ["row", "tile"])
+def test_cast_large_fp32(kind):
+    """More than 96 MB of fp32, which are read around the caches."""
+    x = F.tokens(gen(8), 6200, 4099, 0.3, "cuda")
+    both = poisoned(6200, 4099, kind), poisoned(4099, 6200, kind)
+    D.dopt_fp8_cast(x, *both, stream=stream())
+    same_codes(both[0], x, kind)
+    same_codes(both[1], x.t(), kind)
