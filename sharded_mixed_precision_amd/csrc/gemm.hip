@@ -3,15 +3,17 @@
 //
 // Four kernels, by plan_of: up to 16 rows of a (k_gemm_few), bound by the one reading of b; 128 x 128
 // tiles (k_gemm_tile), bound by latency where tiles are few; 256 x 256 tiles (k_gemm_wide for sums in
-// fp32, k_gemm_big for coarse ones).  Median times on MI355X, where a copy reaches 5.1 TB/s, in brackets those of
-// dopt_fp8_gemm_coarse:
-//   1 x 14336 x 4096        14.6 us, 4.0 TB/s              k_gemm_few
-//   1024 x 2304 x 768       10.1 us (7.6)                  k_gemm_tile, 3 stages
-//   1024 x 4096 x 4096      35 us (20.5)                   k_gemm_tile, 3 stages
-//   8192 x 14336 x 4096     640 us, 1.50 PFLOP/s (374, 2.57)   k_gemm_wide (k_gemm_big)
-//   8192 x 4096 x 14336     614 us, 1.57 PFLOP/s (347, 2.77)   k_gemm_wide (k_gemm_big)
-//   777 x 50257 x 768, fp32 out    93 us                   k_gemm_tile, 2 stages: 40 us of them are the stores
-//   4096 x 4096 x 8192, fp32 +=   202 us, 1.36 PFLOP/s     k_gemm_wide
+// fp32, k_gemm_big for coarse ones), bound by the matrix cores, whose clock falls from 2.4 to 2.05 GHz, and by a tile's first
+// loads and its stores, during which they wait.  Time per call of calls in a row on MI355X, where a library's bf16 product of
+// these large sizes reaches 1.33 to 1.56 PFLOP/s, an e4m3 one without scales of blocks 2.5 to 3.1, and a copy 5.1 TB/s; ranges are over
+// machines; in brackets dopt_fp8_gemm_coarse:
+//   1 x 14336 x 4096              13.1 us, 4.5 TB/s                                   k_gemm_few
+//   1024 x 2304 x 768             8.7 us (7.7)                                        k_gemm_tile, 3 stages
+//   1024 x 4096 x 4096            32 to 36 us (20 to 22)                              k_gemm_tile, 3 stages
+//   8192 x 14336 x 4096           649 to 687 us, 1.40 to 1.48 PFLOP/s (374 to 395)    k_gemm_wide (k_gemm_big)
+//   8192 x 4096 x 14336           612 to 656 us, 1.47 to 1.57 PFLOP/s (347 to 361)    k_gemm_wide (k_gemm_big)
+//   777 x 50257 x 768, fp32 out   94 to 95 us                                         k_gemm_tile, 2 stages: 40 us of them are the stores
+//   4096 x 4096 x 8192, fp32 +=   201 to 213 us, 1.29 to 1.37 PFLOP/s                 k_gemm_wide
 #include <algorithm>
 #include <string>
 #include <type_traits>
@@ -510,7 +512,7 @@ constexpr int kBigOperand = StepMem<kBig>::kB, kBigBuffer = StepMem<kBig>::kByte
 //   phase 1 multiplies the other rows, starts the loads of the step after the next into the
 //           free buffer, and reads the next step's first 64 rows of a and all of b, each
 //           register once its last product is under way.
-// 8192 x 14336 x 4096: 366 to 388 us; the matrix cores are busy 60% of the cycles.  With 8 waves of 128 x 64 and
+// 8192 x 14336 x 4096: 374 to 395 us; the matrix cores are busy 60% of the cycles.  With 8 waves of 128 x 64 and
 // the same order of work 397 to 415 us (more reads of shared memory, and both waves of a SIMD
 // wait at the same time), with reads and products of a step between two barriers 408; by instructions of 32 x 32 390 to
 // 401; with all 16 loads at the start of phase 1 401 to 412, since they fill the path to the

@@ -1,8 +1,8 @@
 // The RMS norm with an 8-bit output (dopt_rmsnorm) and its backward pass (dopt_rmsnorm_grad).
 // Both read a row once and keep it in registers across its sum, and both are
-// bound by memory.  On MI355X (a copy reaches 5.1 TB/s): 8192 x 8192 bf16 with a residual 88 to 95 us (5.0 to 5.4 TB/s);
-// backward of 8192 x 4096 bf16 with a residual's grad 51 us (5.2 TB/s) and 5 for the weight's; one row of 4096
-// 4 us, 1023 x 768 backward 5 and 3 us, both less than the call's host time.
+// bound by memory.  On MI355X (a copy reaches 5.1 TB/s): 8192 x 8192 bf16 with a residual 90.3 us a call (5.2 TB/s);
+// backward of 8192 x 4096 bf16 with a residual's grad 56.5, 52 of them its own kernel (5.2 TB/s) and 5 for the weight's grad; one row of 4096
+// 4 us on the GPU, 1023 x 768 backward 5 and 3, both less than the call's host time.
 #include <algorithm>
 #include <string>
 
