@@ -47,7 +47,7 @@ def build(verbose: bool = False) -> str:
     tmp = SO + ".tmp"
     with tempfile.TemporaryDirectory() as d:
         objects = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
-        with ThreadPoolExecutor(int(os.environ.get("MAX_JOBS", os.cpu_count() or 1))) as pool:
+        with ThreadPoolExecutor(int(os.environ.get("MAX_JOBS") or os.cpu_count() or 1)) as pool:
             list(pool.map(lambda so: _run([HIPCC, *FLAGS, "-c", so[0], "-o", so[1]], verbose), zip(SOURCES, objects)))
         _run([HIPCC, FLAGS[0], "-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, SO)
